@@ -376,6 +376,106 @@ moe_status moe_layer_noalloc(const moe_pool* pool, const int32_t* slot_map,
                              int32_t T, int32_t E, int32_t k, float* out, uint32_t* err_flags,
                              int32_t path, void* stream);
 
+/*
+ * Microscaled rows: the activations' counterpart of the pool's MXFP4. Each 32 consecutive
+ * values of a row share a scale byte s, meaning 2^(s - 127); a value is code * 2^(s - 127).
+ *   MOE_MX_FP4: 4-bit E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), 16 bytes a
+ *               block, element 2j in the low nibble of byte j: moe_pool_pack's canonical
+ *               MXFP4 planes.
+ *   MOE_MX_FP6: 6-bit E2M3 codes (0 to 7.5: steps of 1/8 below 2, of 1/4 below 4, of 1/2),
+ *               24 bytes a block, element i in bits 6i .. 6i + 5 (little-endian). The matrix
+ *               instructions take both at the same rate.
+ * Planes: codes [rows][moe_mx_row_bytes(fmt, K)], scales u8 [rows][K/32]. K is a multiple of
+ * 32. A code plane is 16-byte aligned; a scale plane needs no alignment.
+ */
+typedef enum { MOE_MX_FP4 = 1, MOE_MX_FP6 = 2 } moe_mxfmt;
+
+/* Element types of the calls below that take several. */
+typedef enum { MOE_T_BF16 = 1, MOE_T_FP16 = 2, MOE_T_FP32 = 3 } moe_dtype;
+
+/* Bytes of one row of K codes; 0 for an unknown format or K not a multiple of 32. */
+size_t moe_mx_row_bytes(int32_t fmt, int32_t K);
+
+/*
+ * moe_mx_quantize -- rows of bf16, fp16 or fp32 values to microscaled codes and scales.
+ *   src [rows][K] of src_type (moe_dtype); q, s (out) as above; rows*K < 2^40
+ *   Per block, with a the largest magnitude: s = max(1, floor(log2 a) + 125) (1 for a block of
+ *   zeros), and each code is the format's value nearest to v * 2^(127 - s), halves to the even
+ *   code, saturated at the format's largest magnitude (6 or 7.5). A block that holds an
+ *   infinity or NaN gets s = 255 and zero codes, and stands for 32 NaNs: the products below
+ *   give NaN for what reads it. Weights with such a block do not belong in a pool.
+ *   A loader quantises an expert's matrices to MOE_MX_FP4 and hands the planes to
+ *   moe_pool_pack.
+ *
+ * moe_mx_dequantize -- the values that codes and scales stand for: dst [rows][K] of dst_type,
+ *   code * 2^(s - 127) rounded to nearest even where it does not fit dst_type exactly (bf16
+ *   and fp16 hold every code's digits, not every scale's range); NaN where s = 255.
+ */
+moe_status moe_mx_quantize(const void* src, int32_t src_type, int32_t rows, int32_t K,
+                           int32_t fmt, void* q, uint8_t* s, void* stream);
+moe_status moe_mx_dequantize(const void* q, const uint8_t* s, int32_t fmt, int32_t rows,
+                             int32_t K, void* dst, int32_t dst_type, void* stream);
+
+/*
+ * moe_mx_expert_gate_up, moe_mx_expert_down -- the halves of the expert FFN on microscaled
+ * rows: as moe_expert_gate_up and moe_expert_down, with the row operand in codes and scales
+ * and the products on the scaled matrix instructions (fp32 accumulation).
+ *   pool     MXFP4 (other formats: MOE_ERR_UNSUPPORTED)
+ *   x_q, x_s planes of T rows of H values, in x_fmt (moe_mxfmt); row perm[pos] / k is read for
+ *            bucket position pos
+ *   h_q, h_s planes of T*k rows of I values in bucket order, in h_fmt
+ *   h        bf16 [T*k][I] (out) = bf16_RNE(silu(g) * u);  y fp32 [T*k][H] (out)
+ *   offsets, perm as from moe_bucket; slot_map, err_flags and path as in moe_expert_ffn. Rows
+ *   past offsets[E] are left as they are.
+ *
+ * moe_mx_expert_ffn -- gate_up, then h quantised to h_q, h_s in h_fmt, then down.
+ */
+moe_status moe_mx_expert_gate_up(const moe_pool* pool, const int32_t* slot_map, int32_t E,
+                                 const void* x_q, const uint8_t* x_s, int32_t x_fmt, int32_t T,
+                                 int32_t k, const int32_t* offsets, const int32_t* perm,
+                                 uint16_t* h, uint32_t* err_flags, int32_t path, void* stream);
+moe_status moe_mx_expert_down(const moe_pool* pool, const int32_t* slot_map, int32_t E,
+                              const void* h_q, const uint8_t* h_s, int32_t h_fmt, int32_t T,
+                              int32_t k, const int32_t* offsets, float* y, uint32_t* err_flags,
+                              int32_t path, void* stream);
+moe_status moe_mx_expert_ffn(const moe_pool* pool, const int32_t* slot_map, int32_t E,
+                             const void* x_q, const uint8_t* x_s, int32_t x_fmt, int32_t T,
+                             int32_t k, const int32_t* offsets, const int32_t* perm, uint16_t* h,
+                             void* h_q, uint8_t* h_s, int32_t h_fmt, float* y,
+                             uint32_t* err_flags, int32_t path, void* stream);
+
+/*
+ * The norms before and after the layer, on the residual stream resid [T][H] of resid_type
+ * (MOE_T_BF16 or MOE_T_FP32). All arithmetic is fp32; each output is rounded once.
+ *
+ * moe_add_norm -- the layer's entry:
+ *   s = resid + scale * delta          (delta [T][H] of delta_type, bf16 or fp32; NULL: s = resid)
+ *   resid_out = s                      (resid_type; may be resid itself; NULL only without delta)
+ *   x = bf16(s / sqrt(mean_h(s^2) + eps) * weight)   (weight [H] of weight_type, bf16 or fp32)
+ *   x is computed from s before s is rounded to resid_type.
+ *
+ * moe_combine_norm -- the layer's exit, in place of moe_combine:
+ *   c = sum_{j<k} topk_w[t,j] * y[inv_perm[t*k+j], :]      (increasing j; an inv_perm entry
+ *                                                outside [0, T*k) adds nothing)
+ *   n = c, or c / sqrt(mean_h(c^2) + eps) * post_weight    (post_weight [H], or NULL)
+ *   s = resid + scale * gate * n       (gate [gate_rows][H], gate_rows 1 or T; NULL: no gate)
+ *   resid_out = s                      (resid_type; may be resid itself)
+ *   x = bf16(s / sqrt(mean_h(s^2) + eps) * next_weight)    (the next layer's entry norm;
+ *                                                next_weight and x NULL together to skip it)
+ *   post_weight, gate and next_weight are all of weight_type (bf16 or fp32).
+ * Outputs must not overlap inputs, except resid_out as said.
+ */
+moe_status moe_add_norm(const void* resid, int32_t resid_type, const void* delta,
+                        int32_t delta_type, float scale, const void* weight, int32_t weight_type,
+                        float eps, int32_t T, int32_t H, void* resid_out, uint16_t* x,
+                        void* stream);
+moe_status moe_combine_norm(const float* y, const int32_t* inv_perm, const float* topk_w,
+                            int32_t T, int32_t k, int32_t H, const void* resid,
+                            int32_t resid_type, const void* post_weight, const void* gate,
+                            int32_t gate_rows, float scale, const void* next_weight,
+                            int32_t weight_type, float eps, void* resid_out, uint16_t* x,
+                            void* stream);
+
 const char* moe_status_string(moe_status s);
 const char* moe_last_error(void);
 

@@ -22,6 +22,9 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 MXFP4, Q8_0, Q4_K, Q5_K, Q6_K = 1, 2, 3, 4, 5
 PATH_AUTO, PATH_GEMV, PATH_GROUPED, PATH_PERSISTENT = 0, 1, 2, 3
 SLOT_MISS = -1      # slot_map value of an expert that is not in the pool (MOE_SLOT_MISS)
+MX_FP4, MX_FP6 = 1, 2
+_MX = {"mxfp4": MX_FP4, "mxfp6": MX_FP6}                       # moe_mxfmt
+_DT = {torch.bfloat16: 1, torch.float16: 2, torch.float32: 3}   # moe_dtype
 _FMT = {"mxfp4": MXFP4, "q8_0": Q8_0, "q4_k": Q4_K, "q5_k": Q5_K, "q6_k": Q6_K}
 
 
@@ -85,6 +88,20 @@ _layer_timed = _sig("moe_layer_timed", _i32, ctypes.POINTER(PoolStruct), _p, _p,
                     _i32, _i32, _p, _p, _sz, _p, _i32, _p, _p, _p)
 _layer_noalloc = _sig("moe_layer_noalloc", _i32, ctypes.POINTER(PoolStruct), _p, _p, _p, _p,
                       _i32, _i32, _i32, _p, _p, _i32, _p)
+_mx_row_bytes = _sig("moe_mx_row_bytes", _sz, _i32, _i32)
+_mx_quantize = _sig("moe_mx_quantize", _i32, _p, _i32, _i32, _i32, _i32, _p, _p, _p)
+_mx_dequantize = _sig("moe_mx_dequantize", _i32, _p, _p, _i32, _i32, _i32, _p, _i32, _p)
+_mx_gate_up = _sig("moe_mx_expert_gate_up", _i32, ctypes.POINTER(PoolStruct), _p, _i32, _p, _p,
+                   _i32, _i32, _i32, _p, _p, _p, _p, _i32, _p)
+_mx_down = _sig("moe_mx_expert_down", _i32, ctypes.POINTER(PoolStruct), _p, _i32, _p, _p, _i32,
+                _i32, _i32, _p, _p, _p, _i32, _p)
+_mx_ffn = _sig("moe_mx_expert_ffn", _i32, ctypes.POINTER(PoolStruct), _p, _i32, _p, _p, _i32,
+               _i32, _i32, _p, _p, _p, _p, _p, _i32, _p, _p, _i32, _p)
+_f32 = ctypes.c_float
+_add_norm = _sig("moe_add_norm", _i32, _p, _i32, _p, _i32, _f32, _p, _i32, _f32, _i32, _i32, _p,
+                 _p, _p)
+_combine_norm = _sig("moe_combine_norm", _i32, _p, _p, _p, _i32, _i32, _i32, _p, _i32, _p, _p,
+                     _i32, _f32, _p, _i32, _f32, _p, _p, _p)
 _status_string = _sig("moe_status_string", ctypes.c_char_p, _i32)
 _last_error = _sig("moe_last_error", ctypes.c_char_p)
 
@@ -93,6 +110,8 @@ EXPORTED = ("moe_plane_bytes", "moe_pool_pack", "moe_route_scratch_bytes", "moe_
             "moe_expert_down", "moe_combine", "moe_miss_list", "moe_merge_misses",
             "moe_stage_plan", "moe_stage_copy",
             "moe_layer_workspace", "moe_layer", "moe_layer_timed", "moe_layer_noalloc",
+            "moe_mx_row_bytes", "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_expert_gate_up",
+            "moe_mx_expert_down", "moe_mx_expert_ffn", "moe_add_norm", "moe_combine_norm",
             "moe_status_string", "moe_last_error")
 
 NOALLOC_WS_BYTES = 32 << 20   # MOE_NOALLOC_WS_BYTES
@@ -471,3 +490,191 @@ class LayerCall:
         if st != 0:
             _check(st)
 
+
+# --------------------------------------------- microscaled rows, and the block's two ends
+
+
+def _one_of(name, value, choices):
+    if value not in choices:
+        raise ValueError(f"{name}: {value!r}, expected one of {', '.join(map(repr, choices))}")
+
+
+def _tensor(t, dtypes, shape, name, like):
+    """A contiguous device tensor of one of `dtypes`, on the device of `like`."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    _need(t, t.dtype, shape, name)
+    if t.device != like.device:
+        raise ValueError(f"{name}: on {t.device}, expected {like.device}")
+
+
+def _run(fn, like, stream, *args):
+    """Calls fn(*args, stream) with the device of `like` current, on that device's current
+    stream unless one is given."""
+    with torch.cuda.device(like.device):
+        _check(fn(*args, _stream(stream)))
+
+
+def mx_row_bytes(fmt: str, K: int) -> int:
+    """Bytes of one row of K codes ("mxfp4" or "mxfp6")."""
+    return _mx_row_bytes(_MX[fmt], K)
+
+
+def _mx_planes(q, s, fmt, rows, K, names, like):
+    _one_of("fmt", fmt, _MX)
+    _tensor(q, (torch.uint8,), (*rows, mx_row_bytes(fmt, K)), names[0], like)
+    _tensor(s, (torch.uint8,), (*rows, K // 32), names[1], like)
+
+
+def mx_quantize(x, fmt: str = "mxfp4", q=None, s=None, stream=None):
+    """x bf16, fp16 or fp32 [..., K] -> (codes uint8 [..., mx_row_bytes], scales uint8 [..., K/32]).
+
+    fmt: "mxfp4" (E2M1) or "mxfp6" (E2M3). MXFP4 planes are the canonical layout that
+    Pool.from_canonical and pool_pack take."""
+    _one_of("fmt", fmt, _MX)
+    *rows, K = x.shape
+    _tensor(x, tuple(_DT), x.shape, "x", x)
+    if q is None:
+        q = torch.empty((*rows, mx_row_bytes(fmt, K)), dtype=torch.uint8, device=x.device)
+    if s is None:
+        s = torch.empty((*rows, K // 32), dtype=torch.uint8, device=x.device)
+    _mx_planes(q, s, fmt, rows, K, ("q", "s"), x)
+    _run(_mx_quantize, x, stream, _ptr(x), _DT[x.dtype], x.numel() // max(K, 1), K, _MX[fmt],
+         _ptr(q), _ptr(s))
+    return q, s
+
+
+def mx_dequantize(q, s, fmt: str = "mxfp4", dtype=torch.bfloat16, out=None, stream=None):
+    """The values of codes and scales: bf16, fp16 or fp32 [..., K]."""
+    _one_of("dtype", dtype, _DT)
+    *rows, nb = s.shape
+    K = 32 * nb
+    _mx_planes(q, s, fmt, rows, K, ("q", "s"), q)
+    if out is None:
+        out = torch.empty((*rows, K), dtype=dtype, device=q.device)
+    _tensor(out, (dtype,), (*rows, K), "out", q)
+    _run(_mx_dequantize, q, stream, _ptr(q), _ptr(s), _MX[fmt], s.numel() // max(nb, 1), K,
+         _ptr(out), _DT[dtype])
+    return out
+
+
+def _mx_checks(pool, slot_map, T, k, offsets, perm, err_flags, like):
+    E = slot_map.shape[0]
+    i32 = (torch.int32,)
+    _tensor(slot_map, i32, (E,), "slot_map", like)
+    _tensor(offsets, i32, (E + 1,), "offsets", like)
+    if perm is not None:
+        _tensor(perm, i32, (T * k,), "perm", like)
+    if err_flags is not None and (err_flags.device != like.device or err_flags.numel() < 1 or
+                                  err_flags.element_size() != 4):
+        raise ValueError("err_flags: needs 32-bit words on the operands' device")
+    if pool.planes["gate_q"].device != like.device:
+        raise ValueError(f"pool: on {pool.planes['gate_q'].device}, expected {like.device}")
+    return E
+
+
+def _rows(t, dtype, shape, name, like):
+    """The given output, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _tensor(t, (dtype,), shape, name, like)
+    return t
+
+
+def mx_expert_gate_up(pool: Pool, slot_map, x_q, x_s, fmt: str, k: int, offsets, perm, h=None,
+                      err_flags=None, path=PATH_AUTO, stream=None):
+    """Microscaled rows (mx_quantize of x [T, H]) -> h bf16 [T*k, I] in bucket order."""
+    T = x_q.shape[0]
+    _mx_planes(x_q, x_s, fmt, (T,), pool.H, ("x_q", "x_s"), x_q)
+    E = _mx_checks(pool, slot_map, T, k, offsets, perm, err_flags, x_q)
+    h = _rows(h, torch.bfloat16, (T * k, pool.I), "h", x_q)
+    _run(_mx_gate_up, x_q, stream, ctypes.byref(pool.struct), _ptr(slot_map), E, _ptr(x_q),
+         _ptr(x_s), _MX[fmt], T, k, _ptr(offsets), _ptr(perm), _ptr(h), _ptr(err_flags), path)
+    return h
+
+
+def mx_expert_down(pool: Pool, slot_map, T: int, k: int, offsets, h_q, h_s, fmt: str, y=None,
+                   err_flags=None, path=PATH_AUTO, stream=None):
+    """Microscaled rows (mx_quantize of h [T*k, I]) -> y fp32 [T*k, H] in bucket order."""
+    _mx_planes(h_q, h_s, fmt, (T * k,), pool.I, ("h_q", "h_s"), h_q)
+    E = _mx_checks(pool, slot_map, T, k, offsets, None, err_flags, h_q)
+    y = _rows(y, torch.float32, (T * k, pool.H), "y", h_q)
+    _run(_mx_down, h_q, stream, ctypes.byref(pool.struct), _ptr(slot_map), E, _ptr(h_q),
+         _ptr(h_s), _MX[fmt], T, k, _ptr(offsets), _ptr(y), _ptr(err_flags), path)
+    return y
+
+
+def mx_expert_ffn(pool: Pool, slot_map, x_q, x_s, fmt: str, k: int, offsets, perm, h_fmt=None,
+                  h=None, h_q=None, h_s=None, y=None, err_flags=None, path=PATH_AUTO,
+                  stream=None):
+    """gate/up, h quantised to h_fmt (default: fmt), down -> (h bf16 [T*k, I], y fp32 [T*k, H])."""
+    T = x_q.shape[0]
+    h_fmt = fmt if h_fmt is None else h_fmt
+    _mx_planes(x_q, x_s, fmt, (T,), pool.H, ("x_q", "x_s"), x_q)
+    _one_of("h_fmt", h_fmt, _MX)
+    E = _mx_checks(pool, slot_map, T, k, offsets, perm, err_flags, x_q)
+    h = _rows(h, torch.bfloat16, (T * k, pool.I), "h", x_q)
+    h_q = _rows(h_q, torch.uint8, (T * k, mx_row_bytes(h_fmt, pool.I)), "h_q", x_q)
+    h_s = _rows(h_s, torch.uint8, (T * k, pool.I // 32), "h_s", x_q)
+    y = _rows(y, torch.float32, (T * k, pool.H), "y", x_q)
+    _run(_mx_ffn, x_q, stream, ctypes.byref(pool.struct), _ptr(slot_map), E, _ptr(x_q),
+         _ptr(x_s), _MX[fmt], T, k, _ptr(offsets), _ptr(perm), _ptr(h), _ptr(h_q), _ptr(h_s),
+         _MX[h_fmt], _ptr(y), _ptr(err_flags), path)
+    return h, y
+
+
+_STREAM_TYPES = (torch.bfloat16, torch.float32)
+
+
+def add_norm(resid, weight, eps: float = 1e-6, delta=None, scale: float = 1.0, resid_out=None,
+             x=None, stream=None):
+    """The layer's entry: s = resid + scale * delta, x = bf16(rms-normed s * weight).
+
+    resid bf16 or fp32 [T, H], delta bf16 or fp32 [T, H] or None, weight bf16 or fp32 [H] ->
+    (x bf16 [T, H], resid_out like resid). Without delta the stream is not written and resid
+    is returned in its place; resid_out may be resid itself."""
+    T, H = resid.shape
+    _tensor(resid, _STREAM_TYPES, (T, H), "resid", resid)
+    _tensor(weight, _STREAM_TYPES, (H,), "weight", resid)
+    if delta is not None:
+        _tensor(delta, _STREAM_TYPES, (T, H), "delta", resid)
+    if delta is not None or resid_out is not None:
+        resid_out = _rows(resid_out, resid.dtype, (T, H), "resid_out", resid)
+    x = _rows(x, torch.bfloat16, (T, H), "x", resid)
+    _run(_add_norm, resid, stream, _ptr(resid), _DT[resid.dtype], _ptr(delta),
+         0 if delta is None else _DT[delta.dtype], scale, _ptr(weight), _DT[weight.dtype], eps, T,
+         H, _ptr(resid_out), _ptr(x))
+    return x, resid if resid_out is None else resid_out
+
+
+def combine_norm(y, inv_perm, w, resid, eps: float = 1e-6, post_weight=None, gate=None,
+                 scale: float = 1.0, next_weight=None, resid_out=None, x=None, stream=None):
+    """The layer's exit: combine, post-norm, gate and scale, residual add, next layer's norm.
+
+    y fp32 [T*k, H], inv_perm int32 [T*k], w fp32 [T, k], resid bf16 or fp32 [T, H];
+    post_weight [H], gate [H] or [T, H], next_weight [H]: bf16 or fp32, all of one type, each
+    may be None -> (resid_out like resid, x bf16 [T, H] or None). resid_out may be resid."""
+    T, k = w.shape
+    H = resid.shape[-1]
+    _tensor(y, (torch.float32,), (T * k, H), "y", resid)
+    _tensor(inv_perm, (torch.int32,), (T * k,), "inv_perm", resid)
+    _tensor(w, (torch.float32,), (T, k), "w", resid)
+    _tensor(resid, _STREAM_TYPES, (T, H), "resid", resid)
+    params = {"post_weight": post_weight, "gate": gate, "next_weight": next_weight}
+    given = [t for t in params.values() if t is not None]
+    for name, t in params.items():
+        if t is not None:
+            per_token = name == "gate" and t.dim() == 2
+            _tensor(t, _STREAM_TYPES, (T, H) if per_token else (H,), name, resid)
+            if t.dtype != given[0].dtype:
+                raise TypeError("post_weight, gate and next_weight: more than one dtype")
+    if next_weight is None and x is not None:
+        raise ValueError("x: needs next_weight")
+    resid_out = _rows(resid_out, resid.dtype, (T, H), "resid_out", resid)
+    if next_weight is not None:
+        x = _rows(x, torch.bfloat16, (T, H), "x", resid)
+    _run(_combine_norm, resid, stream, _ptr(y), _ptr(inv_perm), _ptr(w), T, k, H, _ptr(resid),
+         _DT[resid.dtype], _ptr(post_weight), _ptr(gate),
+         T if gate is not None and gate.dim() == 2 else 1, scale, _ptr(next_weight),
+         _DT[given[0].dtype] if given else _DT[torch.float32], eps, _ptr(resid_out), _ptr(x))
+    return resid_out, x

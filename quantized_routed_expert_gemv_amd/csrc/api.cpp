@@ -715,4 +715,239 @@ moe_status moe_layer_timed(const moe_pool* pool, const int32_t* slot_map,
                     err_flags, path, stream, ev_gate_up_begin, ev_gate_up_end);
 }
 
+// ---- microscaled formats and the block's two ends
+
+namespace {
+
+moe_status check_mx(int32_t fmt, int32_t K) {
+  if (fmt != MOE_MX_FP4 && fmt != MOE_MX_FP6)
+    return fail(MOE_ERR_UNSUPPORTED, "unknown microscaled format %d", fmt);
+  if (K <= 0 || K % 32) return fail(MOE_ERR_INVALID_ARG, "K = %d is not a positive multiple of 32", K);
+  return MOE_OK;
+}
+
+moe_status check_type(const char* what, int32_t type, bool fp16) {
+  if (type == MOE_T_BF16 || type == MOE_T_FP32 || (fp16 && type == MOE_T_FP16)) return MOE_OK;
+  return fail(MOE_ERR_UNSUPPORTED, "%s type %d", what, type);
+}
+
+// rows x K values, one thread per 8 of them
+moe_status check_mx_rows(int32_t rows, int32_t K) {
+  if (rows < 0) return fail(MOE_ERR_INVALID_ARG, "rows = %d < 0", rows);
+  if ((int64_t)rows * K >= (int64_t(1) << 40))
+    return fail(MOE_ERR_INVALID_ARG, "rows*K = %lld values, limit 2^40", (long long)rows * K);
+  return MOE_OK;
+}
+
+// Sizes and parameters that both norms share; H as everywhere a multiple of 32.
+moe_status check_norm(int32_t T, int32_t H, int32_t k, int32_t resid_type, int32_t weight_type) {
+  moe_status s = check_shape(T, H, moe::kMaxE, k);
+  if (s != MOE_OK) return s;
+  s = check_type("resid", resid_type, false);
+  if (s != MOE_OK) return s;
+  return check_type("weight", weight_type, false);
+}
+
+// Arguments of the products on microscaled rows.
+moe_status check_mx_product(const moe_pool* pool, const int32_t* slot_map, int32_t E, int32_t fmt,
+                            int32_t T, int32_t k, const int32_t* offsets, uint32_t* err_flags,
+                            int32_t path) {
+  moe_status s = check_ffn_args(pool, slot_map, E, T, k, offsets, err_flags, path);
+  if (s != MOE_OK) return s;
+  if (pool->fmt != MOE_W_MXFP4)
+    return fail(MOE_ERR_UNSUPPORTED, "products on microscaled rows need an MXFP4 pool, not format %d",
+                pool->fmt);
+  return check_mx(fmt, pool->H);
+}
+
+moe_status mx_gate_up(const moe_pool* pool, const int32_t* slot_map, int32_t E, const void* x_q,
+                      const uint8_t* x_s, int32_t x_fmt, int32_t T, int32_t k,
+                      const int32_t* offsets, const int32_t* perm, uint16_t* h, uint32_t* err,
+                      int32_t path, hipStream_t st) {
+  moe::PoolView g, u, d;
+  pool_views(pool, &g, &u, &d);
+  const moe::MxProduct p{g, u, slot_map, pool->n_slots, E, T, k, offsets, perm,
+                         (const uint8_t*)x_q, x_s, pool->H, pool->I, h, nullptr, err};
+  clear_stale_error();
+  return hip_status(moe::launch_mx_product(p, x_fmt, true, use_gemv(path, T), st),
+                    "microscaled gate/up");
+}
+
+moe_status mx_down(const moe_pool* pool, const int32_t* slot_map, int32_t E, const void* h_q,
+                   const uint8_t* h_s, int32_t h_fmt, int32_t T, int32_t k,
+                   const int32_t* offsets, float* y, uint32_t* err, int32_t path,
+                   hipStream_t st) {
+  moe::PoolView g, u, d;
+  pool_views(pool, &g, &u, &d);
+  const moe::MxProduct p{d, d, slot_map, pool->n_slots, E, T, k, offsets, nullptr,
+                         (const uint8_t*)h_q, h_s, pool->I, pool->H, nullptr, y, err};
+  clear_stale_error();
+  return hip_status(moe::launch_mx_product(p, h_fmt, false, use_gemv(path, T), st),
+                    "microscaled down");
+}
+
+}  // namespace
+
+size_t moe_mx_row_bytes(int32_t fmt, int32_t K) {
+  if ((fmt != MOE_MX_FP4 && fmt != MOE_MX_FP6) || K < 0 || K % 32) return 0;
+  return (size_t)(K / 32) * moe::mx_block_bytes(fmt);
+}
+
+moe_status moe_mx_quantize(const void* src, int32_t src_type, int32_t rows, int32_t K,
+                           int32_t fmt, void* q, uint8_t* s, void* stream) {
+  moe_status st = check_mx(fmt, K);
+  if (st != MOE_OK) return st;
+  st = check_type("src", src_type, true);
+  if (st != MOE_OK) return st;
+  st = check_mx_rows(rows, K);
+  if (st != MOE_OK) return st;
+  if (rows == 0) return ok();
+  CHECK_PTR(src);
+  CHECK_PTR(q);
+  if (s == nullptr) return fail(MOE_ERR_INVALID_ARG, "s is NULL");
+  clear_stale_error();
+  return hip_status(moe::launch_mx_quantize(src, src_type, (int64_t)rows * K, fmt, (uint8_t*)q, s,
+                                            (hipStream_t)stream),
+                    "microscaled quantise");
+}
+
+moe_status moe_mx_dequantize(const void* q, const uint8_t* s, int32_t fmt, int32_t rows,
+                             int32_t K, void* dst, int32_t dst_type, void* stream) {
+  moe_status st = check_mx(fmt, K);
+  if (st != MOE_OK) return st;
+  st = check_type("dst", dst_type, true);
+  if (st != MOE_OK) return st;
+  st = check_mx_rows(rows, K);
+  if (st != MOE_OK) return st;
+  if (rows == 0) return ok();
+  CHECK_PTR(q);
+  CHECK_PTR(dst);
+  if (s == nullptr) return fail(MOE_ERR_INVALID_ARG, "s is NULL");
+  clear_stale_error();
+  return hip_status(moe::launch_mx_dequantize((const uint8_t*)q, s, (int64_t)rows * K, fmt, dst,
+                                              dst_type, (hipStream_t)stream),
+                    "microscaled dequantise");
+}
+
+moe_status moe_mx_expert_gate_up(const moe_pool* pool, const int32_t* slot_map, int32_t E,
+                                 const void* x_q, const uint8_t* x_s, int32_t x_fmt, int32_t T,
+                                 int32_t k, const int32_t* offsets, const int32_t* perm,
+                                 uint16_t* h, uint32_t* err_flags, int32_t path, void* stream) {
+  moe_status s = check_mx_product(pool, slot_map, E, x_fmt, T, k, offsets, err_flags, path);
+  if (s != MOE_OK || T == 0) return s == MOE_OK ? ok() : s;
+  CHECK_PTR(x_q);
+  CHECK_PTR(perm);
+  CHECK_PTR(h);
+  if (x_s == nullptr) return fail(MOE_ERR_INVALID_ARG, "x_s is NULL");
+  return mx_gate_up(pool, slot_map, E, x_q, x_s, x_fmt, T, k, offsets, perm, h, err_flags, path,
+                    (hipStream_t)stream);
+}
+
+moe_status moe_mx_expert_down(const moe_pool* pool, const int32_t* slot_map, int32_t E,
+                              const void* h_q, const uint8_t* h_s, int32_t h_fmt, int32_t T,
+                              int32_t k, const int32_t* offsets, float* y, uint32_t* err_flags,
+                              int32_t path, void* stream) {
+  moe_status s = check_mx_product(pool, slot_map, E, h_fmt, T, k, offsets, err_flags, path);
+  if (s != MOE_OK || T == 0) return s == MOE_OK ? ok() : s;
+  CHECK_PTR(h_q);
+  CHECK_PTR(y);
+  if (h_s == nullptr) return fail(MOE_ERR_INVALID_ARG, "h_s is NULL");
+  return mx_down(pool, slot_map, E, h_q, h_s, h_fmt, T, k, offsets, y, err_flags, path,
+                 (hipStream_t)stream);
+}
+
+moe_status moe_mx_expert_ffn(const moe_pool* pool, const int32_t* slot_map, int32_t E,
+                             const void* x_q, const uint8_t* x_s, int32_t x_fmt, int32_t T,
+                             int32_t k, const int32_t* offsets, const int32_t* perm, uint16_t* h,
+                             void* h_q, uint8_t* h_s, int32_t h_fmt, float* y,
+                             uint32_t* err_flags, int32_t path, void* stream) {
+  moe_status s = check_mx_product(pool, slot_map, E, x_fmt, T, k, offsets, err_flags, path);
+  if (s != MOE_OK) return s;
+  s = check_mx(h_fmt, pool->I);
+  if (s != MOE_OK) return s;
+  s = check_mx_rows(T * k, pool->I);
+  if (s != MOE_OK) return s;
+  if (T == 0) return ok();
+  CHECK_PTR(x_q);
+  CHECK_PTR(perm);
+  CHECK_PTR(h);
+  CHECK_PTR(h_q);
+  CHECK_PTR(y);
+  if (x_s == nullptr || h_s == nullptr)
+    return fail(MOE_ERR_INVALID_ARG, "%s is NULL", x_s == nullptr ? "x_s" : "h_s");
+  const hipStream_t st = (hipStream_t)stream;
+  s = mx_gate_up(pool, slot_map, E, x_q, x_s, x_fmt, T, k, offsets, perm, h, err_flags, path, st);
+  if (s != MOE_OK) return s;
+  s = hip_status(moe::launch_mx_quantize(h, MOE_T_BF16, (int64_t)T * k * pool->I, h_fmt,
+                                         (uint8_t*)h_q, h_s, st),
+                 "microscaled quantise");
+  if (s != MOE_OK) return s;
+  return mx_down(pool, slot_map, E, h_q, h_s, h_fmt, T, k, offsets, y, err_flags, path, st);
+}
+
+moe_status moe_add_norm(const void* resid, int32_t resid_type, const void* delta,
+                        int32_t delta_type, float scale, const void* weight, int32_t weight_type,
+                        float eps, int32_t T, int32_t H, void* resid_out, uint16_t* x,
+                        void* stream) {
+  moe_status s = check_norm(T, H, 1, resid_type, weight_type);
+  if (s != MOE_OK) return s;
+  if (delta != nullptr && (s = check_type("delta", delta_type, false)) != MOE_OK) return s;
+  if (T == 0) return ok();
+  CHECK_PTR(resid);
+  if (delta != nullptr) {
+    CHECK_PTR(delta);
+    CHECK_PTR(resid_out);
+  } else if (resid_out != nullptr) {
+    CHECK_PTR(resid_out);
+  }
+  CHECK_PTR(weight);
+  CHECK_PTR(x);
+  moe::BlockNorm a{};
+  a.T = T, a.H = H, a.k = 1;
+  a.resid = resid, a.delta = delta, a.weight = weight;
+  a.eps = eps, a.scale = scale;
+  a.resid_out = resid_out, a.x = x;
+  a.delta_f32 = delta_type == MOE_T_FP32, a.par_f32 = weight_type == MOE_T_FP32;
+  clear_stale_error();
+  return hip_status(moe::launch_block_norm(a, false, resid_type == MOE_T_FP32, (hipStream_t)stream),
+                    "add + norm");
+}
+
+moe_status moe_combine_norm(const float* y, const int32_t* inv_perm, const float* topk_w,
+                            int32_t T, int32_t k, int32_t H, const void* resid,
+                            int32_t resid_type, const void* post_weight, const void* gate,
+                            int32_t gate_rows, float scale, const void* next_weight,
+                            int32_t weight_type, float eps, void* resid_out, uint16_t* x,
+                            void* stream) {
+  moe_status s = check_norm(T, H, k, resid_type, weight_type);
+  if (s != MOE_OK) return s;
+  if (gate != nullptr && gate_rows != 1 && gate_rows != T)
+    return fail(MOE_ERR_INVALID_ARG, "gate_rows = %d, neither 1 nor T = %d", gate_rows, T);
+  if (T == 0) return ok();
+  if ((next_weight == nullptr) != (x == nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "next_weight and x go together: one of them is NULL");
+  CHECK_PTR(y);
+  CHECK_PTR(inv_perm);
+  CHECK_PTR(topk_w);
+  CHECK_PTR(resid);
+  CHECK_PTR(resid_out);
+  if (post_weight != nullptr) CHECK_PTR(post_weight);
+  if (gate != nullptr) CHECK_PTR(gate);
+  if (x != nullptr) {
+    CHECK_PTR(next_weight);
+    CHECK_PTR(x);
+  }
+  moe::BlockNorm a{};
+  a.T = T, a.H = H, a.k = k;
+  a.resid = resid, a.y = y, a.inv_perm = inv_perm, a.w = topk_w;
+  a.post = post_weight, a.gate = gate, a.gate_stride = gate_rows == 1 ? 0 : H;
+  a.weight = next_weight;
+  a.eps = eps, a.scale = scale;
+  a.resid_out = resid_out, a.x = x;
+  a.par_f32 = weight_type == MOE_T_FP32;
+  clear_stale_error();
+  return hip_status(moe::launch_block_norm(a, true, resid_type == MOE_T_FP32, (hipStream_t)stream),
+                    "combine + norm");
+}
+
 }  // extern "C"

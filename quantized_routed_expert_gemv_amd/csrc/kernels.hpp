@@ -133,4 +133,50 @@ hipError_t launch_stage_copy(const StagePlanes& pl, const int32_t* copy_list,
                              const int32_t* counters, int first_slot, int max_copies,
                              int backing_slots, uint32_t* err_flags, hipStream_t stream);
 
+// The norms at a block's two ends (csrc/norm.hip). Entry: delta (nullable) is added to resid;
+// exit: y, inv_perm, w are combined, then post (nullable), gate (nullable).
+struct BlockNorm {
+  int T, H, k;
+  const void* resid;
+  const void* delta;        // entry: [T][H]
+  const float* y;           // exit: [T*k][H]
+  const int32_t* inv_perm;
+  const float* w;
+  const void* post;         // [H]
+  const void* gate;         // [H] (gate_stride 0) or [T][H] (gate_stride H)
+  int64_t gate_stride;
+  const void* weight;       // [H], with x
+  float eps, scale;
+  void* resid_out;          // nullable; may be resid
+  uint16_t* x;              // nullable at the exit
+  bool delta_f32, par_f32;  // types of delta; of post, gate and weight
+};
+hipError_t launch_block_norm(const BlockNorm& a, bool exit, bool resid_f32, hipStream_t stream);
+
+// Microscaled formats (csrc/mxquant.hip): n values, a multiple of 32, flat.
+enum MxFmt : int { kMxFp4 = 1, kMxFp6 = 2 };
+enum DType : int { kBF16 = 1, kFP16 = 2, kFP32 = 3 };
+__host__ __device__ constexpr int mx_block_bytes(int fmt) { return fmt == kMxFp4 ? 16 : 24; }
+hipError_t launch_mx_quantize(const void* src, int type, int64_t n, int fmt, uint8_t* q,
+                              uint8_t* s, hipStream_t st);
+hipError_t launch_mx_dequantize(const uint8_t* q, const uint8_t* s, int64_t n, int fmt, void* dst,
+                                int type, hipStream_t st);
+
+// Expert products on microscaled rows (csrc/mxgemm.hip), MXFP4 pools. gated: q and s hold T
+// token rows, gathered through perm, and h is written; else T*k rows in bucket order, and y.
+struct MxProduct {
+  PoolView a, b;            // gate and up; or down in both
+  const int32_t* slot_map;
+  int n_slots, E, T, k;
+  const int32_t* offsets;
+  const int32_t* perm;      // gated
+  const uint8_t* q;
+  const uint8_t* s;
+  int K, N;
+  uint16_t* h;
+  float* y;
+  uint32_t* err;
+};
+hipError_t launch_mx_product(const MxProduct& p, int fmt, bool gated, bool gemv, hipStream_t st);
+
 }  // namespace moe

@@ -1,0 +1,202 @@
+"""Microscaled formats and block norms without a GPU: the oracle's formats against values
+written out by hand, and the refusals of every call, on the host, before any launch."""
+import ctypes
+import os
+
+import numpy as np
+import pytest
+
+from oracle import mx
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+LIB = os.path.join(ROOT, "quantized_routed_expert_gemv_amd", "libmoe.so")
+OK, INVALID, UNSUPPORTED = 0, 1, 2
+FAKE = ctypes.c_void_p(0x10000)      # aligned, never dereferenced by the checks below
+ODD = ctypes.c_void_p(0x10004)
+P, I32, F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float
+
+
+def test_code_tables():
+    assert mx.code_values("mxfp4").tolist() == [0, .5, 1, 1.5, 2, 3, 4, 6, 0, -.5, -1, -1.5, -2,
+                                                -3, -4, -6]
+    v = mx.code_values("mxfp6")
+    assert v[:9].tolist() == [i / 8 for i in range(9)]
+    assert v[15] == 1.875 and v[16] == 2 and v[17] == 2.25 and v[24] == 4 and v[31] == 7.5
+    assert (v[32:] == -v[:32]).all() and (np.diff(v[:32]) > 0).all()
+
+
+@pytest.mark.parametrize("fmt,x,want", [
+    # amax 6: the scale is one; halves go to the even code
+    ("mxfp4", [6, .25, .75, 1.25, 1.75, 2.5, 3.5, 5, -5], [6, 0, 1, 1, 2, 2, 4, 4, -4]),
+    ("mxfp4", [7.9, 7, 5.1], [6, 6, 6]),                       # saturation
+    ("mxfp6", [7.9, 7.2, 7.25, 2.125, .0625, .1875, -.3125], [7.5, 7, 7, 2, 0, .25, -.25]),
+])
+def test_quantize_by_hand(fmt, x, want):
+    row = np.zeros(32)
+    row[:len(x)] = x
+    c, s = mx.quantize(row, fmt)
+    assert s.tolist() == [127]
+    assert mx.dequantize(mx.pack(c, fmt), s, fmt)[:len(x)].tolist() == want
+
+
+def test_scales():
+    x = np.zeros((6, 32))
+    x[1, 3] = 2.0 ** -140
+    x[2, 5] = np.inf
+    x[3, 7] = np.nan
+    x[4, 0] = 3.4e38
+    x[5, 0] = 2.0 ** -122
+    c, s = mx.quantize(x, "mxfp4")
+    assert s[:, 0].tolist() == [1, 1, 255, 255, 252, 3]
+    assert not c[2:4].any()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp6"])
+def test_pack_round_trip(fmt):
+    c = np.random.default_rng(0).integers(0, 1 << mx.BITS[fmt], (3, 64)).astype(np.uint8)
+    q = mx.pack(c, fmt)
+    assert q.shape == (3, 64 * mx.BITS[fmt] // 8)
+    assert (mx.unpack(q, fmt) == c).all()
+    if fmt == "mxfp4":
+        assert (q == (c[:, 0::2] | c[:, 1::2] << 4)).all()
+
+
+# -------------------------------------------------------------------------- refusals
+
+
+class Pool(ctypes.Structure):
+    _fields_ = [("fmt", I32), ("n_slots", I32), ("H", I32), ("I", I32)] + \
+               [(n, P) for n in ("gate_q", "gate_s", "up_q", "up_s", "down_q", "down_s")]
+
+
+@pytest.fixture(scope="module")
+def lib():
+    lib = ctypes.CDLL(LIB)
+    lib.moe_last_error.restype = ctypes.c_char_p
+    lib.moe_mx_row_bytes.restype = ctypes.c_size_t
+    lib.moe_mx_quantize.argtypes = [P, I32, I32, I32, I32, P, P, P]
+    lib.moe_mx_dequantize.argtypes = [P, P, I32, I32, I32, P, I32, P]
+    pool = ctypes.POINTER(Pool)
+    lib.moe_mx_expert_gate_up.argtypes = [pool, P, I32, P, P, I32, I32, I32, P, P, P, P, I32, P]
+    lib.moe_mx_expert_down.argtypes = [pool, P, I32, P, P, I32, I32, I32, P, P, P, I32, P]
+    lib.moe_mx_expert_ffn.argtypes = [pool, P, I32, P, P, I32, I32, I32, P, P, P, P, P, I32, P, P,
+                                      I32, P]
+    lib.moe_add_norm.argtypes = [P, I32, P, I32, F32, P, I32, F32, I32, I32, P, P, P]
+    lib.moe_combine_norm.argtypes = [P, P, P, I32, I32, I32, P, I32, P, P, I32, F32, P, I32, F32,
+                                     P, P, P]
+    return lib
+
+
+def test_row_bytes(lib):
+    assert lib.moe_mx_row_bytes(1, 2880) == 1440
+    assert lib.moe_mx_row_bytes(2, 2880) == 2160
+    assert lib.moe_mx_row_bytes(2, 0) == 0
+    assert lib.moe_mx_row_bytes(1, 48) == 0
+    assert lib.moe_mx_row_bytes(3, 64) == 0
+
+
+def test_quantize_refusals(lib):
+    q = lib.moe_mx_quantize
+    assert q(FAKE, 1, 4, 64, 3, FAKE, FAKE, None) == UNSUPPORTED
+    assert q(FAKE, 4, 4, 64, 1, FAKE, FAKE, None) == UNSUPPORTED
+    assert q(FAKE, 0, 4, 64, 1, FAKE, FAKE, None) == UNSUPPORTED
+    for rows, K in ((4, 48), (4, 0), (4, -32), (-1, 64), (1 << 30, 1 << 10)):
+        assert q(FAKE, 1, rows, K, 1, FAKE, FAKE, None) == INVALID, (rows, K)
+    assert q(None, 1, 4, 64, 1, FAKE, FAKE, None) == INVALID
+    assert q(ODD, 1, 4, 64, 1, FAKE, FAKE, None) == INVALID
+    assert q(FAKE, 1, 4, 64, 1, ODD, FAKE, None) == INVALID
+    assert q(FAKE, 1, 4, 64, 1, FAKE, None, None) == INVALID
+    assert b"s is NULL" in lib.moe_last_error()
+    assert q(None, 1, 0, 64, 1, None, None, None) == OK
+    d = lib.moe_mx_dequantize
+    assert d(FAKE, FAKE, 5, 4, 64, FAKE, 1, None) == UNSUPPORTED
+    assert d(FAKE, FAKE, 1, 4, 64, FAKE, 4, None) == UNSUPPORTED
+    assert d(FAKE, FAKE, 1, 4, 40, FAKE, 1, None) == INVALID
+    assert d(FAKE, FAKE, 1, -4, 64, FAKE, 1, None) == INVALID
+    assert d(FAKE, None, 1, 4, 64, FAKE, 1, None) == INVALID
+    assert d(FAKE, FAKE, 1, 4, 64, ODD, 1, None) == INVALID
+    assert d(None, None, 1, 0, 64, None, 1, None) == OK
+
+
+def _pool(fmt=1, n_slots=4, H=256, I=256):
+    return ctypes.byref(Pool(fmt, n_slots, H, I, *([0x10000] * 6)))
+
+
+def test_product_refusals(lib):
+    g, d, f = lib.moe_mx_expert_gate_up, lib.moe_mx_expert_down, lib.moe_mx_expert_ffn
+
+    def gate_up(pool=None, sm=FAKE, E=8, q=FAKE, s=FAKE, fmt=1, T=4, k=2, off=FAKE, perm=FAKE,
+                h=FAKE, err=None, path=0):
+        return g(pool or _pool(), sm, E, q, s, fmt, T, k, off, perm, h, err, path, None)
+
+    def down(pool=None, sm=FAKE, E=8, q=FAKE, s=FAKE, fmt=1, T=4, k=2, off=FAKE, y=FAKE, err=None,
+             path=0):
+        return d(pool or _pool(), sm, E, q, s, fmt, T, k, off, y, err, path, None)
+
+    def ffn(pool=None, q=FAKE, s=FAKE, fmt=1, T=4, perm=FAKE, h=FAKE, hq=FAKE, hs=FAKE, hfmt=1,
+            y=FAKE):
+        return f(pool or _pool(), FAKE, 8, q, s, fmt, T, 2, FAKE, perm, h, hq, hs, hfmt, y, None,
+                 0, None)
+
+    for call in (gate_up, down):
+        for pfmt in (2, 3, 4, 5):
+            assert call(pool=_pool(fmt=pfmt)) == UNSUPPORTED
+        assert call(fmt=0) == UNSUPPORTED and call(fmt=3) == UNSUPPORTED
+        for bad in (dict(E=300), dict(k=9), dict(k=0), dict(T=-1), dict(E=1), dict(path=4),
+                    dict(sm=None), dict(off=None), dict(q=None), dict(q=ODD), dict(s=None),
+                    dict(err=ctypes.c_void_p(0x10002)), dict(T=1 << 30)):
+            assert call(**bad) == INVALID, bad
+            assert lib.moe_last_error()
+        assert call(T=0, q=None, s=None, sm=None, off=None) == OK
+    assert gate_up(perm=None) == INVALID and gate_up(h=None) == INVALID
+    assert down(y=None) == INVALID and down(y=ODD) == INVALID
+    for bad in (dict(q=None), dict(s=None), dict(perm=None), dict(h=None), dict(hq=None),
+                dict(hs=None), dict(y=None), dict(hq=ODD)):
+        assert ffn(**bad) == INVALID, bad
+    assert ffn(hfmt=3) == UNSUPPORTED and ffn(fmt=7) == UNSUPPORTED
+    assert ffn(pool=_pool(fmt=2)) == UNSUPPORTED
+    assert ffn(T=0, q=None, h=None) == OK
+
+
+def test_norm_refusals(lib):
+    def add(r=FAKE, rt=1, dl=FAKE, dt=1, w=FAKE, wt=1, T=4, H=64, out=FAKE, x=FAKE):
+        return lib.moe_add_norm(r, rt, dl, dt, 1.0, w, wt, 1e-6, T, H, out, x, None)
+
+    for bad in (dict(rt=2), dict(rt=0), dict(dt=2), dict(wt=2), dict(wt=9)):
+        assert add(**bad) == UNSUPPORTED, bad
+    for bad in (dict(T=-1), dict(H=48), dict(H=0), dict(r=None), dict(r=ODD), dict(dl=ODD),
+                dict(w=None), dict(x=None), dict(out=None), dict(out=ODD)):
+        assert add(**bad) == INVALID, bad
+    assert add(T=0, r=None, w=None, x=None, out=None) == OK
+
+    def comb(y=FAKE, ip=FAKE, w=FAKE, T=4, k=2, H=64, r=FAKE, rt=1, post=None, gate=None, gr=1,
+             nw=FAKE, wt=1, out=FAKE, x=FAKE):
+        return lib.moe_combine_norm(y, ip, w, T, k, H, r, rt, post, gate, gr, 1.0, nw, wt, 1e-6,
+                                    out, x, None)
+
+    assert comb(rt=2) == UNSUPPORTED and comb(wt=2) == UNSUPPORTED
+    for bad in (dict(T=-1), dict(H=33), dict(k=0), dict(k=9), dict(y=None), dict(y=ODD),
+                dict(ip=None), dict(w=None), dict(r=None), dict(out=None), dict(x=None),
+                dict(nw=None), dict(post=ODD), dict(gate=ODD), dict(gate=FAKE, gr=2),
+                dict(gate=FAKE, gr=0), dict(nw=ODD)):
+        assert comb(**bad) == INVALID, bad
+        assert lib.moe_last_error()
+    assert comb(T=0, y=None, ip=None, r=None) == OK
+
+
+def test_binding_refuses_host_tensors():
+    torch = pytest.importorskip("torch")
+    import quantized_routed_expert_gemv_amd as qm
+    x = torch.zeros(4, 64)
+    with pytest.raises(ValueError):
+        qm.mx_quantize(x)
+    with pytest.raises(ValueError):
+        qm.mx_quantize(x, "mxfp8")
+    with pytest.raises(ValueError):
+        qm.add_norm(x, x[0])
+    with pytest.raises(TypeError):
+        qm.add_norm(x.half(), x[0])
+    with pytest.raises(TypeError):
+        qm.mx_quantize(x.double())
+    with pytest.raises(ValueError):
+        qm.mx_dequantize(torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.uint8))
