@@ -173,12 +173,285 @@ hipError_t launch_gemv_t(const MxProduct& p, hipStream_t st) {
   return hipGetLastError();
 }
 
+constexpr int kGemmThreads = 256;
+constexpr int kGemmCols = 256;   // weight rows a tile (gated: half of them gate, half up)
+constexpr int kStepBlocks = 4;   // blocks of K a step: two matrix instructions deep
+
+typedef float v16f __attribute__((__vector_size__(64)));
+
+// 32 weight rows x 64 K  times  64 K x 32 columns. Lane l holds block l / 32 of weight row and
+// of column l % 32; element v of the result is row 8 (v / 4) + 4 (l / 32) + v % 4 of column
+// l % 32. AB: byte of `as` that holds the column's scale.
+template <int FMT, int AB>
+__device__ __forceinline__ v16f mma32(v8i w, uint32_t ws, v8i a, uint32_t as, v16f c) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, a, c, 4, kOperand<FMT>, 0, (int)ws, AB,
+                                                         (int)as);
+}
+
+// Where block b of tile row r lies among the row's kStepBlocks blocks in LDS, such that the 16
+// lanes of each pass of a 64-lane read (32 rows, one block each) touch different banks: a
+// 64-byte row (MXFP4, 16-byte reads) repeats its banks every 4 rows, a 96-byte row (MXFP6,
+// 8-byte reads) every 8.
+template <int FMT>
+__device__ __forceinline__ int lds_place(int r, int b) {
+  return FMT == kMxFp4 ? b ^ ((r >> 2) & 3) : (b + (r >> 3)) & 3;
+}
+
+// A block's codes as they travel from memory to LDS.
+template <int FMT> struct Codes;
+template <> struct Codes<kMxFp4> {
+  u32x4 v;
+  __device__ __forceinline__ void load(const uint8_t* p, bool ok) {
+    v = *(const u32x4*)p;
+    v = ok ? v : u32x4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ void store(uint8_t* p) const { *(u32x4*)p = v; }
+};
+template <> struct Codes<kMxFp6> {
+  u32x2 v[3];
+  __device__ __forceinline__ void load(const uint8_t* p, bool ok) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      v[i] = ((const u32x2*)p)[i];
+      v[i] = ok ? v[i] : u32x2{0, 0};
+    }
+  }
+  __device__ __forceinline__ void store(uint8_t* p) const {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) ((u32x2*)p)[i] = v[i];
+  }
+};
+
+// The expert and first bucket position of row tile mt (tiles of bm rows, expert by expert);
+// false past the last one.
+__device__ bool find_tile(const MxProduct& p, int bm, int mt, int* e, int* m0, int* mend,
+                          int* part, int* found) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  int lo = 0, hi = 0;
+  if ((int)threadIdx.x < p.E) bucket_range(p.offsets, threadIdx.x, p.T * p.k, &lo, &hi);
+  const int nt = (hi - lo + bm - 1) / bm;
+  int end = nt;   // inclusive scan of nt
+#pragma unroll
+  for (int m = 1; m < kWave; m <<= 1) {
+    const int o = __shfl_up(end, m, kWave);
+    if (lane >= m) end += o;
+  }
+  if (lane == kWave - 1) part[wave] = end;
+  if (threadIdx.x == 0) found[0] = -1;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) end += part[w];
+  if (mt < end && mt >= end - nt) {
+    found[0] = threadIdx.x;
+    found[1] = lo + (mt - (end - nt)) * bm;
+    found[2] = hi;
+  }
+  __syncthreads();
+  *e = found[0];
+  *m0 = found[1];
+  *mend = found[2];
+  return *e >= 0;
+}
+
+// Many rows: tiles of 32 MF bucket rows x 256 weight rows; 4 waves, each all rows by 64 weight
+// rows (gated: 32 gate and the same 32 up, so SwiGLU stays in registers). Weight blocks go
+// from the pool straight to the registers of the one wave that uses them (the pool's unit
+// order is the operand's); the gathered rows are shared by the waves and pass through LDS.
+// Both are loaded one step of 128 K ahead.
+template <int FMT, bool GATED, int MF>
+__global__ __launch_bounds__(kGemmThreads, 2) void k_mx_gemm(MxProduct p, int n_mtiles, int n_ntiles) {
+  constexpr int BM = 32 * MF;
+  constexpr int TN = GATED ? kGemmCols / 2 : kGemmCols;   // output columns a tile
+  constexpr int kBytes = mx_block_bytes(FMT);
+  constexpr int NB = BM * kStepBlocks / kGemmThreads;   // row blocks a thread loads a step
+  static_assert(NB >= 1, "a thread loads whole blocks");
+  __shared__ __attribute__((aligned(16))) uint8_t lds_q[2][BM * kStepBlocks * kBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t lds_s[2][BM * kStepBlocks];
+  __shared__ int part[kGemmThreads / kWave];
+  __shared__ int found[3];
+  // XCD-aware tile order, as the bf16 grouped GEMM: workgroups go to the 8 XCDs in turn, and
+  // each XCD gets runs of 64 tiles of 8 x 8 super-tiles, which share their rows in its L2
+  const int xcd = blockIdx.x & 7, local = blockIdx.x >> 3;
+  const int64_t i = (int64_t)(local >> 6) * 512 + xcd * 64 + (local & 63);
+  if (i >= (int64_t)n_mtiles * n_ntiles) return;
+  const int sr = (int)(i / (8LL * n_ntiles));
+  const int sh = min(8, n_mtiles - 8 * sr);
+  const int sj = (int)(i - 8LL * n_ntiles * sr);
+  const int sc = sj / (8 * sh);
+  const int sw = min(8, n_ntiles - 8 * sc);
+  const int sk = sj - 8 * sh * sc;
+  const int mt = 8 * sr + sk / sw, nt = 8 * sc + sk % sw;
+  int e, m0, mend;
+  if (!find_tile(p, BM, mt, &e, &m0, &mend, part, found)) return;
+  const int n0 = nt * TN;
+  const int slot = p.slot_map[e];
+  if (slot < 0 || slot >= p.n_slots) {
+    for (int t = threadIdx.x; t < BM * TN; t += kGemmThreads) {
+      const int pos = m0 + t / TN, n = n0 + t % TN;
+      if (pos < mend && n < p.N) {
+        if (GATED) p.h[(int64_t)pos * p.N + n] = 0;
+        else p.y[(int64_t)pos * p.N + n] = 0.f;
+      }
+    }
+    if (threadIdx.x == 0 && p.err && slot != kSlotMiss) atomicOr(p.err, 1u);
+    return;
+  }
+  const int nb = p.K / kBlock;
+  const int nsteps = (nb + kStepBlocks - 1) / kStepBlocks;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int half = lane >> 5;
+
+  // ---- rows: thread t carries block t % 4 of tile rows t / 4 and, 64 further on, t / 4 + 64
+  const int rb = threadIdx.x & 3;
+  const uint8_t* rq[NB];
+  const uint8_t* rs[NB];
+  int place[NB], splace[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const int r = (threadIdx.x >> 2) + 64 * j;
+    const int64_t row = source_row<GATED>(p, min(m0 + r, mend - 1));   // past the end: the last
+    rq[j] = p.q + (row * nb + rb) * kBytes;
+    rs[j] = p.s + row * nb + rb;
+    place[j] = (r * kStepBlocks + lds_place<FMT>(r, rb)) * kBytes;
+    splace[j] = r * kStepBlocks + rb;
+  }
+  // ---- weights: fragment f is 32 rows from col[f] on; lane l holds row l % 32
+  int col[2];
+  const uint8_t* wq[2];
+  const uint8_t* ws[2];
+#pragma unroll
+  for (int f = 0; f < 2; ++f) {
+    col[f] = GATED ? n0 + 32 * wave : n0 + 64 * wave + 32 * f;
+    const int r = (col[f] < p.N ? col[f] : 0) + (lane & 31);   // never stored past N
+    const PoolView& m = GATED && f ? p.b : p.a;
+    const int64_t u = pool_unit(r, 0, nb);
+    wq[f] = m.q + slot * m.q_slot + u * 16;
+    ws[f] = m.s + slot * m.s_slot + u;
+  }
+  struct Stage {
+    Codes<FMT> q[NB];
+    uint32_t s[NB];
+    u32x4 w[2][2];
+    uint32_t ws[2][2];
+  };
+  auto load = [&](int c, Stage& g) {
+    const bool ok = kStepBlocks * c + rb < nb;
+    const int64_t at = ok ? (int64_t)kStepBlocks * c : -rb;   // past the row: its first block
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      g.q[j].load(rq[j] + at * kBytes, ok);
+      const uint32_t sb = rs[j][at];
+      g.s[j] = ok ? sb : kOne;
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int b = kStepBlocks * c + 2 * s + half;
+      const bool in = b < nb;      // past the row the other operand's codes are zeros
+      const int64_t u = (int64_t)(in ? b : 0) * kRowGroup;
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        g.w[f][s] = *(const u32x4*)(wq[f] + u * 16);
+        const uint32_t sb = ws[f][u];
+        g.ws[f][s] = in ? sb : kOne;
+      }
+    }
+  };
+  auto put = [&](const Stage& g, int buf) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      g.q[j].store(lds_q[buf] + place[j]);
+      lds_s[buf][splace[j]] = (uint8_t)g.s[j];
+    }
+  };
+  v16f acc[MF][2];
+#pragma unroll
+  for (int m = 0; m < MF; ++m)
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[m][f][v] = 0.f;
+  Stage cur, nxt;
+  load(0, cur);
+  put(cur, 0);
+  __syncthreads();
+  for (int c = 0; c < nsteps; ++c) {
+    const int buf = c & 1;
+    if (c + 1 < nsteps) load(c + 1, nxt);
+    uint32_t as[MF];
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+      as[m] = *(const uint32_t*)(lds_s[buf] + (32 * m + (lane & 31)) * kStepBlocks) >> (8 * half);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int m = 0; m < MF; ++m) {
+        const int r = 32 * m + (lane & 31);
+        const v8i a = load_block<FMT>(
+            lds_q[buf] + (r * kStepBlocks + lds_place<FMT>(r, 2 * s + half)) * kBytes, true);
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const v8i w = {(int)cur.w[f][s][0], (int)cur.w[f][s][1], (int)cur.w[f][s][2],
+                         (int)cur.w[f][s][3], 0, 0, 0, 0};
+          acc[m][f] = s ? mma32<FMT, 2>(w, cur.ws[f][s], a, as[m], acc[m][f])
+                        : mma32<FMT, 0>(w, cur.ws[f][s], a, as[m], acc[m][f]);
+        }
+      }
+    }
+    if (c + 1 < nsteps) put(nxt, buf ^ 1);
+    __syncthreads();
+    cur = nxt;
+  }
+  // ---- a lane holds, of one bucket row, 4 groups of 4 neighbouring columns a fragment
+#pragma unroll
+  for (int m = 0; m < MF; ++m) {
+    const int pos = m0 + 32 * m + (lane & 31);
+    if (pos >= mend) continue;
+#pragma unroll
+    for (int f = 0; f < (GATED ? 1 : 2); ++f) {
+      if (col[f] >= p.N) continue;
+      const int64_t o = (int64_t)pos * p.N + col[f] + 4 * half;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        f32x4 v;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) v[t] = acc[m][f][4 * q + t];
+        if constexpr (GATED) {
+          float z[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) z[t] = silu_mul(v[t], acc[m][1][4 * q + t]);
+          *(u32x2*)(p.h + o + 8 * q) = u32x2{pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3])};
+        } else {
+          __builtin_nontemporal_store(v, (f32x4*)(p.y + o + 8 * q));
+        }
+      }
+    }
+  }
+}
+
+template <int FMT, bool GATED, int MF>
+hipError_t launch_gemm_t(const MxProduct& p, hipStream_t st) {
+  constexpr int BM = 32 * MF, TN = GATED ? kGemmCols / 2 : kGemmCols;
+  const int pairs = p.T * p.k;
+  const int n_mtiles = (pairs + BM - 1) / BM + min(p.E, pairs);   // most that can be
+  const int n_ntiles = (p.N + TN - 1) / TN;
+  const int64_t grid = ((int64_t)n_mtiles * n_ntiles + 511) / 512 * 512;
+  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((k_mx_gemm<FMT, GATED, MF>), dim3((unsigned)grid), dim3(kGemmThreads), 0, st, p,
+                     n_mtiles, n_ntiles);
+  return hipGetLastError();
+}
+
+template <int FMT, bool GATED>
+hipError_t launch_t(const MxProduct& p, bool gemv, hipStream_t st) {
+  if (gemv) return launch_gemv_t<FMT, GATED>(p, st);
+  return launch_gemm_t<FMT, GATED, 4>(p, st);
+}
+
 }  // namespace
 
 hipError_t launch_mx_product(const MxProduct& p, int fmt, bool gated, bool gemv, hipStream_t st) {
-  (void)gemv;
-  if (fmt == kMxFp4) return gated ? launch_gemv_t<kMxFp4, true>(p, st) : launch_gemv_t<kMxFp4, false>(p, st);
-  return gated ? launch_gemv_t<kMxFp6, true>(p, st) : launch_gemv_t<kMxFp6, false>(p, st);
+  if (fmt == kMxFp4) return gated ? launch_t<kMxFp4, true>(p, gemv, st) : launch_t<kMxFp4, false>(p, gemv, st);
+  return gated ? launch_t<kMxFp6, true>(p, gemv, st) : launch_t<kMxFp6, false>(p, gemv, st);
 }
 
 }  // namespace moe
