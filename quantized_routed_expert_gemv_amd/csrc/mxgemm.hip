@@ -5,6 +5,8 @@
 // scale bytes as they lie in memory and accumulates in fp32, so nothing is widened. A lane
 // holds one block of 32 of one row; the pool's unit order is that of a wave's lanes.
 // E2M1 and E2M3 operands run at the same rate, twice E4M3's.
+#include <type_traits>
+
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -198,27 +200,17 @@ __device__ __forceinline__ int lds_place(int r, int b) {
 }
 
 // A block's codes as they travel from memory to LDS.
-template <int FMT> struct Codes;
-template <> struct Codes<kMxFp4> {
-  u32x4 v;
-  __device__ __forceinline__ void load(const uint8_t* p, bool ok) {
-    v = *(const u32x4*)p;
-    v = ok ? v : u32x4{0, 0, 0, 0};
-  }
-  __device__ __forceinline__ void store(uint8_t* p) const { *(u32x4*)p = v; }
-};
-template <> struct Codes<kMxFp6> {
-  u32x2 v[3];
-  __device__ __forceinline__ void load(const uint8_t* p, bool ok) {
+template <int FMT> struct Codes {
+  static constexpr int kParts = FMT == kMxFp4 ? 1 : 3;
+  typedef std::conditional_t<FMT == kMxFp4, u32x4, u32x2> Part;
+  Part v[kParts];
+  __device__ __forceinline__ void load(const uint8_t* p) {
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      v[i] = ((const u32x2*)p)[i];
-      v[i] = ok ? v[i] : u32x2{0, 0};
-    }
+    for (int i = 0; i < kParts; ++i) v[i] = ((const Part*)p)[i];
   }
-  __device__ __forceinline__ void store(uint8_t* p) const {
+  __device__ __forceinline__ void store(uint8_t* p, bool ok) const {   // zeros where !ok
 #pragma unroll
-    for (int i = 0; i < 3; ++i) ((u32x2*)p)[i] = v[i];
+    for (int i = 0; i < kParts; ++i) ((Part*)p)[i] = ok ? v[i] : Part{};
   }
 };
 
@@ -334,33 +326,33 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_mx_gemm(MxProduct p, int n_
     u32x4 w[2][2];
     uint32_t ws[2][2];
   };
+  // Loads only: nothing here may wait for them. Blocks past the row read a block of it; their
+  // codes and scale are replaced when they are put in LDS, and zero codes there are enough.
   auto load = [&](int c, Stage& g) {
-    const bool ok = kStepBlocks * c + rb < nb;
-    const int64_t at = ok ? (int64_t)kStepBlocks * c : -rb;   // past the row: its first block
+    const int64_t at = kStepBlocks * c + rb < nb ? (int64_t)kStepBlocks * c : -rb;
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      g.q[j].load(rq[j] + at * kBytes, ok);
-      const uint32_t sb = rs[j][at];
-      g.s[j] = ok ? sb : kOne;
+      g.q[j].load(rq[j] + at * kBytes);
+      g.s[j] = rs[j][at];
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const int b = kStepBlocks * c + 2 * s + half;
-      const bool in = b < nb;      // past the row the other operand's codes are zeros
-      const int64_t u = (int64_t)(in ? b : 0) * kRowGroup;
+      const int64_t u = (int64_t)(b < nb ? b : 0) * kRowGroup;
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
         g.w[f][s] = *(const u32x4*)(wq[f] + u * 16);
-        const uint32_t sb = ws[f][u];
-        g.ws[f][s] = in ? sb : kOne;
+        g.ws[f][s] = ws[f][u];
       }
     }
   };
-  auto put = [&](const Stage& g, int buf) {
+  auto put = [&](const Stage& g, int c) {
+    const bool ok = kStepBlocks * c + rb < nb;
+    const int buf = c & 1;
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      g.q[j].store(lds_q[buf] + place[j]);
-      lds_s[buf][splace[j]] = (uint8_t)g.s[j];
+      g.q[j].store(lds_q[buf] + place[j], ok);
+      lds_s[buf][splace[j]] = (uint8_t)(ok ? g.s[j] : kOne);
     }
   };
   v16f acc[MF][2];
@@ -377,6 +369,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_mx_gemm(MxProduct p, int n_
   for (int c = 0; c < nsteps; ++c) {
     const int buf = c & 1;
     if (c + 1 < nsteps) load(c + 1, nxt);
+    __builtin_amdgcn_sched_barrier(0);   // the loads go first, what waits for them last
     uint32_t as[MF];
 #pragma unroll
     for (int m = 0; m < MF; ++m)
@@ -397,7 +390,8 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_mx_gemm(MxProduct p, int n_
         }
       }
     }
-    if (c + 1 < nsteps) put(nxt, buf ^ 1);
+    __builtin_amdgcn_sched_barrier(0);
+    if (c + 1 < nsteps) put(nxt, c + 1);
     __syncthreads();
     cur = nxt;
   }
