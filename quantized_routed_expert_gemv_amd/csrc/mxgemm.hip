@@ -177,7 +177,11 @@ hipError_t launch_gemv_t(const MxProduct& p, hipStream_t st) {
 
 constexpr int kGemmThreads = 256;
 constexpr int kGemmCols = 256;   // weight rows a tile (gated: half of them gate, half up)
-constexpr int kStepBlocks = 4;   // blocks of K a step: two matrix instructions deep
+constexpr int kMF = 4;
+constexpr int kStepBlocks = 8;    // blocks of K a step: four matrix instructions deep
+constexpr int kSlices = kStepBlocks / 2;
+constexpr int kScaleBlocks = 128;              // blocks of K whose row scales lie in LDS at once
+constexpr int kScaleRow = kScaleBlocks + 8;    // bytes between rows: 34 dwords, bank by bank
 
 typedef float v16f __attribute__((__vector_size__(64)));
 
@@ -190,13 +194,13 @@ __device__ __forceinline__ v16f mma32(v8i w, uint32_t ws, v8i a, uint32_t as, v1
                                                          (int)as);
 }
 
-// Where block b of tile row r lies among the row's kStepBlocks blocks in LDS, such that the 16
-// lanes of each pass of a 64-lane read (32 rows, one block each) touch different banks: a
-// 64-byte row (MXFP4, 16-byte reads) repeats its banks every 4 rows, a 96-byte row (MXFP6,
-// 8-byte reads) every 8.
+// Where block b of tile row r lies among the row's kStepBlocks blocks in LDS, such that the
+// lanes of each pass of a 64-lane read (one block of 32 rows and the next of the same) touch
+// different banks: MXFP4's 128-byte rows repeat their banks every 2 rows, MXFP6's 192-byte
+// rows every 4.
 template <int FMT>
 __device__ __forceinline__ int lds_place(int r, int b) {
-  return FMT == kMxFp4 ? b ^ ((r >> 2) & 3) : (b + (r >> 3)) & 3;
+  return b ^ ((FMT == kMxFp4 ? r >> 1 : r >> 2) & 7);
 }
 
 // A block's codes as they travel from memory to LDS.
@@ -247,8 +251,10 @@ __device__ bool find_tile(const MxProduct& p, int bm, int mt, int* e, int* m0, i
 // Many rows: tiles of 32 MF bucket rows x 256 weight rows; 4 waves, each all rows by 64 weight
 // rows (gated: 32 gate and the same 32 up, so SwiGLU stays in registers). Weight blocks go
 // from the pool straight to the registers of the one wave that uses them (the pool's unit
-// order is the operand's); the gathered rows are shared by the waves and pass through LDS.
-// Both are loaded one step of 128 K ahead.
+// order is the operand's); the gathered rows are shared by the waves and pass through
+// registers to one of two LDS buffers. Both are loaded one step of 256 K ahead: a row's 128
+// bytes of MXFP4 codes are then one whole cache line, where half steps asked L2 for every
+// line twice. Row scales, one byte a block, come 128 blocks at a time for the same reason.
 template <int FMT, bool GATED, int MF>
 __global__ __launch_bounds__(kGemmThreads, 2) void k_mx_gemm(MxProduct p, int n_mtiles, int n_ntiles) {
   constexpr int BM = 32 * MF;
@@ -257,7 +263,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_mx_gemm(MxProduct p, int n_
   constexpr int NB = BM * kStepBlocks / kGemmThreads;   // row blocks a thread loads a step
   static_assert(NB >= 1, "a thread loads whole blocks");
   __shared__ __attribute__((aligned(16))) uint8_t lds_q[2][BM * kStepBlocks * kBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t lds_s[2][BM * kStepBlocks];
+  __shared__ __attribute__((aligned(16))) uint8_t lds_s[BM * kScaleRow];
   __shared__ int part[kGemmThreads / kWave];
   __shared__ int found[3];
   // XCD-aware tile order, as the bf16 grouped GEMM: workgroups go to the 8 XCDs in turn, and
@@ -293,19 +299,16 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_mx_gemm(MxProduct p, int n_
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int half = lane >> 5;
 
-  // ---- rows: thread t carries block t % 4 of tile rows t / 4 and, 64 further on, t / 4 + 64
-  const int rb = threadIdx.x & 3;
+  // ---- rows: thread t carries block t % 8 of tile rows t / 8 + 32 j
+  const int rb = threadIdx.x & (kStepBlocks - 1);
   const uint8_t* rq[NB];
-  const uint8_t* rs[NB];
-  int place[NB], splace[NB];
+  int place[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
-    const int r = (threadIdx.x >> 2) + 64 * j;
+    const int r = threadIdx.x / kStepBlocks + kGemmThreads / kStepBlocks * j;
     const int64_t row = source_row<GATED>(p, min(m0 + r, mend - 1));   // past the end: the last
-    rq[j] = p.q + (row * nb + rb) * kBytes;
-    rs[j] = p.s + row * nb + rb;
+    rq[j] = p.q + row * nb * kBytes;
     place[j] = (r * kStepBlocks + lds_place<FMT>(r, rb)) * kBytes;
-    splace[j] = r * kStepBlocks + rb;
   }
   // ---- weights: fragment f is 32 rows from col[f] on; lane l holds row l % 32
   int col[2];
@@ -314,47 +317,61 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_mx_gemm(MxProduct p, int n_
 #pragma unroll
   for (int f = 0; f < 2; ++f) {
     col[f] = GATED ? n0 + 32 * wave : n0 + 64 * wave + 32 * f;
-    const int r = (col[f] < p.N ? col[f] : 0) + (lane & 31);   // never stored past N
+    const int c0 = col[f] < p.N ? col[f] : 0;   // never stored past N
     const PoolView& m = GATED && f ? p.b : p.a;
-    const int64_t u = pool_unit(r, 0, nb);
+    const int64_t u = pool_unit(c0, 0, nb);
     wq[f] = m.q + slot * m.q_slot + u * 16;
     ws[f] = m.s + slot * m.s_slot + u;
   }
-  struct Stage {
-    Codes<FMT> q[NB];
-    uint32_t s[NB];
-    u32x4 w[2][2];
-    uint32_t ws[2][2];
+  const uint32_t wlane = (uint32_t)((lane & 31) >> 4) * nb * kRowGroup + (lane & 15);   // unit
+  // Loads: nothing here may wait for them. A block past the row reads the row's last; its
+  // codes are replaced by zeros when they are put in LDS, which is enough on one side.
+  Codes<FMT> rows[NB];
+  auto load_rows = [&](int c) {
+    const int b = min(kStepBlocks * c + rb, nb - 1);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) rows[j].load(rq[j] + (uint32_t)b * kBytes);
   };
-  // Loads only: nothing here may wait for them. Blocks past the row read a block of it; their
-  // codes and scale are replaced when they are put in LDS, and zero codes there are enough.
-  auto load = [&](int c, Stage& g) {
-    const int64_t at = kStepBlocks * c + rb < nb ? (int64_t)kStepBlocks * c : -rb;
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      g.q[j].load(rq[j] + at * kBytes);
-      g.s[j] = rs[j][at];
-    }
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int b = kStepBlocks * c + 2 * s + half;
-      const int64_t u = (int64_t)(b < nb ? b : 0) * kRowGroup;
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        g.w[f][s] = *(const u32x4*)(wq[f] + u * 16);
-        g.ws[f][s] = ws[f][u];
-      }
-    }
-  };
-  auto put = [&](const Stage& g, int c) {
+  auto put = [&](int c) {
     const bool ok = kStepBlocks * c + rb < nb;
-    const int buf = c & 1;
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      g.q[j].store(lds_q[buf] + place[j], ok);
-      lds_s[buf][splace[j]] = (uint8_t)(ok ? g.s[j] : kOne);
+    for (int j = 0; j < NB; ++j) rows[j].store(lds_q[c & 1] + place[j], ok);
+  };
+  u32x4 wgt[2][kSlices];
+  uint32_t wsc[2][kSlices];
+  auto load_weights = [&](int c, int s) {
+    const uint32_t u = wlane + (uint32_t)min(kStepBlocks * c + 2 * s + half, nb - 1) * kRowGroup;
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      wgt[f][s] = *(const u32x4*)(wq[f] + u * 16);
+      wsc[f][s] = ws[f][u];
     }
   };
+  // Row scales of blocks b0 .. b0 + kScaleBlocks - 1, and ones past the row: each thread takes
+  // every kParts-th dword of its row. The rows lie at any byte, so a row's last dword is
+  // gathered byte by byte.
+  auto load_scales = [&](int b0) {
+    constexpr int kParts = kGemmThreads / BM;
+    const int r = threadIdx.x / kParts;
+    const uint8_t* src = p.s + (int64_t)source_row<GATED>(p, min(m0 + r, mend - 1)) * nb + b0;
+    const int n = min(nb - b0, kScaleBlocks);
+    uint32_t* dst = (uint32_t*)(lds_s + r * kScaleRow);
+#pragma unroll 8
+    for (int d = threadIdx.x % kParts; d < kScaleBlocks / 4; d += kParts) {
+      uint32_t v = kOne * 0x01010101u;
+      if (4 * d + 4 <= n) {
+        __builtin_memcpy(&v, src + 4 * d, 4);
+      } else {
+        for (int i = 0; 4 * d + i < n; ++i)
+          v = (v & ~(0xFFu << (8 * i))) | (uint32_t)src[4 * d + i] << (8 * i);
+      }
+      dst[d] = v;
+    }
+  };
+  int rplace[kSlices];   // where the lane reads its blocks of the first 32 rows
+#pragma unroll
+  for (int s = 0; s < kSlices; ++s)
+    rplace[s] = ((lane & 31) * kStepBlocks + lds_place<FMT>(lane & 31, 2 * s + half)) * kBytes;
   v16f acc[MF][2];
 #pragma unroll
   for (int m = 0; m < MF; ++m)
@@ -362,38 +379,47 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_mx_gemm(MxProduct p, int n_
     for (int f = 0; f < 2; ++f)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[m][f][v] = 0.f;
-  Stage cur, nxt;
-  load(0, cur);
-  put(cur, 0);
-  __syncthreads();
+  load_rows(0);
+#pragma unroll
+  for (int s = 0; s < kSlices; ++s) load_weights(0, s);
+  put(0);
   for (int c = 0; c < nsteps; ++c) {
-    const int buf = c & 1;
-    if (c + 1 < nsteps) load(c + 1, nxt);
+    const int sb = kStepBlocks * c % kScaleBlocks;
+    if (sb == 0) {
+      load_scales(kStepBlocks * c);
+      __syncthreads();
+    }
+    if (c + 1 < nsteps) load_rows(c + 1);
     __builtin_amdgcn_sched_barrier(0);   // the loads go first, what waits for them last
-    uint32_t as[MF];
+    u32x2 as[MF];
 #pragma unroll
     for (int m = 0; m < MF; ++m)
-      as[m] = *(const uint32_t*)(lds_s[buf] + (32 * m + (lane & 31)) * kStepBlocks) >> (8 * half);
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
+      as[m] = *(const u32x2*)(lds_s + (32 * m + (lane & 31)) * kScaleRow + sb) >> (uint32_t)(8 * half);
+    auto slice = [&](auto sl) {
+      constexpr int s = decltype(sl)::value;
 #pragma unroll
       for (int m = 0; m < MF; ++m) {
-        const int r = 32 * m + (lane & 31);
         const v8i a = load_block<FMT>(
-            lds_q[buf] + (r * kStepBlocks + lds_place<FMT>(r, 2 * s + half)) * kBytes, true);
+            lds_q[c & 1] + rplace[s] + m * 32 * kStepBlocks * kBytes, true);
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-          const v8i w = {(int)cur.w[f][s][0], (int)cur.w[f][s][1], (int)cur.w[f][s][2],
-                         (int)cur.w[f][s][3], 0, 0, 0, 0};
-          acc[m][f] = s ? mma32<FMT, 2>(w, cur.ws[f][s], a, as[m], acc[m][f])
-                        : mma32<FMT, 0>(w, cur.ws[f][s], a, as[m], acc[m][f]);
+          const v8i w = {(int)wgt[f][s][0], (int)wgt[f][s][1], (int)wgt[f][s][2],
+                         (int)wgt[f][s][3], 0, 0, 0, 0};
+          acc[m][f] = mma32<FMT, 2 * (s & 1)>(w, wsc[f][s], a, as[m][s >> 1], acc[m][f]);
         }
       }
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    if (c + 1 < nsteps) put(nxt, c + 1);
+      // the products stay in their slice, and one slice's operands at a time in registers:
+      // without this the compiler reads every slice's first and spills
+#pragma unroll
+      for (int m = 0; m < MF; ++m) asm volatile("" : "+v"(acc[m][0]), "+v"(acc[m][1]));
+      load_weights(min(c + 1, nsteps - 1), s);
+    };
+    slice(std::integral_constant<int, 0>{});
+    slice(std::integral_constant<int, 1>{});
+    slice(std::integral_constant<int, 2>{});
+    slice(std::integral_constant<int, 3>{});
+    if (c + 1 < nsteps) put(c + 1);
     __syncthreads();
-    cur = nxt;
   }
   // ---- a lane holds, of one bucket row, 4 groups of 4 neighbouring columns a fragment
 #pragma unroll
@@ -438,7 +464,7 @@ hipError_t launch_gemm_t(const MxProduct& p, hipStream_t st) {
 template <int FMT, bool GATED>
 hipError_t launch_t(const MxProduct& p, bool gemv, hipStream_t st) {
   if (gemv) return launch_gemv_t<FMT, GATED>(p, st);
-  return launch_gemm_t<FMT, GATED, 4>(p, st);
+  return launch_gemm_t<FMT, GATED, kMF>(p, st);
 }
 
 }  // namespace
