@@ -344,7 +344,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_mx_gemm(MxProduct p, int n_
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
       wgt[f][s] = *(const u32x4*)(wq[f] + u * 16);
-      wsc[f][s] = ws[f][u];
+      wsc[f][s] = *(const uint32_t*)(ws[f] + (u & ~3u));   // the scales of 4 rows
     }
   };
   // Row scales of blocks b0 .. b0 + kScaleBlocks - 1, and ones past the row: each thread takes
@@ -397,6 +397,12 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_mx_gemm(MxProduct p, int n_
       as[m] = *(const u32x2*)(lds_s + (32 * m + (lane & 31)) * kScaleRow + sb) >> (uint32_t)(8 * half);
     auto slice = [&](auto sl) {
       constexpr int s = decltype(sl)::value;
+      uint32_t sw[2];
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        asm volatile("" : "+v"(wsc[f][s]));   // waited for here, not where the step begins
+        sw[f] = wsc[f][s] >> (8 * (lane & 3));
+      }
 #pragma unroll
       for (int m = 0; m < MF; ++m) {
         const v8i a = load_block<FMT>(
@@ -405,7 +411,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_mx_gemm(MxProduct p, int n_
         for (int f = 0; f < 2; ++f) {
           const v8i w = {(int)wgt[f][s][0], (int)wgt[f][s][1], (int)wgt[f][s][2],
                          (int)wgt[f][s][3], 0, 0, 0, 0};
-          acc[m][f] = mma32<FMT, 2 * (s & 1)>(w, wsc[f][s], a, as[m][s >> 1], acc[m][f]);
+          acc[m][f] = mma32<FMT, 2 * (s & 1)>(w, sw[f], a, as[m][s >> 1], acc[m][f]);
         }
       }
       // the products stay in their slice, and one slice's operands at a time in registers:
