@@ -218,6 +218,13 @@ template <int FMT> struct Codes {
   }
 };
 
+// Orders the LDS accesses of a wave's lanes against each other (the wave runs them in order).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // The expert and first bucket position of row tile mt (tiles of bm rows, expert by expert);
 // false past the last one.
 __device__ bool find_tile(const MxProduct& p, int bm, int mt, int* e, int* m0, int* mend,
@@ -427,29 +434,46 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_mx_gemm(MxProduct p, int n_
     if (c + 1 < nsteps) put(c + 1);
     __syncthreads();
   }
-  // ---- a lane holds, of one bucket row, 4 groups of 4 neighbouring columns a fragment
+  // ---- a lane holds, of one bucket row, 4 groups of 4 neighbouring columns a fragment; each
+  // wave turns its fragments round in LDS of its own (the rows' buffers, no longer read), so
+  // that the stores are whole cache lines of a row (gated: halves) and not 16-byte pieces
+  constexpr int kPiece = GATED ? 2 : 4;                    // bytes of an output
+  constexpr int kOutRow = 32 * kPiece + 16;                // padded: no bank conflicts
+  constexpr int kLanesRow = 32 * kPiece / 16;              // lanes that store one row
+  static_assert(4 * 32 * kOutRow <= sizeof(lds_q), "the fragments fit");
+  uint8_t* turn = lds_q[0] + wave * 32 * kOutRow;
+  uint8_t* out = GATED ? (uint8_t*)p.h : (uint8_t*)p.y;
 #pragma unroll
   for (int m = 0; m < MF; ++m) {
-    const int pos = m0 + 32 * m + (lane & 31);
-    if (pos >= mend) continue;
 #pragma unroll
     for (int f = 0; f < (GATED ? 1 : 2); ++f) {
       if (col[f] >= p.N) continue;
-      const int64_t o = (int64_t)pos * p.N + col[f] + 4 * half;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         f32x4 v;
 #pragma unroll
         for (int t = 0; t < 4; ++t) v[t] = acc[m][f][4 * q + t];
+        uint8_t* to = turn + (lane & 31) * kOutRow + (8 * q + 4 * half) * kPiece;
         if constexpr (GATED) {
           float z[4];
 #pragma unroll
           for (int t = 0; t < 4; ++t) z[t] = silu_mul(v[t], acc[m][1][4 * q + t]);
-          *(u32x2*)(p.h + o + 8 * q) = u32x2{pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3])};
+          *(u32x2*)to = u32x2{pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3])};
         } else {
-          __builtin_nontemporal_store(v, (f32x4*)(p.y + o + 8 * q));
+          *(f32x4*)to = v;
         }
       }
+      wave_sync();
+#pragma unroll
+      for (int j = 0; j < kLanesRow / 2; ++j) {
+        const int r = j * (kWave / kLanesRow) + lane / kLanesRow;
+        const int pos = m0 + 32 * m + r;
+        const u32x4 v = *(const u32x4*)(turn + r * kOutRow + lane % kLanesRow * 16);
+        if (pos < mend)
+          __builtin_nontemporal_store(
+              v, (u32x4*)(out + ((int64_t)pos * p.N + col[f]) * kPiece + lane % kLanesRow * 16));
+      }
+      wave_sync();
     }
   }
 }
