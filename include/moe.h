@@ -425,8 +425,9 @@ moe_status moe_mx_dequantize(const void* q, const uint8_t* s, int32_t fmt, int32
  *            bucket position pos
  *   h_q, h_s planes of T*k rows of I values in bucket order, in h_fmt
  *   h        bf16 [T*k][I] (out) = bf16_RNE(silu(g) * u);  y fp32 [T*k][H] (out)
- *   offsets, perm as from moe_bucket; slot_map, err_flags and path as in moe_expert_ffn. Rows
- *   past offsets[E] are left as they are.
+ *   offsets, perm as from moe_bucket; slot_map, err_flags and path as in moe_expert_ffn, except
+ *   that AUTO picks the GEMV schedule for T <= 16 or T*k <= 4*E. Rows past offsets[E] are left
+ *   as they are.
  *
  * moe_mx_expert_ffn -- gate_up, then h quantised to h_q, h_s in h_fmt, then down.
  */

@@ -177,7 +177,6 @@ hipError_t launch_gemv_t(const MxProduct& p, hipStream_t st) {
 
 constexpr int kGemmThreads = 256;
 constexpr int kGemmCols = 256;   // weight rows a tile (gated: half of them gate, half up)
-constexpr int kMF = 4;
 constexpr int kStepBlocks = 8;    // blocks of K a step: four matrix instructions deep
 constexpr int kSlices = kStepBlocks / 2;
 constexpr int kScaleBlocks = 128;              // blocks of K whose row scales lie in LDS at once
@@ -263,13 +262,18 @@ __device__ bool find_tile(const MxProduct& p, int bm, int mt, int* e, int* m0, i
 // bytes of MXFP4 codes are then one whole cache line, where half steps asked L2 for every
 // line twice. Row scales, one byte a block, come 128 blocks at a time for the same reason.
 template <int FMT, bool GATED, int MF>
-__global__ __launch_bounds__(kGemmThreads, 2) void k_mx_gemm(MxProduct p, int n_mtiles, int n_ntiles) {
+__global__ __launch_bounds__(kGemmThreads, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k_mx_gemm(MxProduct p, int n_mtiles, int n_ntiles) {
   constexpr int BM = 32 * MF;
   constexpr int TN = GATED ? kGemmCols / 2 : kGemmCols;   // output columns a tile
   constexpr int kBytes = mx_block_bytes(FMT);
   constexpr int NB = BM * kStepBlocks / kGemmThreads;   // row blocks a thread loads a step
   static_assert(NB >= 1, "a thread loads whole blocks");
-  __shared__ __attribute__((aligned(16))) uint8_t lds_q[2][BM * kStepBlocks * kBytes];
+  // two buffers of rows; the epilogue's fragments take their place
+  constexpr int kBuf = BM * kStepBlocks * kBytes;
+  constexpr int kPiece = GATED ? 2 : 4;                    // bytes of an output
+  constexpr int kOutRow = 32 * kPiece + 16;                // padded: no bank conflicts
+  constexpr int kTurn = kGemmThreads / kWave * 32 * kOutRow;
+  __shared__ __attribute__((aligned(16))) uint8_t lds_q[2 * kBuf > kTurn ? 2 * kBuf : kTurn];
   __shared__ __attribute__((aligned(16))) uint8_t lds_s[BM * kScaleRow];
   __shared__ int part[kGemmThreads / kWave];
   __shared__ int found[3];
@@ -342,7 +346,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_mx_gemm(MxProduct p, int n_
   auto put = [&](int c) {
     const bool ok = kStepBlocks * c + rb < nb;
 #pragma unroll
-    for (int j = 0; j < NB; ++j) rows[j].store(lds_q[c & 1] + place[j], ok);
+    for (int j = 0; j < NB; ++j) rows[j].store(lds_q + (c & 1) * kBuf + place[j], ok);
   };
   u32x4 wgt[2][kSlices];
   uint32_t wsc[2][kSlices];
@@ -413,7 +417,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_mx_gemm(MxProduct p, int n_
 #pragma unroll
       for (int m = 0; m < MF; ++m) {
         const v8i a = load_block<FMT>(
-            lds_q[c & 1] + rplace[s] + m * 32 * kStepBlocks * kBytes, true);
+            lds_q + (c & 1) * kBuf + rplace[s] + m * 32 * kStepBlocks * kBytes, true);
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
           const v8i w = {(int)wgt[f][s][0], (int)wgt[f][s][1], (int)wgt[f][s][2],
@@ -437,11 +441,8 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_mx_gemm(MxProduct p, int n_
   // ---- a lane holds, of one bucket row, 4 groups of 4 neighbouring columns a fragment; each
   // wave turns its fragments round in LDS of its own (the rows' buffers, no longer read), so
   // that the stores are whole cache lines of a row (gated: halves) and not 16-byte pieces
-  constexpr int kPiece = GATED ? 2 : 4;                    // bytes of an output
-  constexpr int kOutRow = 32 * kPiece + 16;                // padded: no bank conflicts
   constexpr int kLanesRow = 32 * kPiece / 16;              // lanes that store one row
-  static_assert(4 * 32 * kOutRow <= sizeof(lds_q), "the fragments fit");
-  uint8_t* turn = lds_q[0] + wave * 32 * kOutRow;
+  uint8_t* turn = lds_q + wave * 32 * kOutRow;
   uint8_t* out = GATED ? (uint8_t*)p.h : (uint8_t*)p.y;
 #pragma unroll
   for (int m = 0; m < MF; ++m) {
@@ -491,10 +492,18 @@ hipError_t launch_gemm_t(const MxProduct& p, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Rows a tile, by the mean rows of an expert: a tall tile reads the weights less often and
+// feeds more products per operand read, a low one leaves fewer of its rows empty and puts more
+// workgroups on a CU. Measured, gate/up us with 32 / 64 / 128 rows: H = I = 2880, 32 experts,
+// MXFP6, mean 41: 68 / 83 / 84; 125: 119 / 117 / 123; 250: 193 / 176 / 164; H 2048, I 768, 128
+// experts, MXFP4, mean 62: 44 / 46 / 53; 125: 70 / 60 / 71; 512: - / 175 / 176.
 template <int FMT, bool GATED>
 hipError_t launch_t(const MxProduct& p, bool gemv, hipStream_t st) {
   if (gemv) return launch_gemv_t<FMT, GATED>(p, st);
-  return launch_gemm_t<FMT, GATED, kMF>(p, st);
+  const int mean = p.T * p.k / p.E;
+  if (mean > 200) return launch_gemm_t<FMT, GATED, 4>(p, st);
+  if (mean > 64) return launch_gemm_t<FMT, GATED, 2>(p, st);
+  return launch_gemm_t<FMT, GATED, 1>(p, st);
 }
 
 }  // namespace
