@@ -494,6 +494,9 @@ class LayerCall:
 # --------------------------------------------- microscaled rows, and the block's two ends
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream   # a stream handle without a Stream object
+
+
 def _one_of(name, value, choices):
     if value not in choices:
         raise ValueError(f"{name}: {value!r}, expected one of {', '.join(map(repr, choices))}")
@@ -501,18 +504,29 @@ def _one_of(name, value, choices):
 
 def _tensor(t, dtypes, shape, name, like):
     """A contiguous device tensor of one of `dtypes`, on the device of `like`."""
+    if t.dtype in dtypes and t.shape == shape and t.is_cuda and t.device == like.device and \
+            t.is_contiguous():
+        return
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
     _need(t, t.dtype, shape, name)
-    if t.device != like.device:
-        raise ValueError(f"{name}: on {t.device}, expected {like.device}")
+    raise ValueError(f"{name}: on {t.device}, expected {like.device}")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _run(fn, like, stream, *args):
     """Calls fn(*args, stream) with the device of `like` current, on that device's current
     stream unless one is given."""
-    with torch.cuda.device(like.device):
-        _check(fn(*args, _stream(stream)))
+    index = like.device.index
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        _check(fn(*args, handle))
+    else:
+        with torch.cuda.device(index):
+            _check(fn(*args, handle))
 
 
 def mx_row_bytes(fmt: str, K: int) -> int:
@@ -539,8 +553,8 @@ def mx_quantize(x, fmt: str = "mxfp4", q=None, s=None, stream=None):
     if s is None:
         s = torch.empty((*rows, K // 32), dtype=torch.uint8, device=x.device)
     _mx_planes(q, s, fmt, rows, K, ("q", "s"), x)
-    _run(_mx_quantize, x, stream, _ptr(x), _DT[x.dtype], x.numel() // max(K, 1), K, _MX[fmt],
-         _ptr(q), _ptr(s))
+    _run(_mx_quantize, x, stream, _addr(x), _DT[x.dtype], x.numel() // max(K, 1), K, _MX[fmt],
+         _addr(q), _addr(s))
     return q, s
 
 
@@ -553,8 +567,8 @@ def mx_dequantize(q, s, fmt: str = "mxfp4", dtype=torch.bfloat16, out=None, stre
     if out is None:
         out = torch.empty((*rows, K), dtype=dtype, device=q.device)
     _tensor(out, (dtype,), (*rows, K), "out", q)
-    _run(_mx_dequantize, q, stream, _ptr(q), _ptr(s), _MX[fmt], s.numel() // max(nb, 1), K,
-         _ptr(out), _DT[dtype])
+    _run(_mx_dequantize, q, stream, _addr(q), _addr(s), _MX[fmt], s.numel() // max(nb, 1), K,
+         _addr(out), _DT[dtype])
     return out
 
 
@@ -588,8 +602,8 @@ def mx_expert_gate_up(pool: Pool, slot_map, x_q, x_s, fmt: str, k: int, offsets,
     _mx_planes(x_q, x_s, fmt, (T,), pool.H, ("x_q", "x_s"), x_q)
     E = _mx_checks(pool, slot_map, T, k, offsets, perm, err_flags, x_q)
     h = _rows(h, torch.bfloat16, (T * k, pool.I), "h", x_q)
-    _run(_mx_gate_up, x_q, stream, ctypes.byref(pool.struct), _ptr(slot_map), E, _ptr(x_q),
-         _ptr(x_s), _MX[fmt], T, k, _ptr(offsets), _ptr(perm), _ptr(h), _ptr(err_flags), path)
+    _run(_mx_gate_up, x_q, stream, ctypes.byref(pool.struct), _addr(slot_map), E, _addr(x_q),
+         _addr(x_s), _MX[fmt], T, k, _addr(offsets), _addr(perm), _addr(h), _addr(err_flags), path)
     return h
 
 
@@ -599,8 +613,8 @@ def mx_expert_down(pool: Pool, slot_map, T: int, k: int, offsets, h_q, h_s, fmt:
     _mx_planes(h_q, h_s, fmt, (T * k,), pool.I, ("h_q", "h_s"), h_q)
     E = _mx_checks(pool, slot_map, T, k, offsets, None, err_flags, h_q)
     y = _rows(y, torch.float32, (T * k, pool.H), "y", h_q)
-    _run(_mx_down, h_q, stream, ctypes.byref(pool.struct), _ptr(slot_map), E, _ptr(h_q),
-         _ptr(h_s), _MX[fmt], T, k, _ptr(offsets), _ptr(y), _ptr(err_flags), path)
+    _run(_mx_down, h_q, stream, ctypes.byref(pool.struct), _addr(slot_map), E, _addr(h_q),
+         _addr(h_s), _MX[fmt], T, k, _addr(offsets), _addr(y), _addr(err_flags), path)
     return y
 
 
@@ -617,9 +631,9 @@ def mx_expert_ffn(pool: Pool, slot_map, x_q, x_s, fmt: str, k: int, offsets, per
     h_q = _rows(h_q, torch.uint8, (T * k, mx_row_bytes(h_fmt, pool.I)), "h_q", x_q)
     h_s = _rows(h_s, torch.uint8, (T * k, pool.I // 32), "h_s", x_q)
     y = _rows(y, torch.float32, (T * k, pool.H), "y", x_q)
-    _run(_mx_ffn, x_q, stream, ctypes.byref(pool.struct), _ptr(slot_map), E, _ptr(x_q),
-         _ptr(x_s), _MX[fmt], T, k, _ptr(offsets), _ptr(perm), _ptr(h), _ptr(h_q), _ptr(h_s),
-         _MX[h_fmt], _ptr(y), _ptr(err_flags), path)
+    _run(_mx_ffn, x_q, stream, ctypes.byref(pool.struct), _addr(slot_map), E, _addr(x_q),
+         _addr(x_s), _MX[fmt], T, k, _addr(offsets), _addr(perm), _addr(h), _addr(h_q), _addr(h_s),
+         _MX[h_fmt], _addr(y), _addr(err_flags), path)
     return h, y
 
 
@@ -641,9 +655,9 @@ def add_norm(resid, weight, eps: float = 1e-6, delta=None, scale: float = 1.0, r
     if delta is not None or resid_out is not None:
         resid_out = _rows(resid_out, resid.dtype, (T, H), "resid_out", resid)
     x = _rows(x, torch.bfloat16, (T, H), "x", resid)
-    _run(_add_norm, resid, stream, _ptr(resid), _DT[resid.dtype], _ptr(delta),
-         0 if delta is None else _DT[delta.dtype], scale, _ptr(weight), _DT[weight.dtype], eps, T,
-         H, _ptr(resid_out), _ptr(x))
+    _run(_add_norm, resid, stream, _addr(resid), _DT[resid.dtype], _addr(delta),
+         0 if delta is None else _DT[delta.dtype], scale, _addr(weight), _DT[weight.dtype], eps, T,
+         H, _addr(resid_out), _addr(x))
     return x, resid if resid_out is None else resid_out
 
 
@@ -673,8 +687,8 @@ def combine_norm(y, inv_perm, w, resid, eps: float = 1e-6, post_weight=None, gat
     resid_out = _rows(resid_out, resid.dtype, (T, H), "resid_out", resid)
     if next_weight is not None:
         x = _rows(x, torch.bfloat16, (T, H), "x", resid)
-    _run(_combine_norm, resid, stream, _ptr(y), _ptr(inv_perm), _ptr(w), T, k, H, _ptr(resid),
-         _DT[resid.dtype], _ptr(post_weight), _ptr(gate),
-         T if gate is not None and gate.dim() == 2 else 1, scale, _ptr(next_weight),
-         _DT[given[0].dtype] if given else _DT[torch.float32], eps, _ptr(resid_out), _ptr(x))
+    _run(_combine_norm, resid, stream, _addr(y), _addr(inv_perm), _addr(w), T, k, H, _addr(resid),
+         _DT[resid.dtype], _addr(post_weight), _addr(gate),
+         T if gate is not None and gate.dim() == 2 else 1, scale, _addr(next_weight),
+         _DT[given[0].dtype] if given else _DT[torch.float32], eps, _addr(resid_out), _addr(x))
     return resid_out, x
