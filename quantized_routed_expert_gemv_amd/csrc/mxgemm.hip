@@ -193,27 +193,35 @@ __device__ __forceinline__ v16f mma32(v8i w, uint32_t ws, v8i a, uint32_t as, v1
                                                          (int)as);
 }
 
-// Where block b of tile row r lies among the row's kStepBlocks blocks in LDS, such that the
-// lanes of each pass of a 64-lane read (one block of 32 rows and the next of the same) touch
-// different banks: MXFP4's 128-byte rows repeat their banks every 2 rows, MXFP6's 192-byte
-// rows every 4.
-template <int FMT>
+// A step's rows in LDS: the first 16 bytes of each block, row by row, then (MXFP6) the last 8
+// of each. Block b of tile row r lies in place b ^ (r / 2 % 8) of the row's eight, and in the
+// second part b ^ (r / 4 % 8), such that the lanes of each pass of a 64-lane read (one block of
+// 32 rows and the next of the same) touch different banks: 128-byte rows repeat their banks
+// every 2 rows, 64-byte rows every 4. Read whole, MXFP6's 24-byte blocks would take three
+// 8-byte reads, at half the rate of 16-byte ones. Rows 32 apart lie at one distance.
 __device__ __forceinline__ int lds_place(int r, int b) {
-  return b ^ ((FMT == kMxFp4 ? r >> 1 : r >> 2) & 7);
+  return (r * kStepBlocks + (b ^ ((r >> 1) & 7))) * 16;
+}
+__device__ __forceinline__ int lds_place_tail(int r, int b) {
+  return (r * kStepBlocks + (b ^ ((r >> 2) & 7))) * 8;
 }
 
 // A block's codes as they travel from memory to LDS.
 template <int FMT> struct Codes {
-  static constexpr int kParts = FMT == kMxFp4 ? 1 : 3;
-  typedef std::conditional_t<FMT == kMxFp4, u32x4, u32x2> Part;
-  Part v[kParts];
+  u32x4 v;
+  u32x2 t;   // MXFP6
   __device__ __forceinline__ void load(const uint8_t* p) {
-#pragma unroll
-    for (int i = 0; i < kParts; ++i) v[i] = ((const Part*)p)[i];
+    typedef u32x4 __attribute__((aligned(8))) u32x4_8;   // MXFP6 blocks: every 24 bytes
+    if constexpr (FMT == kMxFp4) {
+      v = *(const u32x4*)p;
+    } else {
+      v = *(const u32x4_8*)p;
+      t = *(const u32x2*)(p + 16);
+    }
   }
-  __device__ __forceinline__ void store(uint8_t* p, bool ok) const {   // zeros where !ok
-#pragma unroll
-    for (int i = 0; i < kParts; ++i) ((Part*)p)[i] = ok ? v[i] : Part{};
+  __device__ __forceinline__ void store(uint8_t* p, uint8_t* tail, bool ok) const {   // or zeros
+    *(u32x4*)p = ok ? v : u32x4{0, 0, 0, 0};
+    if constexpr (FMT == kMxFp6) *(u32x2*)tail = ok ? t : u32x2{0, 0};
   }
 };
 
@@ -313,13 +321,11 @@ __global__ __launch_bounds__(kGemmThreads, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k
   // ---- rows: thread t carries block t % 8 of tile rows t / 8 + 32 j
   const int rb = threadIdx.x & (kStepBlocks - 1);
   const uint8_t* rq[NB];
-  int place[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
     const int r = threadIdx.x / kStepBlocks + kGemmThreads / kStepBlocks * j;
     const int64_t row = source_row<GATED>(p, min(m0 + r, mend - 1));   // past the end: the last
     rq[j] = p.q + row * nb * kBytes;
-    place[j] = (r * kStepBlocks + lds_place<FMT>(r, rb)) * kBytes;
   }
   // ---- weights: fragment f is 32 rows from col[f] on; lane l holds row l % 32
   int col[2];
@@ -337,6 +343,10 @@ __global__ __launch_bounds__(kGemmThreads, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k
   const uint32_t wlane = (uint32_t)((lane & 31) >> 4) * nb * kRowGroup + (lane & 15);   // unit
   // Loads: nothing here may wait for them. A block past the row reads the row's last; its
   // codes are replaced by zeros when they are put in LDS, which is enough on one side.
+  constexpr int kRows32 = 32 * kStepBlocks;      // blocks from one row to that 32 further on
+  constexpr int kTail = BM * kStepBlocks * 16;   // MXFP6: where a buffer's second part begins
+  const int place = lds_place(threadIdx.x / kStepBlocks, rb);
+  const int place_tail = kTail + lds_place_tail(threadIdx.x / kStepBlocks, rb);
   Codes<FMT> rows[NB];
   auto load_rows = [&](int c) {
     const int b = min(kStepBlocks * c + rb, nb - 1);
@@ -344,9 +354,14 @@ __global__ __launch_bounds__(kGemmThreads, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k
     for (int j = 0; j < NB; ++j) rows[j].load(rq[j] + (uint32_t)b * kBytes);
   };
   auto put = [&](int c) {
-    const bool ok = kStepBlocks * c + rb < nb;
+    uint8_t* to = lds_q + (c & 1) * kBuf;
+    auto all = [&](bool ok) {
 #pragma unroll
-    for (int j = 0; j < NB; ++j) rows[j].store(lds_q + (c & 1) * kBuf + place[j], ok);
+      for (int j = 0; j < NB; ++j)
+        rows[j].store(to + place + j * kRows32 * 16, to + place_tail + j * kRows32 * 8, ok);
+    };
+    if (kStepBlocks * (c + 1) <= nb) all(true);   // only a row's last step can be short
+    else all(kStepBlocks * c + rb < nb);
   };
   u32x4 wgt[2][kSlices];
   uint32_t wsc[2][kSlices];
@@ -358,31 +373,48 @@ __global__ __launch_bounds__(kGemmThreads, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k
       wsc[f][s] = *(const uint32_t*)(ws[f] + (u & ~3u));   // the scales of 4 rows
     }
   };
-  // Row scales of blocks b0 .. b0 + kScaleBlocks - 1, and ones past the row: each thread takes
-  // every kParts-th dword of its row. The rows lie at any byte, so a row's last dword is
-  // gathered byte by byte.
+  // Row scales of blocks b0 .. b0 + kScaleBlocks - 1, and ones past the row: a thread takes
+  // every kParts-th 8 blocks of its row and stores the even ones' bytes, then the odd ones',
+  // so that a lane's four of a step are one dword. The rows lie at any byte, so a row's last
+  // dwords are gathered byte by byte.
   auto load_scales = [&](int b0) {
     constexpr int kParts = kGemmThreads / BM;
     const int r = threadIdx.x / kParts;
     const uint8_t* src = p.s + (int64_t)source_row<GATED>(p, min(m0 + r, mend - 1)) * nb + b0;
     const int n = min(nb - b0, kScaleBlocks);
-    uint32_t* dst = (uint32_t*)(lds_s + r * kScaleRow);
-#pragma unroll 8
-    for (int d = threadIdx.x % kParts; d < kScaleBlocks / 4; d += kParts) {
-      uint32_t v = kOne * 0x01010101u;
-      if (4 * d + 4 <= n) {
-        __builtin_memcpy(&v, src + 4 * d, 4);
-      } else {
-        for (int i = 0; 4 * d + i < n; ++i)
-          v = (v & ~(0xFFu << (8 * i))) | (uint32_t)src[4 * d + i] << (8 * i);
+    u32x2* dst = (u32x2*)(lds_s + r * kScaleRow);
+#pragma unroll 4
+    for (int d = threadIdx.x % kParts; d < kScaleBlocks / 8; d += kParts) {
+      uint32_t v[2] = {kOne * 0x01010101u, kOne * 0x01010101u};
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int at = 8 * d + 4 * w;
+        if (at + 4 <= n) {
+          __builtin_memcpy(&v[w], src + at, 4);
+        } else {
+          for (int i = 0; at + i < n; ++i)
+            v[w] = (v[w] & ~(0xFFu << (8 * i))) | (uint32_t)src[at + i] << (8 * i);
+        }
       }
-      dst[d] = v;
+      dst[d] = u32x2{__builtin_amdgcn_perm(v[1], v[0], 0x06040200u),
+                     __builtin_amdgcn_perm(v[1], v[0], 0x07050301u)};
     }
   };
-  int rplace[kSlices];   // where the lane reads its blocks of the first 32 rows
-#pragma unroll
-  for (int s = 0; s < kSlices; ++s)
-    rplace[s] = ((lane & 31) * kStepBlocks + lds_place<FMT>(lane & 31, 2 * s + half)) * kBytes;
+  // where the lane reads block `half` of the first 32 rows; block 2 s + half lies at an
+  // exclusive or of that
+  const int from = lds_place(lane & 31, half);
+  const int from_tail = lds_place_tail(lane & 31, half);
+  auto read_block = [&](int buf, int s, int m) {
+    const u32x4 v = *(const u32x4*)(lds_q + buf + (from ^ (2 * s * 16)) + m * kRows32 * 16);
+    v8i a = {(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+    if constexpr (FMT == kMxFp6) {
+      const u32x2 t =
+          *(const u32x2*)(lds_q + buf + kTail + (from_tail ^ (2 * s * 8)) + m * kRows32 * 8);
+      a[4] = (int)t[0];
+      a[5] = (int)t[1];
+    }
+    return a;
+  };
   v16f acc[MF][2];
 #pragma unroll
   for (int m = 0; m < MF; ++m)
@@ -402,10 +434,10 @@ __global__ __launch_bounds__(kGemmThreads, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k
     }
     if (c + 1 < nsteps) load_rows(c + 1);
     __builtin_amdgcn_sched_barrier(0);   // the loads go first, what waits for them last
-    u32x2 as[MF];
+    uint32_t as[MF];
 #pragma unroll
     for (int m = 0; m < MF; ++m)
-      as[m] = *(const u32x2*)(lds_s + (32 * m + (lane & 31)) * kScaleRow + sb) >> (uint32_t)(8 * half);
+      as[m] = *(const uint32_t*)(lds_s + (32 * m + (lane & 31)) * kScaleRow + sb + 4 * half);
     auto slice = [&](auto sl) {
       constexpr int s = decltype(sl)::value;
       uint32_t sw[2];
@@ -416,13 +448,12 @@ __global__ __launch_bounds__(kGemmThreads, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k
       }
 #pragma unroll
       for (int m = 0; m < MF; ++m) {
-        const v8i a = load_block<FMT>(
-            lds_q + (c & 1) * kBuf + rplace[s] + m * 32 * kStepBlocks * kBytes, true);
+        const v8i a = read_block((c & 1) * kBuf, s, m);
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
           const v8i w = {(int)wgt[f][s][0], (int)wgt[f][s][1], (int)wgt[f][s][2],
                          (int)wgt[f][s][3], 0, 0, 0, 0};
-          acc[m][f] = mma32<FMT, 2 * (s & 1)>(w, sw[f], a, as[m][s >> 1], acc[m][f]);
+          acc[m][f] = mma32<FMT, s>(w, sw[f], a, as[m], acc[m][f]);
         }
       }
       // the products stay in their slice, and one slice's operands at a time in registers:
