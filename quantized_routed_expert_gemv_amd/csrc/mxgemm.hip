@@ -179,6 +179,7 @@ constexpr int kGemmThreads = 256;
 constexpr int kGemmCols = 256;   // weight rows a tile (gated: half of them gate, half up)
 constexpr int kStepBlocks = 8;    // blocks of K a step: four matrix instructions deep
 constexpr int kSlices = kStepBlocks / 2;
+constexpr int kSuperRows = 16, kSuperCols = 4; // tiles of a run, by rows and columns
 constexpr int kScaleBlocks = 128;              // blocks of K whose row scales lie in LDS at once
 constexpr int kScaleRow = kScaleBlocks + 8;    // bytes between rows: 34 dwords, bank by bank
 
@@ -285,18 +286,18 @@ __global__ __launch_bounds__(kGemmThreads, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k
   __shared__ __attribute__((aligned(16))) uint8_t lds_s[BM * kScaleRow];
   __shared__ int part[kGemmThreads / kWave];
   __shared__ int found[3];
-  // XCD-aware tile order, as the bf16 grouped GEMM: workgroups go to the 8 XCDs in turn, and
-  // each XCD gets runs of 64 tiles of 8 x 8 super-tiles, which share their rows in its L2
+  // XCD-aware tile order: workgroups go to the 8 XCDs in turn, and each XCD gets runs of 64
+  // tiles that share their rows and weights in its L2
   const int xcd = blockIdx.x & 7, local = blockIdx.x >> 3;
   const int64_t i = (int64_t)(local >> 6) * 512 + xcd * 64 + (local & 63);
   if (i >= (int64_t)n_mtiles * n_ntiles) return;
-  const int sr = (int)(i / (8LL * n_ntiles));
-  const int sh = min(8, n_mtiles - 8 * sr);
-  const int sj = (int)(i - 8LL * n_ntiles * sr);
-  const int sc = sj / (8 * sh);
-  const int sw = min(8, n_ntiles - 8 * sc);
-  const int sk = sj - 8 * sh * sc;
-  const int mt = 8 * sr + sk / sw, nt = 8 * sc + sk % sw;
+  const int sr = (int)(i / ((int64_t)kSuperRows * n_ntiles));
+  const int sh = min(kSuperRows, n_mtiles - kSuperRows * sr);
+  const int sj = (int)(i - (int64_t)kSuperRows * n_ntiles * sr);
+  const int sc = sj / (kSuperCols * sh);
+  const int sw = min(kSuperCols, n_ntiles - kSuperCols * sc);
+  const int sk = sj - kSuperCols * sh * sc;
+  const int mt = kSuperRows * sr + sk / sw, nt = kSuperCols * sc + sk % sw;
   int e, m0, mend;
   if (!find_tile(p, BM, mt, &e, &m0, &mend, part, found)) return;
   const int n0 = nt * TN;
@@ -429,7 +430,9 @@ __global__ __launch_bounds__(kGemmThreads, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k
   for (int c = 0; c < nsteps; ++c) {
     const int sb = kStepBlocks * c % kScaleBlocks;
     if (sb == 0) {
-      load_scales(kStepBlocks * c);
+      int b0 = kStepBlocks * c;
+      asm volatile("" : "+s"(b0));   // no addresses kept and stepped along for this
+      load_scales(b0);
       __syncthreads();
     }
     if (c + 1 < nsteps) load_rows(c + 1);
