@@ -6,9 +6,11 @@
 // comes from the unrounded s, so the stream's storage type costs the norm nothing.
 //
 // About ten flops a value: copy rate bounds them (latency for a few rows), so a row is
-// read once and held in registers between its sums and its stores, up to 8192 values; longer
+// read once and held in registers between its sums and its stores, up to 16384 values; longer
 // rows are recomputed from the inputs for each sum. r' may be r itself: a
 // thread stores a value only after every read of it.
+#include <type_traits>
+
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -55,32 +57,55 @@ __device__ __forceinline__ float dot4(f32x4 v, float s) {
   return s;
 }
 
-// sum_j w_j y[pos_j][c..c+3] in increasing j. A position outside [0, T*k) adds nothing.
-__device__ __forceinline__ f32x4 combine4(const BlockNorm& a, const int* pos, const float* wj,
-                                          int c) {
-  f32x4 v[kMaxK], acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int j = 0; j < kMaxK; ++j)   // y is read once: nontemporal
-    v[j] = j < a.k && pos[j] >= 0
-               ? __builtin_nontemporal_load((const f32x4*)(a.y + (int64_t)pos[j] * a.H + c))
-               : f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int j = 0; j < kMaxK; ++j)
-    if (j < a.k) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) acc[q] = fmaf(wj[j], v[j][q], acc[q]);
-    }
-  return acc;
-}
-
-__device__ __forceinline__ void read_choices(const BlockNorm& a, int64_t t, int* pos, float* wj) {
+// A row's choices: positions in y, -1 for one outside [0, T*k), which adds nothing.
+struct Choices {
+  int pos[kMaxK];
+  float w[kMaxK];
+};
+__device__ __forceinline__ Choices read_choices(const BlockNorm& a, int64_t t) {
+  Choices c;
 #pragma unroll
   for (int j = 0; j < kMaxK; ++j) {
     const int64_t p = t * a.k + (j < a.k ? j : 0);
     const int q = a.inv_perm[p];
-    const bool in = (unsigned)q < (unsigned)(a.T * a.k);
-    pos[j] = in ? q : -1;
-    wj[j] = in ? a.w[p] : 0.f;
+    c.pos[j] = (unsigned)q < (unsigned)(a.T * a.k) ? q : -1;
+    c.w[j] = a.w[p];
+  }
+  return c;
+}
+
+// sum_{j < K} w_j y[pos_j][c..c+3] in increasing j. Every load is unconditional (a choice that
+// adds nothing reads row 0 and is dropped), so all of a row's are in flight at once. y is read
+// once where a row stays in registers: nontemporal.
+template <int K, bool NT>
+__device__ __forceinline__ f32x4 combine4(const BlockNorm& a, const Choices& ch, int c) {
+  f32x4 v[K], acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    const f32x4* p = (const f32x4*)(a.y + (int64_t)max(ch.pos[j], 0) * a.H + c);
+    v[j] = NT ? __builtin_nontemporal_load(p) : *p;
+  }
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    const bool in = ch.pos[j] >= 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[q] = in ? fmaf(ch.w[j], v[j][q], acc[q]) : acc[q];
+  }
+  return acc;
+}
+
+// Calls f with k as a constant.
+template <typename F>
+__device__ __forceinline__ void with_k(int k, F f) {
+  switch (k) {
+    case 1: f(std::integral_constant<int, 1>{}); break;
+    case 2: f(std::integral_constant<int, 2>{}); break;
+    case 3: f(std::integral_constant<int, 3>{}); break;
+    case 4: f(std::integral_constant<int, 4>{}); break;
+    case 5: f(std::integral_constant<int, 5>{}); break;
+    case 6: f(std::integral_constant<int, 6>{}); break;
+    case 7: f(std::integral_constant<int, 7>{}); break;
+    default: f(std::integral_constant<int, 8>{});
   }
 }
 
@@ -92,18 +117,24 @@ __global__ __launch_bounds__(TH) void k_block_norm(BlockNorm a) {
   const int64_t t = blockIdx.x;
   const R* rin = (const R*)a.resid + t * a.H;
   f32x4 s[NCH], v[NCH];
-  int pos[kMaxK];
-  float wj[kMaxK];
-  if (EXIT) read_choices(a, t, pos, wj);
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const int c = (i * TH + threadIdx.x) * 4;
     s[i] = v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (c < a.H) {
       s[i] = load4(rin + c);
-      if (EXIT) v[i] = combine4(a, pos, wj, c);
-      else if (a.delta) v[i] = load4(a.delta, a.delta_f32, t * a.H + c);
+      if (!EXIT && a.delta) v[i] = load4(a.delta, a.delta_f32, t * a.H + c);
     }
+  }
+  if constexpr (EXIT) {
+    const Choices ch = read_choices(a, t);
+    with_k(a.k, [&](auto k) {
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        const int c = (i * TH + threadIdx.x) * 4;
+        if (c < a.H) v[i] = combine4<decltype(k)::value, true>(a, ch, c);
+      }
+    });
   }
   if (EXIT && a.post) {
     float ss = 0.f;
@@ -144,19 +175,23 @@ __global__ __launch_bounds__(1024) void k_block_norm_long(BlockNorm a) {
   constexpr int TH = 1024, NW = TH / kWave;
   __shared__ float red[NW];
   const int64_t t = blockIdx.x;
-  int pos[kMaxK];
-  float wj[kMaxK];
-  if (EXIT) read_choices(a, t, pos, wj);
+  Choices ch;
+  if constexpr (EXIT) ch = read_choices(a, t);
+  auto combined = [&](int c) {
+    f32x4 v;
+    with_k(a.k, [&](auto k) { v = combine4<decltype(k)::value, false>(a, ch, c); });
+    return v;
+  };
   float rs_post = 1.f;
   if (EXIT && a.post) {
     float ss = 0.f;
-    for (int c = threadIdx.x * 4; c < a.H; c += TH * 4) ss = dot4(combine4(a, pos, wj, c), ss);
+    for (int c = threadIdx.x * 4; c < a.H; c += TH * 4) ss = dot4(combined(c), ss);
     rs_post = rsqrtf(group_sum<NW>(ss, red) / a.H + a.eps);
   }
   auto value = [&](int c) {
     f32x4 s = load4((const R*)a.resid + t * a.H + c), v = {0.f, 0.f, 0.f, 0.f};
     if (EXIT) {
-      v = combine4(a, pos, wj, c);
+      v = combined(c);
       if (a.post) v = v * rs_post * load4(a.post, a.par_f32, c);
       if (a.gate) v *= load4(a.gate, a.par_f32, t * a.gate_stride + c);
     } else if (a.delta) {
@@ -193,6 +228,8 @@ hipError_t launch_t(const BlockNorm& a, hipStream_t stream) {
     case 4: MOE_NORM(256, 4); break;
     case 5: case 6: MOE_NORM(256, 6); break;
     case 7: case 8: MOE_NORM(256, 8); break;
+    case 9: case 10: case 11: case 12: MOE_NORM(1024, 3); break;
+    case 13: case 14: case 15: case 16: MOE_NORM(1024, 4); break;
     default: hipLaunchKernelGGL((k_block_norm_long<EXIT, R>), grid, dim3(1024), 0, stream, a);
   }
 #undef MOE_NORM
