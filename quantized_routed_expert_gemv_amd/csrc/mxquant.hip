@@ -61,25 +61,29 @@ __device__ __forceinline__ uint32_t e2m3(float t) {
   return c | (u >> 31) << 5;
 }
 
-// 4 threads a block of 32, 8 values a thread: one 16-byte load of a 16-bit type (two of
-// fp32) and the block's maximum by two lane exchanges.
-template <int FMT, typename S>
-__global__ __launch_bounds__(kTh) void k_quantize(const void* __restrict__ src, int64_t n8,
+// A thread takes V values, a block's threads exchange their maxima. V is 8 for E2M1 (one
+// 16-byte load of a 16-bit type, a dword of codes) and 16 for E2M3, whose 16 codes are three
+// whole dwords.
+template <int FMT, typename S, int V>
+__global__ __launch_bounds__(kTh) void k_quantize(const void* __restrict__ src, int64_t n,
                                                   uint8_t* __restrict__ q,
                                                   uint8_t* __restrict__ s) {
-  const int64_t i = (int64_t)blockIdx.x * kTh + threadIdx.x;   // group of 8 values
-  if (i >= n8) return;   // n8 is a multiple of 4: a block's threads go together
-  float v[8];
-  Src<S>::load8(src, i, v);
+  constexpr int kPer = 32 / V;   // threads a block
+  const int64_t i = (int64_t)blockIdx.x * kTh + threadIdx.x;   // group of V values
+  if (i >= n) return;   // n is a multiple of kPer: a block's threads go together
+  float v[V];
+#pragma unroll
+  for (int h = 0; h < V / 8; ++h) Src<S>::load8(src, i * (V / 8) + h, v + 8 * h);
   uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = max_u(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-  m = max_u(m, __shfl_xor(m, 1, kWave));
-  m = max_u(m, __shfl_xor(m, 2, kWave));
+  for (int j = 0; j < V; ++j) m = max_u(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int x = 1; x < kPer; x <<= 1) m = max_u(m, __shfl_xor(m, x, kWave));
   const uint32_t sb = scale_byte(m);
   const bool bad = sb == 255;
-  if ((i & 3) == 0) s[i >> 2] = (uint8_t)sb;
+  if (i % kPer == 0) s[i / kPer] = (uint8_t)sb;
   if constexpr (FMT == kMxFp4) {
+    static_assert(V == 8, "a dword of codes");
     const float sc = __uint_as_float(sb << 23);
     uint32_t c = 0;
     c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], sc, 0);
@@ -88,15 +92,18 @@ __global__ __launch_bounds__(kTh) void k_quantize(const void* __restrict__ src, 
     c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], sc, 3);
     ((uint32_t*)q)[i] = bad ? 0u : c;
   } else {
+    static_assert(V == 16, "three dwords of codes");
     const float inv = __uint_as_float((254u - (bad ? 127u : sb)) << 23);   // 2^(127 - s), exact
-    uint64_t c = 0;
+    uint32_t c[3] = {0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) c |= (uint64_t)e2m3(v[j] * inv) << (6 * j);
-    if (bad) c = 0;
-    uint16_t* o = (uint16_t*)(q + i * 6);
-    o[0] = (uint16_t)c;
-    o[1] = (uint16_t)(c >> 16);
-    o[2] = (uint16_t)(c >> 32);
+    for (int j = 0; j < V; ++j) {
+      const uint32_t code = bad ? 0u : e2m3(v[j] * inv);
+      c[6 * j / 32] |= code << (6 * j % 32);
+      if (6 * j % 32 > 26) c[6 * j / 32 + 1] |= code >> (32 - 6 * j % 32);
+    }
+    uint32_t* o = (uint32_t*)(q + i * 12);
+#pragma unroll
+    for (int d = 0; d < 3; ++d) o[d] = c[d];
   }
 }
 
@@ -111,58 +118,76 @@ __device__ __forceinline__ float code_value(uint32_t c) {
   return (c >> (B + 2)) & 1u ? -v : v;
 }
 
-// 8 values a thread: one 4- (E2M1) or 6-byte read, one 16-byte store of a 16-bit type. A
-// value is code * 2^(s - 127), rounded to the output's type where it is too fine for it.
+// V values a thread, 32 bytes stored: 16 of a 16-bit type (an 8- or 12-byte read of codes), 8
+// of fp32 (wider strides between the lanes' stores cost a quarter of the rate). A value is
+// code * 2^(s - 127), rounded to the output's type where it is too fine for it.
 template <int FMT, typename D>
 __global__ __launch_bounds__(kTh) void k_dequantize(const uint8_t* __restrict__ q,
-                                                    const uint8_t* __restrict__ s, int64_t n8,
+                                                    const uint8_t* __restrict__ s, int64_t n,
                                                     void* __restrict__ dst) {
+  constexpr int kBits = FMT == kMxFp4 ? 4 : 6, V = 32 / sizeof(D), kHalves = kBits * V / 16;
   const int64_t i = (int64_t)blockIdx.x * kTh + threadIdx.x;
-  if (i >= n8) return;
-  const uint32_t sb = s[i >> 2];
+  if (i >= n) return;
+  const uint32_t sb = s[i / (32 / V)];
   // 2^(s - 127) in two factors, so that s = 0 needs no subnormal constant
   const float f0 = __uint_as_float((sb == 255 ? 255u : sb / 2 + 64) << 23);
   const float f1 = __uint_as_float((sb == 255 ? 127u : sb - sb / 2 + 63) << 23);
-  float v[8];
-  uint64_t c;
-  if constexpr (FMT == kMxFp4) {
-    c = ((const uint32_t*)q)[i];
-  } else {
-    const uint16_t* p = (const uint16_t*)(q + i * 6);
-    c = p[0] | (uint64_t)p[1] << 16 | (uint64_t)p[2] << 32;
-  }
+  uint32_t c[(kHalves + 1) / 2] = {};
+  if constexpr (kHalves % 2 == 0) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    constexpr int kBits = FMT == kMxFp4 ? 4 : 6;
-    v[j] = code_value<kBits - 3>((uint32_t)(c >> (kBits * j)) & ((1u << kBits) - 1)) * f0 * f1;
+    for (int d = 0; d < kHalves / 2; ++d) c[d] = ((const uint32_t*)q)[i * (kHalves / 2) + d];
+  } else {   // 6 bytes, 2-byte aligned
+#pragma unroll
+    for (int d = 0; d < kHalves; ++d)
+      c[d / 2] |= (uint32_t)((const uint16_t*)q)[i * kHalves + d] << (16 * (d % 2));
+  }
+  float v[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int at = kBits * j;
+    uint32_t code = c[at / 32] >> (at % 32);
+    if (at % 32 > 32 - kBits) code |= c[at / 32 + 1] << (32 - at % 32);
+    v[j] = code_value<kBits - 3>(code & ((1u << kBits) - 1)) * f0 * f1;
     if (sb == 255) v[j] = __builtin_nanf("");
   }
-  if constexpr (sizeof(D) == 4) {
-    ((f32x4*)dst)[2 * i] = f32x4{v[0], v[1], v[2], v[3]};
-    ((f32x4*)dst)[2 * i + 1] = f32x4{v[4], v[5], v[6], v[7]};
-  } else {
-    typedef D d8 __attribute__((__vector_size__(16)));
-    ((d8*)dst)[i] = d8{(D)v[0], (D)v[1], (D)v[2], (D)v[3], (D)v[4], (D)v[5], (D)v[6], (D)v[7]};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float* u = v + V / 2 * h;
+    if constexpr (sizeof(D) == 4) {
+      ((f32x4*)dst)[2 * i + h] = f32x4{u[0], u[1], u[2], u[3]};
+    } else {
+      typedef D d8 __attribute__((__vector_size__(16)));
+      ((d8*)dst)[2 * i + h] = d8{(D)u[0], (D)u[1], (D)u[2], (D)u[3], (D)u[4], (D)u[5], (D)u[6], (D)u[7]};
+    }
   }
 }
 
 template <int FMT>
-hipError_t quantize_f(const void* src, int type, int64_t n8, uint8_t* q, uint8_t* s,
+hipError_t quantize_f(const void* src, int type, int64_t n, uint8_t* q, uint8_t* s,
                       hipStream_t st) {
-  const dim3 grid((unsigned)((n8 + kTh - 1) / kTh));
-  if (type == kBF16) hipLaunchKernelGGL((k_quantize<FMT, __bf16>), grid, dim3(kTh), 0, st, src, n8, q, s);
-  else if (type == kFP16) hipLaunchKernelGGL((k_quantize<FMT, _Float16>), grid, dim3(kTh), 0, st, src, n8, q, s);
-  else hipLaunchKernelGGL((k_quantize<FMT, float>), grid, dim3(kTh), 0, st, src, n8, q, s);
+  constexpr int V = FMT == kMxFp4 ? 8 : 16;
+  n /= V;
+  const dim3 grid((unsigned)((n + kTh - 1) / kTh));
+  if (type == kBF16)
+    hipLaunchKernelGGL((k_quantize<FMT, __bf16, V>), grid, dim3(kTh), 0, st, src, n, q, s);
+  else if (type == kFP16)
+    hipLaunchKernelGGL((k_quantize<FMT, _Float16, V>), grid, dim3(kTh), 0, st, src, n, q, s);
+  else
+    hipLaunchKernelGGL((k_quantize<FMT, float, V>), grid, dim3(kTh), 0, st, src, n, q, s);
   return hipGetLastError();
 }
 
 template <int FMT>
-hipError_t dequantize_f(const uint8_t* q, const uint8_t* s, int64_t n8, void* dst, int type,
+hipError_t dequantize_f(const uint8_t* q, const uint8_t* s, int64_t n, void* dst, int type,
                         hipStream_t st) {
-  const dim3 grid((unsigned)((n8 + kTh - 1) / kTh));
-  if (type == kBF16) hipLaunchKernelGGL((k_dequantize<FMT, __bf16>), grid, dim3(kTh), 0, st, q, s, n8, dst);
-  else if (type == kFP16) hipLaunchKernelGGL((k_dequantize<FMT, _Float16>), grid, dim3(kTh), 0, st, q, s, n8, dst);
-  else hipLaunchKernelGGL((k_dequantize<FMT, float>), grid, dim3(kTh), 0, st, q, s, n8, dst);
+  n /= type == kFP32 ? 8 : 16;
+  const dim3 grid((unsigned)((n + kTh - 1) / kTh));
+  if (type == kBF16)
+    hipLaunchKernelGGL((k_dequantize<FMT, __bf16>), grid, dim3(kTh), 0, st, q, s, n, dst);
+  else if (type == kFP16)
+    hipLaunchKernelGGL((k_dequantize<FMT, _Float16>), grid, dim3(kTh), 0, st, q, s, n, dst);
+  else
+    hipLaunchKernelGGL((k_dequantize<FMT, float>), grid, dim3(kTh), 0, st, q, s, n, dst);
   return hipGetLastError();
 }
 
@@ -170,14 +195,14 @@ hipError_t dequantize_f(const uint8_t* q, const uint8_t* s, int64_t n8, void* ds
 
 hipError_t launch_mx_quantize(const void* src, int type, int64_t n, int fmt, uint8_t* q,
                               uint8_t* s, hipStream_t st) {
-  return fmt == kMxFp4 ? quantize_f<kMxFp4>(src, type, n / 8, q, s, st)
-                       : quantize_f<kMxFp6>(src, type, n / 8, q, s, st);
+  return fmt == kMxFp4 ? quantize_f<kMxFp4>(src, type, n, q, s, st)
+                       : quantize_f<kMxFp6>(src, type, n, q, s, st);
 }
 
 hipError_t launch_mx_dequantize(const uint8_t* q, const uint8_t* s, int64_t n, int fmt, void* dst,
                                 int type, hipStream_t st) {
-  return fmt == kMxFp4 ? dequantize_f<kMxFp4>(q, s, n / 8, dst, type, st)
-                       : dequantize_f<kMxFp6>(q, s, n / 8, dst, type, st);
+  return fmt == kMxFp4 ? dequantize_f<kMxFp4>(q, s, n, dst, type, st)
+                       : dequantize_f<kMxFp6>(q, s, n, dst, type, st);
 }
 
 }  // namespace moe
