@@ -420,7 +420,7 @@ moe_status moe_mx_dequantize(const void* q, const uint8_t* s, int32_t fmt, int32
  * moe_mx_expert_gate_up, moe_mx_expert_down -- the halves of the expert FFN on microscaled
  * rows: as moe_expert_gate_up and moe_expert_down, with the row operand in codes and scales
  * and the products on the scaled matrix instructions (fp32 accumulation).
- *   pool     MXFP4 (other formats: MOE_ERR_UNSUPPORTED)
+ *   pool     MXFP4 (other formats: MOE_ERR_UNSUPPORTED), H and I below 2^27
  *   x_q, x_s planes of T rows of H values, in x_fmt (moe_mxfmt); row perm[pos] / k is read for
  *            bucket position pos
  *   h_q, h_s planes of T*k rows of I values in bucket order, in h_fmt
@@ -447,7 +447,8 @@ moe_status moe_mx_expert_ffn(const moe_pool* pool, const int32_t* slot_map, int3
 
 /*
  * The norms before and after the layer, on the residual stream resid [T][H] of resid_type
- * (MOE_T_BF16 or MOE_T_FP32). All arithmetic is fp32; each output is rounded once.
+ * (MOE_T_BF16 or MOE_T_FP32). All arithmetic is fp32; each output is rounded once. eps is
+ * finite and not negative.
  *
  * moe_add_norm -- the layer's entry:
  *   s = resid + scale * delta          (delta [T][H] of delta_type, bf16 or fp32; NULL: s = resid)

@@ -740,9 +740,12 @@ moe_status check_mx_rows(int32_t rows, int32_t K) {
 }
 
 // Sizes and parameters that both norms share; H as everywhere a multiple of 32.
-moe_status check_norm(int32_t T, int32_t H, int32_t k, int32_t resid_type, int32_t weight_type) {
+moe_status check_norm(int32_t T, int32_t H, int32_t k, int32_t resid_type, int32_t weight_type,
+                      float eps) {
   moe_status s = check_shape(T, H, moe::kMaxE, k);
   if (s != MOE_OK) return s;
+  if (!(eps >= 0.f) || eps > 3.4e38f)
+    return fail(MOE_ERR_INVALID_ARG, "eps = %g is negative or not finite", (double)eps);
   s = check_type("resid", resid_type, false);
   if (s != MOE_OK) return s;
   return check_type("weight", weight_type, false);
@@ -757,6 +760,9 @@ moe_status check_mx_product(const moe_pool* pool, const int32_t* slot_map, int32
   if (pool->fmt != MOE_W_MXFP4)
     return fail(MOE_ERR_UNSUPPORTED, "products on microscaled rows need an MXFP4 pool, not format %d",
                 pool->fmt);
+  // the kernels step through a row group's units in 32 bits: 256 bytes a block, two groups
+  if (pool->H >= 1 << 27 || pool->I >= 1 << 27)
+    return fail(MOE_ERR_INVALID_ARG, "H = %d, I = %d, limit 2^27", pool->H, pool->I);
   return check_mx(fmt, pool->H);
 }
 
@@ -897,7 +903,7 @@ moe_status moe_add_norm(const void* resid, int32_t resid_type, const void* delta
                         int32_t delta_type, float scale, const void* weight, int32_t weight_type,
                         float eps, int32_t T, int32_t H, void* resid_out, uint16_t* x,
                         void* stream) {
-  moe_status s = check_norm(T, H, 1, resid_type, weight_type);
+  moe_status s = check_norm(T, H, 1, resid_type, weight_type, eps);
   if (s != MOE_OK) return s;
   if (delta != nullptr && (s = check_type("delta", delta_type, false)) != MOE_OK) return s;
   if (T == 0) return ok();
@@ -927,7 +933,7 @@ moe_status moe_combine_norm(const float* y, const int32_t* inv_perm, const float
                             int32_t gate_rows, float scale, const void* next_weight,
                             int32_t weight_type, float eps, void* resid_out, uint16_t* x,
                             void* stream) {
-  moe_status s = check_norm(T, H, k, resid_type, weight_type);
+  moe_status s = check_norm(T, H, k, resid_type, weight_type, eps);
   if (s != MOE_OK) return s;
   if (gate != nullptr && gate_rows != 1 && gate_rows != T)
     return fail(MOE_ERR_INVALID_ARG, "gate_rows = %d, neither 1 nor T = %d", gate_rows, T);

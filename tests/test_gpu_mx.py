@@ -235,6 +235,35 @@ def test_products_wide(fmt, path):
 
 
 @pytest.mark.parametrize("path", [qm.PATH_GEMV, qm.PATH_GROUPED])
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T", [9, 150, 450])
+def test_products_long_rows(T, fmt, path):
+    """Rows of more than 128 blocks, odd in number, on every tile height."""
+    p = Problem(T, 4128, 4192, 2, 1, fmt, seed=T)
+    p.check_gate_up(p.gate_up(path=path))
+    p.check_down(p.down(path=path))
+
+
+@pytest.mark.parametrize("path", [qm.PATH_GEMV, qm.PATH_GROUPED])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_scales_far_apart(fmt, path):
+    """Neighbouring blocks' scales 2^-60 to 2^59: the bound is on sum |w a| all the same."""
+    p = Problem(70, 288, 352, 3, 2, fmt, seed=4, scale_spread=60)
+    p.check_down(p.down(path=path))
+
+
+@pytest.mark.parametrize("T", [2, 90])
+def test_a_stream_of_the_callers(T):
+    p = Problem(T, 256, 160, 8, 2, "mxfp4")
+    h, y = p.gate_up(), p.down()
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    h2, y2 = p.gate_up(stream=st), p.down(stream=st)
+    st.synchronize()
+    assert torch.equal(h, h2) and torch.equal(y, y2)
+
+
+@pytest.mark.parametrize("path", [qm.PATH_GEMV, qm.PATH_GROUPED])
 def test_one_expert_twice_for_a_token(path):
     """16 tokens that name one expert in every choice: 64 rows of it on the few-token path."""
     p = Problem(16, 96, 64, 4, 4, "mxfp6", ids=torch.full((16, 4), 2))

@@ -148,6 +148,8 @@ def test_product_refusals(lib):
             assert call(**bad) == INVALID, bad
             assert lib.moe_last_error()
         assert call(T=0, q=None, s=None, sm=None, off=None) == OK
+        assert call(pool=_pool(H=1 << 27, I=32), T=1, k=1) == INVALID
+        assert call(pool=_pool(H=32, I=1 << 27), T=1, k=1) == INVALID
     assert gate_up(perm=None) == INVALID and gate_up(h=None) == INVALID
     assert down(y=None) == INVALID and down(y=ODD) == INVALID
     for bad in (dict(q=None), dict(s=None), dict(perm=None), dict(h=None), dict(hq=None),
@@ -159,26 +161,27 @@ def test_product_refusals(lib):
 
 
 def test_norm_refusals(lib):
-    def add(r=FAKE, rt=1, dl=FAKE, dt=1, w=FAKE, wt=1, T=4, H=64, out=FAKE, x=FAKE):
-        return lib.moe_add_norm(r, rt, dl, dt, 1.0, w, wt, 1e-6, T, H, out, x, None)
+    def add(r=FAKE, rt=1, dl=FAKE, dt=1, w=FAKE, wt=1, T=4, H=64, out=FAKE, x=FAKE, eps=1e-6):
+        return lib.moe_add_norm(r, rt, dl, dt, 1.0, w, wt, eps, T, H, out, x, None)
 
     for bad in (dict(rt=2), dict(rt=0), dict(dt=2), dict(wt=2), dict(wt=9)):
         assert add(**bad) == UNSUPPORTED, bad
     for bad in (dict(T=-1), dict(H=48), dict(H=0), dict(r=None), dict(r=ODD), dict(dl=ODD),
-                dict(w=None), dict(x=None), dict(out=None), dict(out=ODD)):
+                dict(w=None), dict(x=None), dict(out=None), dict(out=ODD), dict(eps=-1e-6),
+                dict(eps=float("nan")), dict(eps=float("inf"))):
         assert add(**bad) == INVALID, bad
     assert add(T=0, r=None, w=None, x=None, out=None) == OK
 
     def comb(y=FAKE, ip=FAKE, w=FAKE, T=4, k=2, H=64, r=FAKE, rt=1, post=None, gate=None, gr=1,
-             nw=FAKE, wt=1, out=FAKE, x=FAKE):
-        return lib.moe_combine_norm(y, ip, w, T, k, H, r, rt, post, gate, gr, 1.0, nw, wt, 1e-6,
+             nw=FAKE, wt=1, out=FAKE, x=FAKE, eps=1e-6):
+        return lib.moe_combine_norm(y, ip, w, T, k, H, r, rt, post, gate, gr, 1.0, nw, wt, eps,
                                     out, x, None)
 
     assert comb(rt=2) == UNSUPPORTED and comb(wt=2) == UNSUPPORTED
     for bad in (dict(T=-1), dict(H=33), dict(k=0), dict(k=9), dict(y=None), dict(y=ODD),
                 dict(ip=None), dict(w=None), dict(r=None), dict(out=None), dict(x=None),
                 dict(nw=None), dict(post=ODD), dict(gate=ODD), dict(gate=FAKE, gr=2),
-                dict(gate=FAKE, gr=0), dict(nw=ODD)):
+                dict(gate=FAKE, gr=0), dict(nw=ODD), dict(eps=-1.0), dict(eps=float("nan"))):
         assert comb(**bad) == INVALID, bad
         assert lib.moe_last_error()
     assert comb(T=0, y=None, ip=None, r=None) == OK
