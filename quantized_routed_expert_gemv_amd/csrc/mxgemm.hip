@@ -175,8 +175,6 @@ hipError_t launch_gemv_t(const MxProduct& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-constexpr int kGemmThreads = 256;
-constexpr int kGemmCols = 256;   // weight rows a tile (gated: half of them gate, half up)
 constexpr int kStepBlocks = 8;    // blocks of K a step: four matrix instructions deep
 constexpr int kSlices = kStepBlocks / 2;
 constexpr int kSuperRows = 16, kSuperCols = 4; // tiles of a run, by rows and columns
@@ -263,28 +261,35 @@ __device__ bool find_tile(const MxProduct& p, int bm, int mt, int* e, int* m0, i
   return *e >= 0;
 }
 
-// Many rows: tiles of 32 MF bucket rows x 256 weight rows; 4 waves, each all rows by 64 weight
-// rows (gated: 32 gate and the same 32 up, so SwiGLU stays in registers). Weight blocks go
-// from the pool straight to the registers of the one wave that uses them (the pool's unit
+// Many rows: tiles of 32 MF bucket rows x 64 NW weight rows; NW waves, each all rows by 64
+// weight rows (gated: 32 gate and the same 32 up, so SwiGLU stays in registers). Weight blocks
+// go from the pool straight to the registers of the one wave that uses them (the pool's unit
 // order is the operand's); the gathered rows are shared by the waves and pass through
 // registers to one of two LDS buffers. Both are loaded one step of 256 K ahead: a row's 128
 // bytes of MXFP4 codes are then one whole cache line, where half steps asked L2 for every
 // line twice. Row scales, one byte a block, come 128 blocks at a time for the same reason.
-template <int FMT, bool GATED, int MF>
-__global__ __launch_bounds__(kGemmThreads, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k_mx_gemm(MxProduct p, int n_mtiles, int n_ntiles) {
+// Measured: gate/up, 16384 tokens, H = I = 2880, 4 of 32 experts: MXFP4 0.73-0.77 ms (2.8-3.0
+// PFLOP/s), MXFP6 0.90 ms. The chip's power bounds it: the clock falls from 2.4 to 1.4-1.8 GHz
+// with the matrix pipes busy 43-47% of the time, and tiles of 128 rows by four or eight waves
+// or of 256 rows all gain 3.6 PFLOP/s over a longer K; with the loads left out it is 5.3, at
+// what the instruction sustains on such operands.
+template <int FMT, bool GATED, int MF, int NW>
+__global__ __launch_bounds__(kWave * NW, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k_mx_gemm(
+    MxProduct p, int n_mtiles, int n_ntiles) {
+  constexpr int kThreads = kWave * NW, kCols = 64 * NW;   // weight rows a tile
   constexpr int BM = 32 * MF;
-  constexpr int TN = GATED ? kGemmCols / 2 : kGemmCols;   // output columns a tile
+  constexpr int TN = GATED ? kCols / 2 : kCols;   // output columns a tile
   constexpr int kBytes = mx_block_bytes(FMT);
-  constexpr int NB = BM * kStepBlocks / kGemmThreads;   // row blocks a thread loads a step
+  constexpr int NB = BM * kStepBlocks / kThreads;   // row blocks a thread loads a step
   static_assert(NB >= 1, "a thread loads whole blocks");
   // two buffers of rows; the epilogue's fragments take their place
   constexpr int kBuf = BM * kStepBlocks * kBytes;
   constexpr int kPiece = GATED ? 2 : 4;                    // bytes of an output
   constexpr int kOutRow = 32 * kPiece + 16;                // padded: no bank conflicts
-  constexpr int kTurn = kGemmThreads / kWave * 32 * kOutRow;
+  constexpr int kTurn = kThreads / kWave * 32 * kOutRow;
   __shared__ __attribute__((aligned(16))) uint8_t lds_q[2 * kBuf > kTurn ? 2 * kBuf : kTurn];
   __shared__ __attribute__((aligned(16))) uint8_t lds_s[BM * kScaleRow];
-  __shared__ int part[kGemmThreads / kWave];
+  __shared__ int part[kThreads / kWave];
   __shared__ int found[3];
   // XCD-aware tile order: workgroups go to the 8 XCDs in turn, and each XCD gets runs of 64
   // tiles that share their rows and weights in its L2
@@ -303,7 +308,7 @@ __global__ __launch_bounds__(kGemmThreads, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k
   const int n0 = nt * TN;
   const int slot = p.slot_map[e];
   if (slot < 0 || slot >= p.n_slots) {
-    for (int t = threadIdx.x; t < BM * TN; t += kGemmThreads) {
+    for (int t = threadIdx.x; t < BM * TN; t += kThreads) {
       const int pos = m0 + t / TN, n = n0 + t % TN;
       if (pos < mend && n < p.N) {
         if (GATED) p.h[(int64_t)pos * p.N + n] = 0;
@@ -319,12 +324,12 @@ __global__ __launch_bounds__(kGemmThreads, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int half = lane >> 5;
 
-  // ---- rows: thread t carries block t % 8 of tile rows t / 8 + 32 j
+  // ---- rows: thread t carries block t % 8 of tile rows t / 8 + kThreads / 8 j
   const int rb = threadIdx.x & (kStepBlocks - 1);
   const uint8_t* rq[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
-    const int r = threadIdx.x / kStepBlocks + kGemmThreads / kStepBlocks * j;
+    const int r = threadIdx.x / kStepBlocks + kThreads / kStepBlocks * j;
     const int64_t row = source_row<GATED>(p, min(m0 + r, mend - 1));   // past the end: the last
     rq[j] = p.q + row * nb * kBytes;
   }
@@ -359,7 +364,7 @@ __global__ __launch_bounds__(kGemmThreads, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k
     auto all = [&](bool ok) {
 #pragma unroll
       for (int j = 0; j < NB; ++j)
-        rows[j].store(to + place + j * kRows32 * 16, to + place_tail + j * kRows32 * 8, ok);
+        rows[j].store(to + place + j * kThreads * 16, to + place_tail + j * kThreads * 8, ok);
     };
     if (kStepBlocks * (c + 1) <= nb) all(true);   // only a row's last step can be short
     else all(kStepBlocks * c + rb < nb);
@@ -379,7 +384,7 @@ __global__ __launch_bounds__(kGemmThreads, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k
   // so that a lane's four of a step are one dword. The rows lie at any byte, so a row's last
   // dwords are gathered byte by byte.
   auto load_scales = [&](int b0) {
-    constexpr int kParts = kGemmThreads / BM;
+    constexpr int kParts = kThreads / BM;
     const int r = threadIdx.x / kParts;
     const uint8_t* src = p.s + (int64_t)source_row<GATED>(p, min(m0 + r, mend - 1)) * nb + b0;
     const int n = min(nb - b0, kScaleBlocks);
@@ -513,31 +518,39 @@ __global__ __launch_bounds__(kGemmThreads, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k
   }
 }
 
-template <int FMT, bool GATED, int MF>
+template <int FMT, bool GATED, int MF, int NW>
 hipError_t launch_gemm_t(const MxProduct& p, hipStream_t st) {
-  constexpr int BM = 32 * MF, TN = GATED ? kGemmCols / 2 : kGemmCols;
+  constexpr int BM = 32 * MF, kCols = 64 * NW, TN = GATED ? kCols / 2 : kCols;
   const int pairs = p.T * p.k;
   const int n_mtiles = (pairs + BM - 1) / BM + min(p.E, pairs);   // most that can be
   const int n_ntiles = (p.N + TN - 1) / TN;
   const int64_t grid = ((int64_t)n_mtiles * n_ntiles + 511) / 512 * 512;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((k_mx_gemm<FMT, GATED, MF>), dim3((unsigned)grid), dim3(kGemmThreads), 0, st, p,
+  hipLaunchKernelGGL((k_mx_gemm<FMT, GATED, MF, NW>), dim3((unsigned)grid), dim3(kWave * NW), 0, st, p,
                      n_mtiles, n_ntiles);
   return hipGetLastError();
 }
 
-// Rows a tile, by the mean rows of an expert: a tall tile reads the weights less often and
-// feeds more products per operand read, a low one leaves fewer of its rows empty and puts more
-// workgroups on a CU. Measured, gate/up us with 32 / 64 / 128 rows: H = I = 2880, 32 experts,
-// MXFP6, mean 41: 68 / 83 / 84; 125: 119 / 117 / 123; 250: 193 / 176 / 164; H 2048, I 768, 128
-// experts, MXFP4, mean 62: 44 / 46 / 53; 125: 70 / 60 / 71; 512: - / 175 / 176.
+// Rows a tile. A tall tile reads the weights less often and feeds more products per operand
+// read; a low one leaves fewer of its rows empty, and there are more of them to fill the CUs.
+// So by the mean rows of an expert: gate/up us with 32 / 64 / 128 rows, H = I = 2880, 32
+// experts, MXFP6, mean 41: 68 / 83 / 84; 125: 119 / 117 / 123; 250: 193 / 176 / 164; H 2048,
+// I 768, 128 experts, MXFP4, mean 62: 44 / 46 / 53; 125: 70 / 60 / 71. And by the tiles that
+// there are (256 CUs hold 512 of 128 rows at once): MXFP4, down, 188 tiles of 128 rows,
+// H 1024, I 1536: 18 / 14 / 22; 63 tiles, H = I = 1024: 9.0 / 12 / 16; gate/up, 564 tiles:
+// 32 / 29 / 31; 1000 tiles, H 256, I 512: 26 / 24 / 23.
+// MXFP6 rows take eight waves a tile of 128 x 512: half the row bytes and registers a wave
+// (four waves spill): gate/up, 16384 tokens, H = I = 2880: 939 against 900 us; 4096 tokens,
+// H 4096, I 14336: 763 against 711. MXFP4: 774 against 787 and 627 against 624, so four.
 template <int FMT, bool GATED>
 hipError_t launch_t(const MxProduct& p, bool gemv, hipStream_t st) {
   if (gemv) return launch_gemv_t<FMT, GATED>(p, st);
-  const int mean = p.T * p.k / p.E;
-  if (mean > 200) return launch_gemm_t<FMT, GATED, 4>(p, st);
-  if (mean > 64) return launch_gemm_t<FMT, GATED, 2>(p, st);
-  return launch_gemm_t<FMT, GATED, 1>(p, st);
+  const int pairs = p.T * p.k, mean = pairs / p.E;
+  const int64_t n_ntiles = (p.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256);
+  if (mean > 200 && pairs / 128 * n_ntiles >= 768)
+    return launch_gemm_t<FMT, GATED, 4, FMT == kMxFp6 ? 8 : 4>(p, st);
+  if (mean > 64 && pairs / 64 * n_ntiles >= 300) return launch_gemm_t<FMT, GATED, 2, 4>(p, st);
+  return launch_gemm_t<FMT, GATED, 1, 4>(p, st);
 }
 
 }  // namespace

@@ -238,10 +238,45 @@ def test_products_wide(fmt, path):
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("T", [9, 150, 450])
 def test_products_long_rows(T, fmt, path):
-    """Rows of more than 128 blocks, odd in number, on every tile height."""
+    """Rows of more than 128 blocks, odd in number."""
     p = Problem(T, 4128, 4192, 2, 1, fmt, seed=T)
     p.check_gate_up(p.gate_up(path=path))
     p.check_down(p.down(path=path))
+
+
+# Enough tiles for the taller ones: 64 rows (T = 700, 32 experts of 87 rows on average) and 128
+# (T = 6500, 8 experts of 1625), for the product whose output is the wide one; short rows, rows
+# whose last step is ragged, and rows of more than 128 blocks.
+TALL = [(700, 160, 1056, 32, 4), (700, 2080, 160, 32, 4), (700, 4192, 1056, 32, 4),
+        (700, 2080, 4192, 32, 4), (6500, 32, 1056, 8, 2), (6500, 2080, 32, 8, 2),
+        (6500, 288, 1056, 8, 2), (6500, 2080, 352, 8, 2), (6500, 4192, 1056, 8, 2),
+        (6500, 2080, 4192, 8, 2)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,H,I,E,k", TALL)
+def test_products_tall(T, H, I, E, k, fmt):
+    """A miss, an expert whole, a NaN block, and rows past the last bucket."""
+    p = Problem(T, H, I, E, k, fmt, seed=H + I, missing=(3,))
+    n = T * k
+    if I == 1056:
+        h = p.gate_up()
+        p.check_gate_up(h, {1, 3})
+        p.xd[1][5, H // 32 - 1] = 255
+        h2 = p.gate_up()
+        hit = ((p.perm // k) == 5) & (h.abs().sum(1) > 0)   # but for the pair that misses
+        assert 1 <= int(hit.sum()) <= k
+        assert torch.isnan(h2[hit]).all() and torch.equal(h2[~hit], h[~hit])
+    else:
+        y = p.down()
+        p.check_down(y, {1, 3})
+        p.hd[1][n - 1, I // 32 - 1] = 255
+        y2 = p.down()
+        assert torch.isnan(y2[n - 1]).all() and torch.equal(y2[:-1], y[:-1])
+        p.offsets.clamp_(max=n - 9)
+        y2.fill_(7)
+        p.down(y=y2)
+        assert bool((y2[n - 9:] == 7).all()) and torch.equal(y2[:n - 9], y[:n - 9])
 
 
 @pytest.mark.parametrize("path", [qm.PATH_GEMV, qm.PATH_GROUPED])
