@@ -268,8 +268,8 @@ __device__ bool find_tile(const MxProduct& p, int bm, int mt, int* e, int* m0, i
 // registers to one of two LDS buffers. Both are loaded one step of 256 K ahead: a row's 128
 // bytes of MXFP4 codes are then one whole cache line, where half steps asked L2 for every
 // line twice. Row scales, one byte a block, come 128 blocks at a time for the same reason.
-// Measured: gate/up, 16384 tokens, H = I = 2880, 4 of 32 experts: MXFP4 0.73-0.77 ms (2.8-3.0
-// PFLOP/s), MXFP6 0.90 ms. The chip's power bounds it: the clock falls from 2.4 to 1.4-1.8 GHz
+// Measured: gate/up, 16384 tokens, H = I = 2880, 4 of 32 experts: MXFP4 0.68 ms (3.2
+// PFLOP/s), MXFP6 0.80 ms. The chip's power bounds it: the clock falls from 2.4 to 1.4-1.8 GHz
 // with the matrix pipes busy 43-47% of the time, and tiles of 128 rows by four or eight waves
 // or of 256 rows all gain 3.6 PFLOP/s over a longer K; with the loads left out it is 5.3, at
 // what the instruction sustains on such operands.
@@ -432,7 +432,9 @@ __global__ __launch_bounds__(kWave * NW, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k_m
 #pragma unroll
   for (int s = 0; s < kSlices; ++s) load_weights(0, s);
   put(0);
-  for (int c = 0; c < nsteps; ++c) {
+  // put(0) is seen behind the barrier that the first scales bring
+  uint32_t as[MF];
+  auto read_scales = [&](int c) {   // those of 128 blocks on are loaded where their first is due
     const int sb = kStepBlocks * c % kScaleBlocks;
     if (sb == 0) {
       int b0 = kStepBlocks * c;
@@ -440,43 +442,61 @@ __global__ __launch_bounds__(kWave * NW, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k_m
       load_scales(b0);
       __syncthreads();
     }
-    if (c + 1 < nsteps) load_rows(c + 1);
-    __builtin_amdgcn_sched_barrier(0);   // the loads go first, what waits for them last
-    uint32_t as[MF];
 #pragma unroll
     for (int m = 0; m < MF; ++m)
       as[m] = *(const uint32_t*)(lds_s + (32 * m + (lane & 31)) * kScaleRow + sb + 4 * half);
-    auto slice = [&](auto sl) {
-      constexpr int s = decltype(sl)::value;
-      uint32_t sw[2];
+  };
+  auto products = [&](int c, auto sl) {   // of one slice, a pair of blocks
+    constexpr int s = decltype(sl)::value;
+    uint32_t wscale[2];
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      asm volatile("" : "+v"(wsc[f][s]));   // waited for here, not where the step begins
+      wscale[f] = wsc[f][s] >> (8 * (lane & 3));
+    }
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+      const v8i a = read_block((c & 1) * kBuf, s, m);
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        asm volatile("" : "+v"(wsc[f][s]));   // waited for here, not where the step begins
-        sw[f] = wsc[f][s] >> (8 * (lane & 3));
+        const v8i w = {(int)wgt[f][s][0], (int)wgt[f][s][1], (int)wgt[f][s][2],
+                       (int)wgt[f][s][3], 0, 0, 0, 0};
+        acc[m][f] = mma32<FMT, s>(w, wscale[f], a, as[m], acc[m][f]);
       }
+    }
+    // the products stay in their slice, and one slice's operands at a time in registers:
+    // without this the compiler reads every slice's first and spills
 #pragma unroll
-      for (int m = 0; m < MF; ++m) {
-        const v8i a = read_block((c & 1) * kBuf, s, m);
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const v8i w = {(int)wgt[f][s][0], (int)wgt[f][s][1], (int)wgt[f][s][2],
-                         (int)wgt[f][s][3], 0, 0, 0, 0};
-          acc[m][f] = mma32<FMT, s>(w, sw[f], a, as[m], acc[m][f]);
-        }
-      }
-      // the products stay in their slice, and one slice's operands at a time in registers:
-      // without this the compiler reads every slice's first and spills
-#pragma unroll
-      for (int m = 0; m < MF; ++m) asm volatile("" : "+v"(acc[m][0]), "+v"(acc[m][1]));
-      load_weights(min(c + 1, nsteps - 1), s);
-    };
-    slice(std::integral_constant<int, 0>{});
-    slice(std::integral_constant<int, 1>{});
-    slice(std::integral_constant<int, 2>{});
-    slice(std::integral_constant<int, 3>{});
-    if (c + 1 < nsteps) put(c + 1);
+    for (int m = 0; m < MF; ++m) asm volatile("" : "+v"(acc[m][0]), "+v"(acc[m][1]));
+  };
+  typedef std::integral_constant<int, 0> S0;
+  typedef std::integral_constant<int, 1> S1;
+  typedef std::integral_constant<int, 2> S2;
+  typedef std::integral_constant<int, 3> S3;
+  const int last = nsteps - 1;
+  for (int c = 0; c < last; ++c) {
+    read_scales(c);
+    load_rows(c + 1);
+    __builtin_amdgcn_sched_barrier(0);   // the loads go first, what waits for them last
+    products(c, S0{});
+    load_weights(c + 1, 0);
+    products(c, S1{});
+    load_weights(c + 1, 1);
+    products(c, S2{});
+    load_weights(c + 1, 2);
+    products(c, S3{});
+    load_weights(c + 1, 3);
+    put(c + 1);
     __syncthreads();
   }
+  // the last step, of 1 to kStepBlocks blocks
+  const int left = nb - kStepBlocks * last;
+  read_scales(last);
+  products(last, S0{});
+  if (left > 2) products(last, S1{});
+  if (left > 4) products(last, S2{});
+  if (left > 6) products(last, S3{});
+  __syncthreads();   // the rows' buffers have been read
   // ---- a lane holds, of one bucket row, 4 groups of 4 neighbouring columns a fragment; each
   // wave turns its fragments round in LDS of its own (the rows' buffers, no longer read), so
   // that the stores are whole cache lines of a row (gated: halves) and not 16-byte pieces
