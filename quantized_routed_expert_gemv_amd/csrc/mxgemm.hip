@@ -74,7 +74,9 @@ constexpr int kGemvThreads = 256;
 // Few rows: the weights' bytes bound it. One workgroup a 16-row group of one active expert;
 // its 4 waves share the row group's blocks, 4 at a time (one coalesced KiB), and add their
 // sums in LDS in wave order. Up to 16 rows of the expert ride along as the instruction's
-// columns; more are taken 16 at a time.
+// columns; more are taken 16 at a time. Measured: gate/up of one token, H = I = 2880, 4
+// experts: 7.7 us for 35 MB (4.6 TB/s); down of four tokens, H 4096, I 14336: 33 us for about
+// 5 experts' 156 MB.
 template <int FMT, bool GATED>
 __global__ __launch_bounds__(kGemvThreads) void k_mx_gemv(MxProduct p) {
   constexpr int NM = GATED ? 2 : 1;
