@@ -540,6 +540,16 @@ def _mx_planes(q, s, fmt, rows, K, names, like):
     _tensor(s, (torch.uint8,), (*rows, K // 32), names[1], like)
 
 
+def _rows(t, dtype, shape, name, like):
+    """The given output, checked, or a new one."""
+    if t is None:
+        if dtype == like.dtype and shape == like.shape:
+            return torch.empty_like(like)
+        return like.new_empty(shape, dtype=dtype)
+    _tensor(t, (dtype,), shape, name, like)
+    return t
+
+
 def mx_quantize(x, fmt: str = "mxfp4", q=None, s=None, stream=None):
     """x bf16, fp16 or fp32 [..., K] -> (codes uint8 [..., mx_row_bytes], scales uint8 [..., K/32]).
 
@@ -547,12 +557,9 @@ def mx_quantize(x, fmt: str = "mxfp4", q=None, s=None, stream=None):
     Pool.from_canonical and pool_pack take."""
     _one_of("fmt", fmt, _MX)
     *rows, K = x.shape
-    _tensor(x, tuple(_DT), x.shape, "x", x)
-    if q is None:
-        q = torch.empty((*rows, mx_row_bytes(fmt, K)), dtype=torch.uint8, device=x.device)
-    if s is None:
-        s = torch.empty((*rows, K // 32), dtype=torch.uint8, device=x.device)
-    _mx_planes(q, s, fmt, rows, K, ("q", "s"), x)
+    _tensor(x, _DT, x.shape, "x", x)
+    q = _rows(q, torch.uint8, (*rows, mx_row_bytes(fmt, K)), "q", x)
+    s = _rows(s, torch.uint8, (*rows, K // 32), "s", x)
     _run(_mx_quantize, x, stream, _addr(x), _DT[x.dtype], x.numel() // max(K, 1), K, _MX[fmt],
          _addr(q), _addr(s))
     return q, s
@@ -564,9 +571,7 @@ def mx_dequantize(q, s, fmt: str = "mxfp4", dtype=torch.bfloat16, out=None, stre
     *rows, nb = s.shape
     K = 32 * nb
     _mx_planes(q, s, fmt, rows, K, ("q", "s"), q)
-    if out is None:
-        out = torch.empty((*rows, K), dtype=dtype, device=q.device)
-    _tensor(out, (dtype,), (*rows, K), "out", q)
+    out = _rows(out, dtype, (*rows, K), "out", q)
     _run(_mx_dequantize, q, stream, _addr(q), _addr(s), _MX[fmt], s.numel() // max(nb, 1), K,
          _addr(out), _DT[dtype])
     return out
@@ -585,14 +590,6 @@ def _mx_checks(pool, slot_map, T, k, offsets, perm, err_flags, like):
     if pool.planes["gate_q"].device != like.device:
         raise ValueError(f"pool: on {pool.planes['gate_q'].device}, expected {like.device}")
     return E
-
-
-def _rows(t, dtype, shape, name, like):
-    """The given output, checked, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    _tensor(t, (dtype,), shape, name, like)
-    return t
 
 
 def mx_expert_gate_up(pool: Pool, slot_map, x_q, x_s, fmt: str, k: int, offsets, perm, h=None,
