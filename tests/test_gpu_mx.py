@@ -422,6 +422,37 @@ def test_ffn_is_its_three_calls(T):
     assert torch.equal(h, h1) and torch.equal(y, y1)
 
 
+def test_outputs_of_the_callers():
+    """Every output given; the flag of a slot outside the pool comes out of the fused call too."""
+    T, H, I, k = 6, 96, 64, 2
+    p = Problem(T, H, I, 4, k, "mxfp6", ids=torch.tensor([[0, 2]]).repeat(T, 1))
+    x = torch.randn(T, H, device="cuda").bfloat16()
+    new = lambda *s, dt=torch.uint8: torch.empty(s, dtype=dt, device="cuda")  # noqa: E731
+    q, s_ = new(T, qm.mx_row_bytes("mxfp6", H)), new(T, H // 32)
+    assert qm.mx_quantize(x, "mxfp6", q=q, s=s_)[0] is q
+    out = new(T, H, dt=torch.float32)
+    assert qm.mx_dequantize(q, s_, "mxfp6", torch.float32, out=out) is out
+    assert torch.equal(out, qm.mx_dequantize(q, s_, "mxfp6", torch.float32))
+    h, y = new(T * k, I, dt=torch.bfloat16), new(T * k, H, dt=torch.float32)
+    hq, hs = new(T * k, qm.mx_row_bytes("mxfp4", I)), new(T * k, I // 32)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = (p.pool, p.slot_map, q, s_, "mxfp6", k, p.offsets, p.perm)
+    got = qm.mx_expert_ffn(*args, h_fmt="mxfp4", h=h, h_q=hq, h_s=hs, y=y, err_flags=err)
+    assert got[0] is h and got[1] is y and int(err) == 0
+    h1, y1 = qm.mx_expert_ffn(*args, h_fmt="mxfp4")
+    assert torch.equal(h, h1) and torch.equal(y, y1)
+    assert torch.equal(hq, qm.mx_quantize(h, "mxfp4")[0])
+    p.slot_map[2] = 1000
+    h2, y2 = qm.mx_expert_ffn(*args, h_fmt="mxfp4", err_flags=err)
+    half = int(p.offsets[1])
+    assert int(err) == 1 and torch.equal(y2[:half], y[:half]) and not y2[half:].any()
+    assert not h2[half:].any()
+    with pytest.raises(qm.MoeError):   # a row further on: codes at 8 bytes, not at 16
+        qm.mx_dequantize(new(T + 1, 72)[1:], s_, "mxfp6")
+    with pytest.raises(ValueError):
+        qm.mx_quantize(x, "mxfp6", q=q[:, :-1])
+
+
 def test_no_tokens():
     p = Problem(3, 64, 32, 4, 2, "mxfp4")
     z = torch.zeros(5, dtype=torch.int32, device="cuda")

@@ -119,6 +119,22 @@ def test_positions_outside_add_nothing():
     assert torch.equal(out, r)
 
 
+@pytest.mark.parametrize("rt", [BF, F32])
+def test_outputs_of_the_callers(rt):
+    r, w = torch.randn(5, 96, device="cuda").to(rt), torch.ones(96, device="cuda")
+    out, x = torch.empty_like(r), torch.empty(5, 96, dtype=BF, device="cuda")
+    got = qm.add_norm(r, w, resid_out=out, x=x)      # without delta the stream is copied
+    assert got[0] is x and got[1] is out and torch.equal(out, r)
+    assert torch.equal(x, qm.add_norm(r, w)[0])
+    assert torch.equal(qm.add_norm(r, w, delta=r, scale=0.0)[0], x)
+    y, inv = torch.randn(5, 96, device="cuda"), torch.arange(5, dtype=torch.int32, device="cuda")
+    one = torch.ones(5, 1, device="cuda")
+    got = qm.combine_norm(y, inv, one, r, next_weight=w, resid_out=out, x=x)
+    assert got[0] is out and got[1] is x
+    want, _ = qm.combine_norm(y, inv, one, r, gate=torch.ones(5, 96, device="cuda"))
+    assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("H", [64, 2880, 9216])
 def test_zero_and_nan_rows(H):
     r = torch.randn(4, H, device="cuda")
