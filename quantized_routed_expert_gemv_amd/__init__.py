@@ -495,6 +495,7 @@ class LayerCall:
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream   # a stream handle without a Stream object
+_current_device = torch._C._cuda_getDevice           # torch is initialised: tensors are there
 
 
 def _one_of(name, value, choices):
@@ -504,8 +505,8 @@ def _one_of(name, value, choices):
 
 def _tensor(t, dtypes, shape, name, like):
     """A contiguous device tensor of one of `dtypes`, on the device of `like`."""
-    if t.dtype in dtypes and t.shape == shape and t.is_cuda and t.device == like.device and \
-            t.is_contiguous():
+    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and \
+            t.get_device() == like.get_device() >= 0:
         return
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
@@ -520,13 +521,15 @@ def _addr(t):
 def _run(fn, like, stream, *args):
     """Calls fn(*args, stream) with the device of `like` current, on that device's current
     stream unless one is given."""
-    index = like.device.index
+    index = like.get_device()
     handle = _raw_stream(index) if stream is None else stream.cuda_stream
-    if index == torch.cuda.current_device():
-        _check(fn(*args, handle))
+    if index == _current_device():
+        status = fn(*args, handle)
     else:
         with torch.cuda.device(index):
-            _check(fn(*args, handle))
+            status = fn(*args, handle)
+    if status:
+        _check(status)
 
 
 def mx_row_bytes(fmt: str, K: int) -> int:
