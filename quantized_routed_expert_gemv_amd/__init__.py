@@ -492,6 +492,9 @@ class LayerCall:
 
 
 # --------------------------------------------- microscaled rows, and the block's two ends
+#
+# stream: the torch stream to run on, of the tensors' device (default: the current one). Outputs
+# that a call makes are that stream's, as tensors made under `with torch.cuda.stream(stream)` are.
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream   # a stream handle without a Stream object
@@ -522,7 +525,12 @@ def _run(fn, like, stream, *args):
     """Calls fn(*args, stream) with the device of `like` current, on that device's current
     stream unless one is given."""
     index = like.get_device()
-    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    if stream is None:
+        handle = _raw_stream(index)
+    else:
+        if stream.device != like.device:
+            raise ValueError(f"stream: on {stream.device}, expected {like.device}")
+        handle = stream.cuda_stream
     if index == _current_device():
         status = fn(*args, handle)
     else:
@@ -543,14 +551,19 @@ def _mx_planes(q, s, fmt, rows, K, names, like):
     _tensor(s, (torch.uint8,), (*rows, K // 32), names[1], like)
 
 
-def _rows(t, dtype, shape, name, like):
-    """The given output, checked, or a new one."""
-    if t is None:
-        if dtype == like.dtype and shape == like.shape:
-            return torch.empty_like(like)
-        return like.new_empty(shape, dtype=dtype)
-    _tensor(t, (dtype,), shape, name, like)
-    return t
+def _rows(t, dtype, shape, name, like, stream):
+    """The given output, checked, or a new one. A new one belongs to the stream that writes it:
+    taken from another stream's memory it could still be in use there, and a temporary could be
+    handed out there again, as soon as the call returns, while this stream still uses it."""
+    if t is not None:
+        _tensor(t, (dtype,), shape, name, like)
+        return t
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return like.new_empty(shape, dtype=dtype)
+    if dtype == like.dtype and shape == like.shape:
+        return torch.empty_like(like)
+    return like.new_empty(shape, dtype=dtype)
 
 
 def mx_quantize(x, fmt: str = "mxfp4", q=None, s=None, stream=None):
@@ -561,8 +574,8 @@ def mx_quantize(x, fmt: str = "mxfp4", q=None, s=None, stream=None):
     _one_of("fmt", fmt, _MX)
     *rows, K = x.shape
     _tensor(x, _DT, x.shape, "x", x)
-    q = _rows(q, torch.uint8, (*rows, mx_row_bytes(fmt, K)), "q", x)
-    s = _rows(s, torch.uint8, (*rows, K // 32), "s", x)
+    q = _rows(q, torch.uint8, (*rows, mx_row_bytes(fmt, K)), "q", x, stream)
+    s = _rows(s, torch.uint8, (*rows, K // 32), "s", x, stream)
     _run(_mx_quantize, x, stream, _addr(x), _DT[x.dtype], x.numel() // max(K, 1), K, _MX[fmt],
          _addr(q), _addr(s))
     return q, s
@@ -574,7 +587,7 @@ def mx_dequantize(q, s, fmt: str = "mxfp4", dtype=torch.bfloat16, out=None, stre
     *rows, nb = s.shape
     K = 32 * nb
     _mx_planes(q, s, fmt, rows, K, ("q", "s"), q)
-    out = _rows(out, dtype, (*rows, K), "out", q)
+    out = _rows(out, dtype, (*rows, K), "out", q, stream)
     _run(_mx_dequantize, q, stream, _addr(q), _addr(s), _MX[fmt], s.numel() // max(nb, 1), K,
          _addr(out), _DT[dtype])
     return out
@@ -601,7 +614,7 @@ def mx_expert_gate_up(pool: Pool, slot_map, x_q, x_s, fmt: str, k: int, offsets,
     T = x_q.shape[0]
     _mx_planes(x_q, x_s, fmt, (T,), pool.H, ("x_q", "x_s"), x_q)
     E = _mx_checks(pool, slot_map, T, k, offsets, perm, err_flags, x_q)
-    h = _rows(h, torch.bfloat16, (T * k, pool.I), "h", x_q)
+    h = _rows(h, torch.bfloat16, (T * k, pool.I), "h", x_q, stream)
     _run(_mx_gate_up, x_q, stream, ctypes.byref(pool.struct), _addr(slot_map), E, _addr(x_q),
          _addr(x_s), _MX[fmt], T, k, _addr(offsets), _addr(perm), _addr(h), _addr(err_flags), path)
     return h
@@ -612,7 +625,7 @@ def mx_expert_down(pool: Pool, slot_map, T: int, k: int, offsets, h_q, h_s, fmt:
     """Microscaled rows (mx_quantize of h [T*k, I]) -> y fp32 [T*k, H] in bucket order."""
     _mx_planes(h_q, h_s, fmt, (T * k,), pool.I, ("h_q", "h_s"), h_q)
     E = _mx_checks(pool, slot_map, T, k, offsets, None, err_flags, h_q)
-    y = _rows(y, torch.float32, (T * k, pool.H), "y", h_q)
+    y = _rows(y, torch.float32, (T * k, pool.H), "y", h_q, stream)
     _run(_mx_down, h_q, stream, ctypes.byref(pool.struct), _addr(slot_map), E, _addr(h_q),
          _addr(h_s), _MX[fmt], T, k, _addr(offsets), _addr(y), _addr(err_flags), path)
     return y
@@ -627,10 +640,10 @@ def mx_expert_ffn(pool: Pool, slot_map, x_q, x_s, fmt: str, k: int, offsets, per
     _mx_planes(x_q, x_s, fmt, (T,), pool.H, ("x_q", "x_s"), x_q)
     _one_of("h_fmt", h_fmt, _MX)
     E = _mx_checks(pool, slot_map, T, k, offsets, perm, err_flags, x_q)
-    h = _rows(h, torch.bfloat16, (T * k, pool.I), "h", x_q)
-    h_q = _rows(h_q, torch.uint8, (T * k, mx_row_bytes(h_fmt, pool.I)), "h_q", x_q)
-    h_s = _rows(h_s, torch.uint8, (T * k, pool.I // 32), "h_s", x_q)
-    y = _rows(y, torch.float32, (T * k, pool.H), "y", x_q)
+    h = _rows(h, torch.bfloat16, (T * k, pool.I), "h", x_q, stream)
+    h_q = _rows(h_q, torch.uint8, (T * k, mx_row_bytes(h_fmt, pool.I)), "h_q", x_q, stream)
+    h_s = _rows(h_s, torch.uint8, (T * k, pool.I // 32), "h_s", x_q, stream)
+    y = _rows(y, torch.float32, (T * k, pool.H), "y", x_q, stream)
     _run(_mx_ffn, x_q, stream, ctypes.byref(pool.struct), _addr(slot_map), E, _addr(x_q),
          _addr(x_s), _MX[fmt], T, k, _addr(offsets), _addr(perm), _addr(h), _addr(h_q), _addr(h_s),
          _MX[h_fmt], _addr(y), _addr(err_flags), path)
@@ -653,8 +666,8 @@ def add_norm(resid, weight, eps: float = 1e-6, delta=None, scale: float = 1.0, r
     if delta is not None:
         _tensor(delta, _STREAM_TYPES, (T, H), "delta", resid)
     if delta is not None or resid_out is not None:
-        resid_out = _rows(resid_out, resid.dtype, (T, H), "resid_out", resid)
-    x = _rows(x, torch.bfloat16, (T, H), "x", resid)
+        resid_out = _rows(resid_out, resid.dtype, (T, H), "resid_out", resid, stream)
+    x = _rows(x, torch.bfloat16, (T, H), "x", resid, stream)
     _run(_add_norm, resid, stream, _addr(resid), _DT[resid.dtype], _addr(delta),
          0 if delta is None else _DT[delta.dtype], scale, _addr(weight), _DT[weight.dtype], eps, T,
          H, _addr(resid_out), _addr(x))
@@ -684,9 +697,9 @@ def combine_norm(y, inv_perm, w, resid, eps: float = 1e-6, post_weight=None, gat
                 raise TypeError("post_weight, gate and next_weight: more than one dtype")
     if next_weight is None and x is not None:
         raise ValueError("x: needs next_weight")
-    resid_out = _rows(resid_out, resid.dtype, (T, H), "resid_out", resid)
+    resid_out = _rows(resid_out, resid.dtype, (T, H), "resid_out", resid, stream)
     if next_weight is not None:
-        x = _rows(x, torch.bfloat16, (T, H), "x", resid)
+        x = _rows(x, torch.bfloat16, (T, H), "x", resid, stream)
     _run(_combine_norm, resid, stream, _addr(y), _addr(inv_perm), _addr(w), T, k, H, _addr(resid),
          _DT[resid.dtype], _addr(post_weight), _addr(gate),
          T if gate is not None and gate.dim() == 2 else 1, scale, _addr(next_weight),
