@@ -178,6 +178,7 @@ __global__ __launch_bounds__(1024) void k_block_norm_long(BlockNorm a) {
   constexpr int TH = 1024, NW = TH / kWave;
   __shared__ float red[NW];
   const int64_t t = blockIdx.x;
+  const uint32_t H = a.H;   // a column past the last, up to 2^31 + 4095, has to compare as such
   Choices ch;
   if constexpr (EXIT) ch = read_choices(a, t);
   auto combined = [&](int c) {
@@ -188,7 +189,7 @@ __global__ __launch_bounds__(1024) void k_block_norm_long(BlockNorm a) {
   float rs_post = 1.f;
   if (EXIT && a.post) {
     double ss = 0.;
-    for (int c = threadIdx.x * 4; c < a.H; c += TH * 4) ss += dot4(combined(c), 0.f);
+    for (uint32_t c = threadIdx.x * 4; c < H; c += TH * 4) ss += dot4(combined(c), 0.f);
     rs_post = rsqrtf(group_sum<NW>((float)ss, red) / a.H + a.eps);
   }
   auto value = [&](int c) {
@@ -207,10 +208,10 @@ __global__ __launch_bounds__(1024) void k_block_norm_long(BlockNorm a) {
   float rs = 1.f;
   if (a.x) {
     double ss = 0.;
-    for (int c = threadIdx.x * 4; c < a.H; c += TH * 4) ss += dot4(value(c), 0.f);
+    for (uint32_t c = threadIdx.x * 4; c < H; c += TH * 4) ss += dot4(value(c), 0.f);
     rs = rsqrtf(group_sum<NW>((float)ss, red) / a.H + a.eps);
   }
-  for (int c = threadIdx.x * 4; c < a.H; c += TH * 4) {
+  for (uint32_t c = threadIdx.x * 4; c < H; c += TH * 4) {
     const f32x4 s = value(c);
     if (a.resid_out) store4((R*)a.resid_out + t * a.H + c, s);
     if (a.x) store4(a.x + t * a.H + c, s * rs * load4(a.weight, a.par_f32, c));

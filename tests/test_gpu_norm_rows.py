@@ -37,3 +37,32 @@ def test_long_sums_keep_their_digits():
     out, x = qm.combine_norm(y, inv, one, torch.zeros_like(r), post_weight=5 * w, next_weight=w)
     assert torch.equal(out.view(-1), 5 * r.view(-1) * w)
     assert torch.equal(x, r)
+
+
+@pytest.mark.parametrize("exit", [False, True])
+def test_the_longest_row(exit):
+    """H = 2^31 - 32: the column behind a thread's last one does not fit 31 bits."""
+    H = (1 << 31) - 32
+    w, r = signs(H, 5), signs(H, 3).view(1, H)
+    if not exit:
+        x, out = qm.add_norm(r, w, delta=r, scale=2.0)
+        assert torch.equal(out, 3 * r)          # 1 + 2 * 1: the same row, three times as far
+        del out
+    else:
+        one = torch.ones(1, 1, device="cuda")
+        y = signs(H, 7, F32).view(1, H)
+        inv = torch.zeros(1, dtype=torch.int32, device="cuda")
+        want = signs(H, 7) * w + r.view(-1)     # y has a mean square of 1, too
+        out, x = qm.combine_norm(y, inv, one, r, eps=0.0, post_weight=w, next_weight=w)
+        del y, one
+        assert torch.equal(out.view(-1), want)
+        # 0 or +-2: x = s / rms(s) w, rms^2 = 4 times the share of columns that are not zero
+        hit = want != 0
+        scale = (4 * hit.sum().double() / H).rsqrt().float()
+        del hit
+        want = (want.float() * scale * w).view(1, H)
+        # 2^-8 for the rounding to bf16; each thread's sum of whole numbers is exact below 2^24,
+        # the 1024 threads' has 21 adds of half a step
+        assert bool(((x.float() - want).abs() <= (2.0 ** -8 + 2.0 ** -18) * want.abs()).all())
+        return
+    assert torch.equal(x.view(-1), r.view(-1) * w)
