@@ -150,6 +150,7 @@ struct BlockNorm {
   void* resid_out;          // nullable; may be resid
   uint16_t* x;              // nullable at the exit
   bool delta_f32, par_f32;  // types of delta; of post, gate and weight
+  int t0;                   // first row of a launch; 0 from callers
 };
 hipError_t launch_block_norm(const BlockNorm& a, bool exit, bool resid_f32, hipStream_t stream);
 

@@ -116,7 +116,7 @@ template <int TH, int NCH, bool EXIT, typename R>
 __global__ __launch_bounds__(TH) void k_block_norm(BlockNorm a) {
   constexpr int NW = TH / kWave;
   __shared__ float red[NW];
-  const int64_t t = blockIdx.x;
+  const int64_t t = (int64_t)a.t0 + blockIdx.x;
   const R* rin = (const R*)a.resid + t * a.H;
   f32x4 s[NCH], v[NCH];
 #pragma unroll
@@ -177,7 +177,7 @@ template <bool EXIT, typename R>
 __global__ __launch_bounds__(1024) void k_block_norm_long(BlockNorm a) {
   constexpr int TH = 1024, NW = TH / kWave;
   __shared__ float red[NW];
-  const int64_t t = blockIdx.x;
+  const int64_t t = (int64_t)a.t0 + blockIdx.x;
   const uint32_t H = a.H;   // a column past the last, up to 2^31 + 4095, has to compare as such
   Choices ch;
   if constexpr (EXIT) ch = read_choices(a, t);
@@ -218,32 +218,38 @@ __global__ __launch_bounds__(1024) void k_block_norm_long(BlockNorm a) {
   }
 }
 
+// A launch holds fewer than 2^32 threads: rows go 2^21 at a time, of 1024 threads at most.
+constexpr int kMaxRows = 1 << 21;
+
 template <bool EXIT, typename R>
-hipError_t launch_t(const BlockNorm& a, hipStream_t stream) {
-  const dim3 grid((unsigned)a.T);
+hipError_t launch_t(BlockNorm a, hipStream_t stream) {
+  for (; a.t0 < a.T; a.t0 += kMaxRows) {
+    const dim3 grid((unsigned)min(a.T - a.t0, kMaxRows));
 #define MOE_NORM(TH, NCH)                                                                  \
   hipLaunchKernelGGL((k_block_norm<TH, NCH, EXIT, R>), grid, dim3(TH), 0, stream, a)
-  if (a.H <= 256) MOE_NORM(64, 1);
-  else if (a.H <= 512) MOE_NORM(64, 2);
-  else if (a.H <= 1024) MOE_NORM(64, 4);
-  else switch ((a.H + 1023) / 1024) {   // chunks of 256 threads x 4 values
-    case 2: MOE_NORM(256, 2); break;
-    case 3: MOE_NORM(256, 3); break;
-    case 4: MOE_NORM(256, 4); break;
-    case 5: case 6: MOE_NORM(256, 6); break;
-    case 7: case 8: MOE_NORM(256, 8); break;
-    case 9: case 10: case 11: case 12: MOE_NORM(1024, 3); break;
-    case 13: case 14: case 15: case 16: MOE_NORM(1024, 4); break;
-    default: hipLaunchKernelGGL((k_block_norm_long<EXIT, R>), grid, dim3(1024), 0, stream, a);
-  }
+    if (a.H <= 256) MOE_NORM(64, 1);
+    else if (a.H <= 512) MOE_NORM(64, 2);
+    else if (a.H <= 1024) MOE_NORM(64, 4);
+    else switch ((a.H + 1023) / 1024) {   // chunks of 256 threads x 4 values
+      case 2: MOE_NORM(256, 2); break;
+      case 3: MOE_NORM(256, 3); break;
+      case 4: MOE_NORM(256, 4); break;
+      case 5: case 6: MOE_NORM(256, 6); break;
+      case 7: case 8: MOE_NORM(256, 8); break;
+      case 9: case 10: case 11: case 12: MOE_NORM(1024, 3); break;
+      case 13: case 14: case 15: case 16: MOE_NORM(1024, 4); break;
+      default: hipLaunchKernelGGL((k_block_norm_long<EXIT, R>), grid, dim3(1024), 0, stream, a);
+    }
 #undef MOE_NORM
-  return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
 
 hipError_t launch_block_norm(const BlockNorm& a, bool exit, bool resid_f32, hipStream_t stream) {
-  if (a.T <= 0) return hipSuccess;
   if (exit) return resid_f32 ? launch_t<true, float>(a, stream) : launch_t<true, uint16_t>(a, stream);
   return resid_f32 ? launch_t<false, float>(a, stream) : launch_t<false, uint16_t>(a, stream);
 }

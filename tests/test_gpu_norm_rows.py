@@ -66,3 +66,53 @@ def test_the_longest_row(exit):
         assert bool(((x.float() - want).abs() <= (2.0 ** -8 + 2.0 ** -18) * want.abs()).all())
         return
     assert torch.equal(x.view(-1), r.view(-1) * w)
+
+
+# more rows than one launch may have threads for, 2^32: 64 threads a row up to H = 1024, 1024
+# from H = 8224 on
+MANY = [((1 << 26) + 3, 32), ((1 << 22) + 3, 8224)]
+
+
+def rows_like(t, first, last):
+    """Row i of t equals first[i % len(first)], and its last rows equal `last`."""
+    n, m = len(t) - len(last), len(first)
+    assert n % m == 0 and torch.equal(t[n:], last)
+    step = max(m, (1 << 28) // t.shape[1] // m * m)
+    for i in range(0, n, step):
+        part = t[i:min(i + step, n)].view(-1, *first.shape)
+        assert torch.equal(part, first.expand_as(part)), f"rows {i} on"
+
+
+def repeated(first, last, T):
+    t = torch.empty(T, first.shape[1], dtype=first.dtype, device="cuda")
+    n = T - len(last)
+    t[:n].view(-1, *first.shape).copy_(first.expand(n // len(first), *first.shape))
+    t[n:] = last
+    return t
+
+
+@pytest.mark.parametrize("T,H", MANY)
+def test_more_rows_than_a_launch(T, H):
+    g = torch.Generator("cuda").manual_seed(H)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    first, last, w = rand(64, H).to(BF), rand(3, H).to(BF), rand(H).to(BF)
+    r = repeated(first, last, T)
+    x, out = qm.add_norm(r, w, delta=r, scale=0.5, resid_out=r)
+    want = [qm.add_norm(v, w, delta=v, scale=0.5) for v in (first, last)]
+    rows_like(x, want[0][0], want[1][0])
+    rows_like(out, want[0][1], want[1][1])
+
+
+def test_more_rows_than_a_launch_at_the_exit():
+    T, H = (1 << 26) + 3, 32
+    g = torch.Generator("cuda").manual_seed(7)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    first, last, w = rand(64, H), rand(3, H), rand(H)
+    y, r = repeated(first, last, T), repeated(first.to(BF), last.to(BF), T)
+    tw = torch.full((T, 1), 0.5, device="cuda")
+    inv = torch.arange(T, dtype=torch.int32, device="cuda")
+    out, x = qm.combine_norm(y, inv, tw, r, post_weight=w, gate=r.float(), next_weight=w)
+    want = [qm.combine_norm(v, inv[:len(v)], tw[:len(v)], v.to(BF), post_weight=w,
+                            gate=v.to(BF).float(), next_weight=w) for v in (first, last)]
+    rows_like(out, want[0][0], want[1][0])
+    rows_like(x, want[0][1], want[1][1])
