@@ -230,7 +230,7 @@ hipError_t launch_t(BlockNorm a, hipStream_t stream) {
     if (a.H <= 256) MOE_NORM(64, 1);
     else if (a.H <= 512) MOE_NORM(64, 2);
     else if (a.H <= 1024) MOE_NORM(64, 4);
-    else switch ((a.H + 1023) / 1024) {   // chunks of 256 threads x 4 values
+    else switch ((a.H - 1) / 1024 + 1) {   // chunks of 256 threads x 4 values
       case 2: MOE_NORM(256, 2); break;
       case 3: MOE_NORM(256, 3); break;
       case 4: MOE_NORM(256, 4); break;
