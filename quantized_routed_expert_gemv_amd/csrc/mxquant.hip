@@ -10,6 +10,8 @@
 // Copy rate bounds these kernels; see each for its split. Measured on 92160 x 2880 values,
 // MXFP4 / MXFP6: quantise from bf16 114 / 143 us (5.9 / 5.2 TB/s), from fp32 208 / 224 us;
 // dequantise to bf16 158 / 153 us (4.3 / 4.8 TB/s), to fp32 235 / 256 us.
+#include <algorithm>
+
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -193,18 +195,35 @@ hipError_t dequantize_f(const uint8_t* q, const uint8_t* s, int64_t n, void* dst
   return hipGetLastError();
 }
 
+// A launch holds fewer than 2^32 threads, of 8 values or 16: values go 2^34 at a time.
+constexpr int64_t kMaxValues = int64_t(1) << 34;
+
 }  // namespace
 
 hipError_t launch_mx_quantize(const void* src, int type, int64_t n, int fmt, uint8_t* q,
                               uint8_t* s, hipStream_t st) {
-  return fmt == kMxFp4 ? quantize_f<kMxFp4>(src, type, n, q, s, st)
-                       : quantize_f<kMxFp6>(src, type, n, q, s, st);
+  for (int64_t at = 0; at < n; at += kMaxValues) {
+    const void* from = (const uint8_t*)src + at * (type == kFP32 ? 4 : 2);
+    uint8_t* to = q + at / 32 * mx_block_bytes(fmt);
+    const int64_t m = std::min(n - at, kMaxValues);   // HIP has its own min for int alone
+    const hipError_t e = fmt == kMxFp4 ? quantize_f<kMxFp4>(from, type, m, to, s + at / 32, st)
+                                       : quantize_f<kMxFp6>(from, type, m, to, s + at / 32, st);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_mx_dequantize(const uint8_t* q, const uint8_t* s, int64_t n, int fmt, void* dst,
                                 int type, hipStream_t st) {
-  return fmt == kMxFp4 ? dequantize_f<kMxFp4>(q, s, n, dst, type, st)
-                       : dequantize_f<kMxFp6>(q, s, n, dst, type, st);
+  for (int64_t at = 0; at < n; at += kMaxValues) {
+    const uint8_t* from = q + at / 32 * mx_block_bytes(fmt);
+    void* to = (uint8_t*)dst + at * (type == kFP32 ? 4 : 2);
+    const int64_t m = std::min(n - at, kMaxValues);   // HIP has its own min for int alone
+    const hipError_t e = fmt == kMxFp4 ? dequantize_f<kMxFp4>(from, s + at / 32, m, to, type, st)
+                                       : dequantize_f<kMxFp6>(from, s + at / 32, m, to, type, st);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace moe

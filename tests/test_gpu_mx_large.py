@@ -1,0 +1,53 @@
+"""Microscaled calls at sizes past one launch or past 32 bits of an index."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+import quantized_routed_expert_gemv_amd as qm  # noqa: E402
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(autouse=True)
+def give_back():
+    yield
+    torch.cuda.empty_cache()
+
+
+def repeated(first, last, rows):
+    t = torch.empty(rows, first.shape[1], dtype=first.dtype, device="cuda")
+    n = rows - len(last)
+    t[:n].view(-1, *first.shape).copy_(first.expand(n // len(first), *first.shape))
+    t[n:] = last
+    return t
+
+
+def rows_like(t, first, last):
+    """Row i of t equals first[i % len(first)], and its last rows equal `last`."""
+    n, m = len(t) - len(last), len(first)
+    assert n % m == 0 and torch.equal(t[n:], last)
+    step = max(m, (1 << 28) // t.shape[1] // m * m)
+    for i in range(0, n, step):
+        part = t[i:min(i + step, n)].view(-1, *first.shape)
+        assert torch.equal(part, first.expand_as(part)), f"rows {i} on"
+
+
+# a launch has fewer than 2^32 threads, of 8 values (MXFP4 codes, fp32 values) or of 16, and
+# takes 2^34 values
+@pytest.mark.parametrize("fmt,log_values,dt", [("mxfp4", 35, F32), ("mxfp6", 34, BF)])
+def test_more_values_than_a_launch(fmt, log_values, dt):
+    K = 1 << 15
+    rows = (1 << (log_values - 15)) + 3
+    g = torch.Generator("cuda").manual_seed(1)
+    first, last = (torch.randn(n, K, generator=g, device="cuda").to(BF) for n in (64, 3))
+    x = repeated(first, last, rows)
+    q, s = qm.mx_quantize(x, fmt)
+    del x
+    torch.cuda.empty_cache()
+    f, l = qm.mx_quantize(first, fmt), qm.mx_quantize(last, fmt)
+    rows_like(q, f[0], l[0])
+    rows_like(s, f[1], l[1])
+    v = qm.mx_dequantize(q, s, fmt, dt)
+    rows_like(v, qm.mx_dequantize(*f, fmt, dt), qm.mx_dequantize(*l, fmt, dt))
