@@ -278,7 +278,7 @@ __device__ bool find_tile(const MxProduct& p, int bm, int mt, int* e, int* m0, i
 // what the instruction sustains on such operands.
 template <int FMT, bool GATED, int MF, int NW>
 __global__ __launch_bounds__(kWave * NW, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k_mx_gemm(
-    MxProduct p, int n_mtiles, int n_ntiles) {
+    MxProduct p, int n_mtiles, int n_ntiles, int first) {
   constexpr int kThreads = kWave * NW, kCols = 64 * NW;   // weight rows a tile
   constexpr int BM = 32 * MF;
   constexpr int TN = GATED ? kCols / 2 : kCols;   // output columns a tile
@@ -295,9 +295,9 @@ __global__ __launch_bounds__(kWave * NW, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k_m
   __shared__ int part[kThreads / kWave];
   __shared__ int found[3];
   // XCD-aware tile order: workgroups go to the 8 XCDs in turn, and each XCD gets runs of 64
-  // tiles that share their rows and weights in its L2
+  // tiles that share their rows and weights in its L2; first: 512s of tiles of earlier launches
   const int xcd = blockIdx.x & 7, local = blockIdx.x >> 3;
-  const int64_t i = (int64_t)(local >> 6) * 512 + xcd * 64 + (local & 63);
+  const int64_t i = (int64_t)(first + (local >> 6)) * 512 + xcd * 64 + (local & 63);
   if (i >= (int64_t)n_mtiles * n_ntiles) return;
   const int sr = (int)(i / ((int64_t)kSuperRows * n_ntiles));
   const int sh = min(kSuperRows, n_mtiles - kSuperRows * sr);
@@ -547,11 +547,18 @@ hipError_t launch_gemm_t(const MxProduct& p, hipStream_t st) {
   const int pairs = p.T * p.k;
   const int n_mtiles = (pairs + BM - 1) / BM + min(p.E, pairs);   // most that can be
   const int n_ntiles = (p.N + TN - 1) / TN;
-  const int64_t grid = ((int64_t)n_mtiles * n_ntiles + 511) / 512 * 512;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((k_mx_gemm<FMT, GATED, MF, NW>), dim3((unsigned)grid), dim3(kWave * NW), 0, st, p,
-                     n_mtiles, n_ntiles);
-  return hipGetLastError();
+  // a launch holds fewer than 2^32 threads: 2^22 workgroups of at most 512 at a time. T*k*N below
+  // 2^38 fills at most 2^25 tiles, and 256 experts' last ones 2^28 of N below 2^27
+  constexpr int kMax = (1 << 22) / 512;
+  const int n = (int)(((int64_t)n_mtiles * n_ntiles + 511) / 512);   // below 2^21
+  for (int first = 0; first < n; first += kMax) {
+    const dim3 grid(512 * (n - first < kMax ? n - first : kMax));
+    hipLaunchKernelGGL((k_mx_gemm<FMT, GATED, MF, NW>), grid, dim3(kWave * NW), 0, st, p, n_mtiles,
+                       n_ntiles, first);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // Rows a tile. A tall tile reads the weights less often and feeds more products per operand

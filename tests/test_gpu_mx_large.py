@@ -51,3 +51,21 @@ def test_more_values_than_a_launch(fmt, log_values, dt):
     rows_like(s, f[1], l[1])
     v = qm.mx_dequantize(q, s, fmt, dt)
     rows_like(v, qm.mx_dequantize(*f, fmt, dt), qm.mx_dequantize(*l, fmt, dt))
+
+
+def test_more_tiles_than_a_launch():
+    """66 row tiles by 2^18 of 256 columns, of 256 threads each, pass 2^32 threads."""
+    H, I, T = 1 << 26, 32, 64
+    g = torch.Generator("cuda").manual_seed(2)
+    rand = lambda a, b, *s: torch.randint(a, b, s, generator=g, dtype=torch.uint8, device="cuda")  # noqa: E731
+    pool = qm.Pool.empty("mxfp4", 1, H, I)
+    qm.pool_pack("mxfp4", 1, H, I, rand(0, 256, H, I // 2), rand(118, 124, H, 1),
+                 pool.planes["down_q"], pool.planes["down_s"])
+    sm = torch.zeros(T, dtype=torch.int32, device="cuda")
+    ids = torch.arange(T, dtype=torch.int32, device="cuda").view(T, 1)
+    off = qm.bucket(ids, T)[1]
+    hq, hs = rand(0, 256, T, I // 2), rand(123, 131, T, 1)
+    y = qm.mx_expert_down(pool, sm, T, 1, off, hq, hs, "mxfp4", path=qm.PATH_GROUPED)
+    # one block a row: its sum is exact, so both schedules give the same
+    few = qm.mx_expert_down(pool, sm, T, 1, off, hq, hs, "mxfp4", path=qm.PATH_GEMV)
+    assert bool(y[:, -32:].any(1).all()) and torch.equal(y, few)
