@@ -110,8 +110,9 @@ __global__ __launch_bounds__(kGemvThreads) void k_mx_gemv(MxProduct p) {
   const int n0 = blockIdx.x * kRowGroup;
   const int slot = p.slot_map[e];
   if (slot < 0 || slot >= p.n_slots) {
-    for (int t = threadIdx.x; t < (hi - lo) * kRowGroup; t += kGemvThreads) {
-      const int64_t o = (int64_t)(lo + t / kRowGroup) * p.N + n0 + t % kRowGroup;
+    // 64 bits: an expert of 2^27 rows has 2^31 values here
+    for (int64_t t = threadIdx.x; t < (int64_t)(hi - lo) * kRowGroup; t += kGemvThreads) {
+      const int64_t o = (lo + t / kRowGroup) * p.N + n0 + t % kRowGroup;
       if (GATED) p.h[o] = 0;
       else p.y[o] = 0.f;
     }

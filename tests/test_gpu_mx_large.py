@@ -69,3 +69,21 @@ def test_more_tiles_than_a_launch():
     # one block a row: its sum is exact, so both schedules give the same
     few = qm.mx_expert_down(pool, sm, T, 1, off, hq, hs, "mxfp4", path=qm.PATH_GEMV)
     assert bool(y[:, -32:].any(1).all()) and torch.equal(y, few)
+
+
+def test_a_miss_of_many_rows():
+    """An expert outside the pool whose rows hold 2^31 values and more in 16 columns."""
+    T, H, I = (1 << 27) + 5, 32, 32
+    pool = qm.Pool.empty("mxfp4", 1, H, I)
+    sm = torch.full((1,), qm.SLOT_MISS, dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    perm = torch.arange(T, dtype=torch.int32, device="cuda")
+    q = torch.zeros(T, I // 2, dtype=torch.uint8, device="cuda")
+    s = torch.full((T, 1), 127, dtype=torch.uint8, device="cuda")
+    h = torch.full((T, I), 7, dtype=BF, device="cuda")
+    qm.mx_expert_gate_up(pool, sm, q, s, "mxfp4", 1, off, perm, h=h, path=qm.PATH_GEMV)
+    assert not h.any()
+    del h, perm
+    y = torch.full((T, H), 7, dtype=F32, device="cuda")
+    qm.mx_expert_down(pool, sm, T, 1, off, q, s, "mxfp4", y=y, path=qm.PATH_GEMV)
+    assert not y.any()
