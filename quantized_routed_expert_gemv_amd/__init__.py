@@ -540,8 +540,15 @@ def _run(fn, like, stream, *args):
         _check(status)
 
 
+def _sizes(a, b):
+    """The C calls take 32-bit sizes, and ctypes passes the low bits of larger ones."""
+    if a > 0x7FFFFFFF or b > 0x7FFFFFFF:
+        raise ValueError(f"sizes {a} and {b}: limit 2^31 - 1")
+
+
 def mx_row_bytes(fmt: str, K: int) -> int:
     """Bytes of one row of K codes ("mxfp4" or "mxfp6")."""
+    _sizes(K, 0)
     return _mx_row_bytes(_MX[fmt], K)
 
 
@@ -573,10 +580,12 @@ def mx_quantize(x, fmt: str = "mxfp4", q=None, s=None, stream=None):
     Pool.from_canonical and pool_pack take."""
     _one_of("fmt", fmt, _MX)
     *rows, K = x.shape
+    n = x.numel() // max(K, 1)
+    _sizes(n, K)
     _tensor(x, _DT, x.shape, "x", x)
     q = _rows(q, torch.uint8, (*rows, mx_row_bytes(fmt, K)), "q", x, stream)
     s = _rows(s, torch.uint8, (*rows, K // 32), "s", x, stream)
-    _run(_mx_quantize, x, stream, _addr(x), _DT[x.dtype], x.numel() // max(K, 1), K, _MX[fmt],
+    _run(_mx_quantize, x, stream, _addr(x), _DT[x.dtype], n, K, _MX[fmt],
          _addr(q), _addr(s))
     return q, s
 
@@ -585,16 +594,18 @@ def mx_dequantize(q, s, fmt: str = "mxfp4", dtype=torch.bfloat16, out=None, stre
     """The values of codes and scales: bf16, fp16 or fp32 [..., K]."""
     _one_of("dtype", dtype, _DT)
     *rows, nb = s.shape
-    K = 32 * nb
+    K, n = 32 * nb, s.numel() // max(nb, 1)
+    _sizes(n, K)
     _mx_planes(q, s, fmt, rows, K, ("q", "s"), q)
     out = _rows(out, dtype, (*rows, K), "out", q, stream)
-    _run(_mx_dequantize, q, stream, _addr(q), _addr(s), _MX[fmt], s.numel() // max(nb, 1), K,
+    _run(_mx_dequantize, q, stream, _addr(q), _addr(s), _MX[fmt], n, K,
          _addr(out), _DT[dtype])
     return out
 
 
 def _mx_checks(pool, slot_map, T, k, offsets, perm, err_flags, like):
     E = slot_map.shape[0]
+    _sizes(T, k)
     i32 = (torch.int32,)
     _tensor(slot_map, i32, (E,), "slot_map", like)
     _tensor(offsets, i32, (E + 1,), "offsets", like)
@@ -661,6 +672,7 @@ def add_norm(resid, weight, eps: float = 1e-6, delta=None, scale: float = 1.0, r
     (x bf16 [T, H], resid_out like resid). Without delta the stream is not written and resid
     is returned in its place; resid_out may be resid itself."""
     T, H = resid.shape
+    _sizes(T, H)
     _tensor(resid, _STREAM_TYPES, (T, H), "resid", resid)
     _tensor(weight, _STREAM_TYPES, (H,), "weight", resid)
     if delta is not None:
@@ -683,6 +695,7 @@ def combine_norm(y, inv_perm, w, resid, eps: float = 1e-6, post_weight=None, gat
     may be None -> (resid_out like resid, x bf16 [T, H] or None). resid_out may be resid."""
     T, k = w.shape
     H = resid.shape[-1]
+    _sizes(T, H)
     _tensor(y, (torch.float32,), (T * k, H), "y", resid)
     _tensor(inv_perm, (torch.int32,), (T * k,), "inv_perm", resid)
     _tensor(w, (torch.float32,), (T, k), "w", resid)
