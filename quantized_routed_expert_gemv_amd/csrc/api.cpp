@@ -919,7 +919,8 @@ moe_status moe_add_norm(const void* resid, int32_t resid_type, const void* delta
   moe::BlockNorm a{};
   a.T = T, a.H = H, a.k = 1;
   a.resid = resid, a.delta = delta, a.weight = weight;
-  a.eps = eps, a.scale = scale;
+  a.eps = eps;
+  a.scale = delta != nullptr ? scale : -0.f;   // -0 * 0 + resid is resid, bit by bit
   a.resid_out = resid_out, a.x = x;
   a.delta_f32 = delta_type == MOE_T_FP32, a.par_f32 = weight_type == MOE_T_FP32;
   clear_stale_error();
