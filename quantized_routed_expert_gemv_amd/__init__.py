@@ -497,10 +497,6 @@ class LayerCall:
 # that a call makes are that stream's, as tensors made under `with torch.cuda.stream(stream)` are.
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream   # a stream handle without a Stream object
-_current_device = torch._C._cuda_getDevice           # torch is initialised: tensors are there
-
-
 def _one_of(name, value, choices):
     if value not in choices:
         raise ValueError(f"{name}: {value!r}, expected one of {', '.join(map(repr, choices))}")
@@ -525,13 +521,14 @@ def _run(fn, like, stream, *args):
     """Calls fn(*args, stream) with the device of `like` current, on that device's current
     stream unless one is given."""
     index = like.get_device()
+    cuda = torch._C   # its calls make no Stream object, and are there where torch has GPU support
     if stream is None:
-        handle = _raw_stream(index)
+        handle = cuda._cuda_getCurrentRawStream(index)
     else:
         if stream.device != like.device:
             raise ValueError(f"stream: on {stream.device}, expected {like.device}")
         handle = stream.cuda_stream
-    if index == _current_device():
+    if index == cuda._cuda_getDevice():
         status = fn(*args, handle)
     else:
         with torch.cuda.device(index):
