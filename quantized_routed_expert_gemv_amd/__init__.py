@@ -537,15 +537,17 @@ def _run(fn, like, stream, *args):
         _check(status)
 
 
-def _sizes(a, b):
-    """The C calls take 32-bit sizes, and ctypes passes the low bits of larger ones."""
-    if a > 0x7FFFFFFF or b > 0x7FFFFFFF:
-        raise ValueError(f"sizes {a} and {b}: limit 2^31 - 1")
+_SIZE = 0x7FFFFFFF   # the C calls take 32-bit sizes, and ctypes passes the low bits of larger ones
+
+
+def _too_large(*sizes):
+    raise ValueError(f"sizes {sizes}: limit 2^31 - 1")
 
 
 def mx_row_bytes(fmt: str, K: int) -> int:
     """Bytes of one row of K codes ("mxfp4" or "mxfp6")."""
-    _sizes(K, 0)
+    if K > _SIZE:
+        _too_large(K)
     return _mx_row_bytes(_MX[fmt], K)
 
 
@@ -578,7 +580,8 @@ def mx_quantize(x, fmt: str = "mxfp4", q=None, s=None, stream=None):
     _one_of("fmt", fmt, _MX)
     *rows, K = x.shape
     n = x.numel() // max(K, 1)
-    _sizes(n, K)
+    if n > _SIZE or K > _SIZE:
+        _too_large(n, K)
     _tensor(x, _DT, x.shape, "x", x)
     q = _rows(q, torch.uint8, (*rows, mx_row_bytes(fmt, K)), "q", x, stream)
     s = _rows(s, torch.uint8, (*rows, K // 32), "s", x, stream)
@@ -592,7 +595,8 @@ def mx_dequantize(q, s, fmt: str = "mxfp4", dtype=torch.bfloat16, out=None, stre
     _one_of("dtype", dtype, _DT)
     *rows, nb = s.shape
     K, n = 32 * nb, s.numel() // max(nb, 1)
-    _sizes(n, K)
+    if n > _SIZE or K > _SIZE:
+        _too_large(n, K)
     _mx_planes(q, s, fmt, rows, K, ("q", "s"), q)
     out = _rows(out, dtype, (*rows, K), "out", q, stream)
     _run(_mx_dequantize, q, stream, _addr(q), _addr(s), _MX[fmt], n, K,
@@ -602,7 +606,8 @@ def mx_dequantize(q, s, fmt: str = "mxfp4", dtype=torch.bfloat16, out=None, stre
 
 def _mx_checks(pool, slot_map, T, k, offsets, perm, err_flags, like):
     E = slot_map.shape[0]
-    _sizes(T, k)
+    if T > _SIZE or k > _SIZE:
+        _too_large(T, k)
     i32 = (torch.int32,)
     _tensor(slot_map, i32, (E,), "slot_map", like)
     _tensor(offsets, i32, (E + 1,), "offsets", like)
@@ -669,7 +674,8 @@ def add_norm(resid, weight, eps: float = 1e-6, delta=None, scale: float = 1.0, r
     (x bf16 [T, H], resid_out like resid). Without delta the stream is not written and resid
     is returned in its place; resid_out may be resid itself."""
     T, H = resid.shape
-    _sizes(T, H)
+    if T > _SIZE or H > _SIZE:
+        _too_large(T, H)
     _tensor(resid, _STREAM_TYPES, (T, H), "resid", resid)
     _tensor(weight, _STREAM_TYPES, (H,), "weight", resid)
     if delta is not None:
@@ -692,7 +698,8 @@ def combine_norm(y, inv_perm, w, resid, eps: float = 1e-6, post_weight=None, gat
     may be None -> (resid_out like resid, x bf16 [T, H] or None). resid_out may be resid."""
     T, k = w.shape
     H = resid.shape[-1]
-    _sizes(T, H)
+    if T > _SIZE or H > _SIZE:
+        _too_large(T, H)
     _tensor(y, (torch.float32,), (T * k, H), "y", resid)
     _tensor(inv_perm, (torch.int32,), (T * k,), "inv_perm", resid)
     _tensor(w, (torch.float32,), (T, k), "w", resid)
