@@ -11,6 +11,7 @@ is no fallback. If the library has not been built, importing this package raises
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -131,6 +132,13 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on(stream):
+    """Makes the given stream current. What a call allocates belongs to the stream that writes it:
+    taken from another stream's memory it could still be in use there, and a temporary could be
+    handed out there again, as soon as the call returns, while this stream still uses it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _need(t, dtype, shape, name):
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
@@ -171,13 +179,15 @@ class Pool:
     def from_canonical(cls, fmt: str, H: int, I: int, planes: dict, device="cuda", stream=None):
         """planes: name -> array [S, rows, ...] in the canonical layout (numpy or torch)."""
         n_slots = int(planes["gate_q"].shape[0])
-        pool = cls.empty(fmt, n_slots, H, I, device)
-        for n, rows, K in (("gate", I, H), ("up", I, H), ("down", H, I)):
-            q = torch.as_tensor(planes[n + "_q"]).contiguous().view(torch.uint8).to(device)
-            s = torch.as_tensor(planes[n + "_s"]).contiguous()
-            s = (s.view(torch.int16) if s.dtype == torch.uint16 else s).view(torch.uint8).to(device)
-            pool_pack(fmt, n_slots, rows, K, q, s, pool.planes[n + "_q"], pool.planes[n + "_s"],
-                      stream)
+        with _on(stream):   # the uploads, too: the packing follows them
+            pool = cls.empty(fmt, n_slots, H, I, device)
+            for n, rows, K in (("gate", I, H), ("up", I, H), ("down", H, I)):
+                q = torch.as_tensor(planes[n + "_q"]).contiguous().view(torch.uint8).to(device)
+                s = torch.as_tensor(planes[n + "_s"]).contiguous()
+                s = (s.view(torch.int16) if s.dtype == torch.uint16 else s).view(torch.uint8)
+                s = s.to(device)
+                pool_pack(fmt, n_slots, rows, K, q, s, pool.planes[n + "_q"],
+                          pool.planes[n + "_s"], stream)
         return pool
 
 
@@ -197,8 +207,15 @@ def bucket_scratch_bytes(T: int, k: int, E: int) -> int:
     return _bucket_scratch(T, k, E)
 
 
-def _scratch(nbytes, device):
-    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device) if nbytes else None
+def _new(shape, dtype, device, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _scratch(nbytes, device, stream):
+    return _new(max(nbytes, 256), torch.uint8, device, stream) if nbytes else None
 
 
 def route(x, w_router, bias, k: int, ids=None, w=None, scratch=None, stream=None):
@@ -210,12 +227,12 @@ def route(x, w_router, bias, k: int, ids=None, w=None, scratch=None, stream=None
     if bias is not None:
         _need(bias, torch.float32, (E,), "bias")
     if ids is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=x.device)
+        ids = _new((T, k), torch.int32, x.device, stream)
     if w is None:
-        w = torch.empty((T, k), dtype=torch.float32, device=x.device)
+        w = _new((T, k), torch.float32, x.device, stream)
     ns = route_scratch_bytes(T, H, E)
     if scratch is None:
-        scratch = _scratch(ns, x.device)
+        scratch = _scratch(ns, x.device, stream)
     _check(_route(_ptr(x), _ptr(w_router), _ptr(bias), T, H, E, k, _ptr(ids), _ptr(w),
                   _ptr(scratch), scratch.numel() if scratch is not None else 0, _stream(stream)))
     return ids, w
@@ -228,16 +245,16 @@ def bucket(ids, E: int, counts=None, offsets=None, perm=None, inv_perm=None, scr
     _need(ids, torch.int32, (T, k), "ids")
     dev = ids.device
     if counts is None:
-        counts = torch.empty(E, dtype=torch.int32, device=dev)
+        counts = _new(E, torch.int32, dev, stream)
     if offsets is None:
-        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        offsets = _new(E + 1, torch.int32, dev, stream)
     if perm is None:
-        perm = torch.empty(max(T * k, 1), dtype=torch.int32, device=dev)[:T * k]
+        perm = _new(max(T * k, 1), torch.int32, dev, stream)[:T * k]
     if inv_perm is None:
-        inv_perm = torch.empty(max(T * k, 1), dtype=torch.int32, device=dev)[:T * k]
+        inv_perm = _new(max(T * k, 1), torch.int32, dev, stream)[:T * k]
     ns = bucket_scratch_bytes(T, k, E)
     if scratch is None:
-        scratch = _scratch(ns, dev)
+        scratch = _scratch(ns, dev, stream)
     _check(_bucket(_ptr(ids), T, k, E, _ptr(counts), _ptr(offsets), _ptr(perm), _ptr(inv_perm),
                    _ptr(scratch), scratch.numel() if scratch is not None else 0, _stream(stream)))
     return counts, offsets, perm, inv_perm
@@ -252,8 +269,8 @@ def expert_ffn(pool: Pool, slot_map, x, k: int, offsets, perm, err_flags=None, p
     _need(slot_map, torch.int32, (E,), "slot_map")
     _need(offsets, torch.int32, (E + 1,), "offsets")
     dev = x.device
-    h = torch.empty((max(T * k, 1), pool.I), dtype=torch.bfloat16, device=dev)[:T * k]
-    y = torch.empty((max(T * k, 1), pool.H), dtype=torch.float32, device=dev)[:T * k]
+    h = _new((max(T * k, 1), pool.I), torch.bfloat16, dev, stream)[:T * k]
+    y = _new((max(T * k, 1), pool.H), torch.float32, dev, stream)[:T * k]
     _check(_ffn(ctypes.byref(pool.struct), _ptr(slot_map), E, _ptr(x), T, k, _ptr(offsets),
                 _ptr(perm), _ptr(h), _ptr(y), _ptr(err_flags), path, _stream(stream)))
     return h, y
@@ -266,7 +283,7 @@ def expert_gate_up(pool: Pool, slot_map, x, k: int, offsets, perm, h=None, err_f
     E = slot_map.shape[0]
     _need(x, torch.bfloat16, (T, pool.H), "x")
     if h is None:
-        h = torch.empty((max(T * k, 1), pool.I), dtype=torch.bfloat16, device=x.device)[:T * k]
+        h = _new((max(T * k, 1), pool.I), torch.bfloat16, x.device, stream)[:T * k]
     _check(_gate_up(ctypes.byref(pool.struct), _ptr(slot_map), E, _ptr(x), T, k, _ptr(offsets),
                     _ptr(perm), _ptr(h), _ptr(err_flags), path, _stream(stream)))
     return h
@@ -278,7 +295,7 @@ def expert_down(pool: Pool, slot_map, T: int, k: int, offsets, h, y=None, err_fl
     E = slot_map.shape[0]
     _need(h, torch.bfloat16, (T * k, pool.I), "h")
     if y is None:
-        y = torch.empty((max(T * k, 1), pool.H), dtype=torch.float32, device=h.device)[:T * k]
+        y = _new((max(T * k, 1), pool.H), torch.float32, h.device, stream)[:T * k]
     _check(_down(ctypes.byref(pool.struct), _ptr(slot_map), E, T, k, _ptr(offsets), _ptr(h),
                  _ptr(y), _ptr(err_flags), path, _stream(stream)))
     return y
@@ -291,7 +308,7 @@ def combine(y, inv_perm, w, out=None, stream=None):
     _need(y, torch.float32, (T * k, H), "y")
     _need(w, torch.float32, (T, k), "w")
     if out is None:
-        out = torch.empty((T, H), dtype=torch.float32, device=y.device)
+        out = _new((T, H), torch.float32, y.device, stream)
     _check(_combine(_ptr(y), _ptr(inv_perm), _ptr(w), T, k, H, _ptr(out), _stream(stream)))
     return out
 
@@ -307,12 +324,13 @@ def miss_list(slot_map, offsets, perm, k: int, stream=None):
     n = perm.shape[0]
     T = n // k
     dev = slot_map.device
-    miss_pos = torch.empty(max(n, 1), dtype=torch.int32, device=dev)
-    miss_of_pair = torch.empty(max(n, 1), dtype=torch.int32, device=dev)
-    counters = torch.empty(4, dtype=torch.int32, device=dev)
+    miss_pos = _new(max(n, 1), torch.int32, dev, stream)
+    miss_of_pair = _new(max(n, 1), torch.int32, dev, stream)
+    counters = _new(4, torch.int32, dev, stream)
     _check(_miss_list(_ptr(slot_map), E, _ptr(offsets), _ptr(perm), T, k, _ptr(miss_pos),
                       _ptr(miss_of_pair), _ptr(counters), _stream(stream)))
-    n_miss = int(counters[1].item())
+    with _on(stream):   # read back behind the kernel that counts
+        n_miss = int(counters[1].item())
     return miss_pos[:n_miss], miss_of_pair[:n], counters
 
 
@@ -343,11 +361,11 @@ def stage_plan(counts, slot_map, first_slot: int, n_stage: int, slot_map_out=Non
     _need(slot_map, torch.int32, (E,), "slot_map")
     dev = slot_map.device
     if slot_map_out is None:
-        slot_map_out = torch.empty(E, dtype=torch.int32, device=dev)
+        slot_map_out = _new(E, torch.int32, dev, stream)
     if copy_list is None:
-        copy_list = torch.empty(E, dtype=torch.int32, device=dev)
+        copy_list = _new(E, torch.int32, dev, stream)
     if counters is None:
-        counters = torch.empty(2, dtype=torch.int32, device=dev)
+        counters = _new(2, torch.int32, dev, stream)
     _check(_stage_plan(_ptr(counts), _ptr(slot_map), E, first_slot, n_stage,
                        _ptr(slot_map_out), _ptr(copy_list), _ptr(counters), _stream(stream)))
     return slot_map_out, copy_list, counters
@@ -428,9 +446,10 @@ def layer(pool: Pool, slot_map, w_router, bias, x, k: int, out=None, workspace=N
     if bias is not None:
         _need(bias, torch.float32, (E,), "bias")
     if out is None:
-        out = torch.empty((T, H), dtype=torch.float32, device=x.device)
+        out = _new((T, H), torch.float32, x.device, stream)
     if workspace is None:
-        workspace = Workspace(T, pool.H, pool.I, E, k, x.device)
+        with _on(stream):
+            workspace = Workspace(T, pool.H, pool.I, E, k, x.device)
     args = (ctypes.byref(pool.struct), _ptr(slot_map), _ptr(w_router), _ptr(bias), _ptr(x),
             T, E, k, _ptr(out), _ptr(workspace.buf), workspace.buf.numel(), _ptr(err_flags),
             path, _stream(stream))
@@ -453,7 +472,7 @@ def layer_noalloc(pool: Pool, slot_map, w_router, bias, x, k: int, out=None, err
     if bias is not None:
         _need(bias, torch.float32, (E,), "bias")
     if out is None:
-        out = torch.empty((T, H), dtype=torch.float32, device=x.device)
+        out = _new((T, H), torch.float32, x.device, stream)
     _need(out, torch.float32, (T, pool.H), "out")
     _check(_layer_noalloc(ctypes.byref(pool.struct), _ptr(slot_map), _ptr(w_router), _ptr(bias),
                           _ptr(x), T, E, k, _ptr(out), _ptr(err_flags), path, _stream(stream)))
@@ -558,14 +577,12 @@ def _mx_planes(q, s, fmt, rows, K, names, like):
 
 
 def _rows(t, dtype, shape, name, like, stream):
-    """The given output, checked, or a new one. A new one belongs to the stream that writes it:
-    taken from another stream's memory it could still be in use there, and a temporary could be
-    handed out there again, as soon as the call returns, while this stream still uses it."""
+    """The given output, checked, or a new one, of the stream that writes it."""
     if t is not None:
         _tensor(t, (dtype,), shape, name, like)
         return t
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream):
             return like.new_empty(shape, dtype=dtype)
     if dtype == like.dtype and shape == like.shape:
         return torch.empty_like(like)

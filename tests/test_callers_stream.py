@@ -93,3 +93,57 @@ def test_a_stream_of_another_device_is_refused():
         qm._run(lambda *a: launched.append(a) or 0, like,
                 SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=16))
     assert not launched
+
+
+# --------------------------------------------------------------- the layer and its stages
+
+X, WR = _zeros(T, H, dt=BF), _zeros(E, H, dt=BF)
+IDS, COUNTS = _zeros(T, K, dt=I32), _zeros(E, dt=I32)
+PLANES = {n + p: torch.zeros(E, 16 * 3, c, dtype=U8) for n in ("gate", "up", "down")
+          for p, c in (("_q", 16), ("_s", 1))}
+LAYER_CALLS = {
+    "route": (3, lambda st: qm.route(X, WR, None, K, stream=st)),
+    "bucket": (5, lambda st: qm.bucket(IDS, E, stream=st)),
+    "expert_ffn": (2, lambda st: qm.expert_ffn(POOL, SM, X, K, OFF, PERM, stream=st)),
+    "expert_gate_up": (1, lambda st: qm.expert_gate_up(POOL, SM, X, K, OFF, PERM, stream=st)),
+    "expert_down": (1, lambda st: qm.expert_down(POOL, SM, T, K, OFF, _zeros(T * K, I, dt=BF),
+                                                 stream=st)),
+    "combine": (1, lambda st: qm.combine(_zeros(T * K, H), PERM, _zeros(T, K), stream=st)),
+    "miss_list": (3, lambda st: qm.miss_list(SM, OFF, PERM, K, stream=st)),
+    "stage_plan": (3, lambda st: qm.stage_plan(COUNTS, SM, 0, 1, stream=st)),
+    "layer": (2, lambda st: qm.layer(POOL, SM, WR, None, X, K, stream=st)),
+    "layer_noalloc": (1, lambda st: qm.layer_noalloc(POOL, SM, WR, None, X, K, stream=st)),
+    "from_canonical": (6, lambda st: qm.Pool.from_canonical("mxfp4", 32, 48, PLANES, "cpu", st)),
+}
+
+
+@pytest.fixture
+def layer_notes(notes, monkeypatch):
+    monkeypatch.setattr(qm, "_need", lambda *a: None)
+    monkeypatch.setattr(qm, "route_scratch_bytes", lambda *a: 512)
+    monkeypatch.setattr(qm, "bucket_scratch_bytes", lambda *a: 512)
+    for fn in ("_pool_pack", "_route", "_bucket", "_ffn", "_gate_up", "_down", "_combine",
+               "_miss_list", "_stage_plan", "_layer", "_layer_noalloc"):
+        monkeypatch.setattr(qm, fn, lambda *a: 0)
+    monkeypatch.setattr(qm, "_stream", lambda *a: None)
+    return notes
+
+
+@pytest.mark.parametrize("name", LAYER_CALLS)
+def test_layer_buffers_belong_to_the_given_stream(layer_notes, name):
+    n, call = LAYER_CALLS[name]
+    side = object()
+    with layer_notes:
+        call(side)
+    assert layer_notes.seen == [side] * len(layer_notes.seen) and len(layer_notes.seen) >= n
+
+
+def test_miss_count_is_read_behind_the_kernel(layer_notes, monkeypatch):
+    read = []
+    item = torch.Tensor.item
+    monkeypatch.setattr(torch.Tensor, "item", lambda t: read.append(layer_notes.current) or 0)
+    side = object()
+    with layer_notes:
+        qm.miss_list(SM, OFF, PERM, K, stream=side)
+    monkeypatch.setattr(torch.Tensor, "item", item)
+    assert read == [side]

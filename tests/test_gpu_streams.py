@@ -26,7 +26,7 @@ class Args:
     def __init__(self):
         g = torch.Generator("cuda").manual_seed(0)
         rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
-        planes = {}
+        self.planes = planes = {}
         for n, r, c in (("gate", I, H), ("up", I, H), ("down", H, I)):
             planes[n + "_q"], planes[n + "_s"] = qm.mx_quantize(rand(E, r, c) / c ** 0.5)
         self.pool = qm.Pool.from_canonical("mxfp4", H, I, planes)
@@ -34,8 +34,10 @@ class Args:
         self.x, self.w = rand(T, H).to(BF), rand(H)
         self.x4 = qm.mx_quantize(self.x)
         self.h4 = qm.mx_quantize(rand(T * K, I))
-        ids = torch.argsort(rand(T, E), 1)[:, :K].to(torch.int32).contiguous()
-        _, self.off, self.perm, self.inv = qm.bucket(ids, E)
+        self.ids = torch.argsort(rand(T, E), 1)[:, :K].to(torch.int32).contiguous()
+        _, self.off, self.perm, self.inv = qm.bucket(self.ids, E)
+        self.part = torch.where(self.sm % 3 == 0, qm.SLOT_MISS, self.sm).to(torch.int32)
+        self.wr = (rand(E, H) / H ** 0.5).to(BF)
         self.y, self.tw = rand(T * K, H), rand(T, K)
 
 
@@ -51,6 +53,16 @@ CALLS = {   # call -> (result, the shape and type of a buffer that it makes)
     "add_norm": (lambda a, st: qm.add_norm(a.x, a.w, delta=a.x, stream=st), (T, H), BF),
     "combine_norm": (lambda a, st: qm.combine_norm(a.y, a.inv, a.tw, a.x, next_weight=a.w,
                                                    stream=st), (T, H), BF),
+    "route": (lambda a, st: qm.route(a.x, a.wr, None, K, stream=st), (T, K), F32),
+    "bucket": (lambda a, st: qm.bucket(a.ids, E, stream=st), (T * K,), torch.int32),
+    "miss_list": (lambda a, st: qm.miss_list(a.part, a.off, a.perm, K, stream=st), (T * K,),
+                  torch.int32),
+    "expert_ffn": (lambda a, st: qm.expert_ffn(a.pool, a.sm, a.x, K, a.off, a.perm, stream=st),
+                   (T * K, H), F32),
+    "layer": (lambda a, st: qm.layer(a.pool, a.sm, a.wr, None, a.x, K, stream=st)[0], (T, H), F32),
+    "from_canonical": (lambda a, st: tuple(qm.Pool.from_canonical("mxfp4", H, I, a.planes,
+                                                                  stream=st).planes.values()),
+                       (E, I, H // 2), U8),
 }
 
 
