@@ -6,6 +6,7 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("needs a GPU", allow_module_level=True)
 import quantized_routed_expert_gemv_amd as qm  # noqa: E402
+import test_gpu_norm as against_oracle  # noqa: E402
 
 BF, F32 = torch.bfloat16, torch.float32
 
@@ -14,6 +15,19 @@ BF, F32 = torch.bfloat16, torch.float32
 def give_back():
     yield
     torch.cuda.empty_cache()
+
+
+# rows of 12289 to 16384 values, which have a variant of their own, and the borders next to it
+@pytest.mark.parametrize("T,H", [(3, 12288), (2, 12320), (3, 14336), (2, 16384), (1, 16416)])
+@pytest.mark.parametrize("rt", [BF, F32])
+@pytest.mark.parametrize("exit", [False, True])
+def test_wide_rows(T, H, rt, exit):
+    if exit:
+        against_oracle.test_combine_norm(T, H, 4, rt, F32, 1, 2, 1)
+        against_oracle.test_combine_norm(T, H, 3, rt, BF, 0, 1, 1)
+    else:
+        against_oracle.test_add_norm(T, H, rt, BF, F32)
+        against_oracle.test_add_norm(T, H, rt, None, BF)
 
 
 def signs(n, every, dt=BF):
