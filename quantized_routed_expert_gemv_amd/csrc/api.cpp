@@ -2,6 +2,7 @@
 // workspace layout and dispatch to the kernels. No call allocates, frees or synchronises.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -744,7 +745,7 @@ moe_status check_norm(int32_t T, int32_t H, int32_t k, int32_t resid_type, int32
                       float eps) {
   moe_status s = check_shape(T, H, moe::kMaxE, k);
   if (s != MOE_OK) return s;
-  if (!(eps >= 0.f) || eps > 3.4e38f)
+  if (!(eps >= 0.f && eps <= FLT_MAX))
     return fail(MOE_ERR_INVALID_ARG, "eps = %g is negative or not finite", (double)eps);
   s = check_type("resid", resid_type, false);
   if (s != MOE_OK) return s;

@@ -61,3 +61,19 @@ def test_row_bytes_past_32_bits():
     with pytest.raises(ValueError):
         qm.mx_row_bytes("mxfp4", BIG)
     assert qm.mx_row_bytes("mxfp6", (1 << 31) - 32) == ((1 << 31) - 32) // 4 * 3
+
+
+def test_the_largest_eps_is_taken():
+    """eps is finite and not negative: fp32's largest number is one, what is past it is not.
+    No rows, so nothing is launched."""
+    import ctypes
+    import os
+    lib = ctypes.CDLL(os.path.join(os.path.dirname(qm.__file__), "libmoe.so"))
+    f32, ptr = ctypes.c_float, ctypes.c_void_p
+
+    def add_norm(eps):
+        return lib.moe_add_norm(ptr(), 1, ptr(), 1, f32(1.0), ptr(), 1, f32(eps), 0, 64, ptr(), ptr(),
+                                ptr())
+
+    assert [add_norm(e) for e in (0.0, 3.402e38, float.fromhex("0x1.fffffep127"))] == [0, 0, 0]
+    assert [add_norm(e) for e in (-1e-45, 3.41e38, float("inf"), float("nan"))] == [1, 1, 1, 1]
