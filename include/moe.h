@@ -447,8 +447,9 @@ moe_status moe_mx_expert_ffn(const moe_pool* pool, const int32_t* slot_map, int3
 
 /*
  * The norms before and after the layer, on the residual stream resid [T][H] of resid_type
- * (MOE_T_BF16 or MOE_T_FP32). All arithmetic is fp32; each output is rounded once. eps is
- * finite and not negative.
+ * (MOE_T_BF16 or MOE_T_FP32). All arithmetic is fp32 (rows of more than 16384 values add their
+ * squares in fp64); each output is rounded once. eps is finite and not negative. A row's sum of
+ * squares has to fit fp32: where it passes 3.4e38, x is 0.
  *
  * moe_add_norm -- the layer's entry:
  *   s = resid + scale * delta          (delta [T][H] of delta_type, bf16 or fp32; NULL: s = resid)

@@ -768,9 +768,13 @@ moe_status check_mx_product(const moe_pool* pool, const int32_t* slot_map, int32
 }
 
 // AUTO for the products on microscaled rows: the few-token kernel for up to 16 tokens (one
-// column tile an expert) and where experts have at most 4 rows on average. Measured there:
-// H = I = 2880, 32 experts, mean 2, gate/up 24 us against 32 us of the 32-row tiles; H 2048,
-// I 768, 128 experts, mean 4: 24 against 25, and 40 against 24 at mean 8.
+// column tile an expert) and where experts have at most 4 rows on average. Measured,
+// us of it against the 32-row tiles, uniform load and one where the r-th expert is wanted r^-1.2
+// times as often: H = I = 2880, 32 experts, MXFP6, gate/up, mean 2: 48 against 58, 28 against 35;
+// mean 4: 52 against 61, 41 against 43; mean 8: 59 against 62, 54 against 50; H 2048, I 768, 128
+// experts, MXFP4, gate/up, mean 4: 41 against 48, 23 against 23; mean 8: 44 against 48, 39 against
+// 21. Down gains less: mean 2: 30 against 30, 14 against 23; mean 4: 34 against 32, 23 against
+// 27; the 128 experts, mean 4: 30 against 21, 16 against 12.
 bool use_mx_gemv(int32_t path, int32_t T, int32_t k, int32_t E) {
   return use_gemv(path, T) || (path == MOE_PATH_AUTO && (int64_t)T * k <= 4 * E);
 }

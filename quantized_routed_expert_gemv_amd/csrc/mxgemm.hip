@@ -75,9 +75,9 @@ constexpr int kGemvThreads = 256;
 // Few rows: the weights' bytes bound it. One workgroup a 16-row group of one active expert;
 // its 4 waves share the row group's blocks, 4 at a time (one coalesced KiB), and add their
 // sums in LDS in wave order. Up to 16 rows of the expert ride along as the instruction's
-// columns; more are taken 16 at a time. Measured: gate/up of one token, H = I = 2880, 4
-// experts: 7.7 us for 35 MB (4.6 TB/s); down of four tokens, H 4096, I 14336: 33 us for about
-// 5 experts' 156 MB.
+// columns; more are taken 16 at a time. Measured, in rows of calls: gate/up of one token, H = I =
+// 2880, 4 experts: 8.7 us for 35 MB (4.0 TB/s; 9.3 us in a kernel trace); down of four tokens, H
+// 4096, I 14336: 33 us for about 5 experts' 156 MB.
 template <int FMT, bool GATED>
 __global__ __launch_bounds__(kGemvThreads) void k_mx_gemv(MxProduct p) {
   constexpr int NM = GATED ? 2 : 1;
@@ -198,9 +198,10 @@ __device__ __forceinline__ v16f mma32(v8i w, uint32_t ws, v8i a, uint32_t as, v1
 
 // A step's rows in LDS: the first 16 bytes of each block, row by row, then (MXFP6) the last 8
 // of each. Block b of tile row r lies in place b ^ (r / 2 % 8) of the row's eight, and in the
-// second part b ^ (r / 4 % 8), such that the lanes of each pass of a 64-lane read (one block of
-// 32 rows and the next of the same) touch different banks: 128-byte rows repeat their banks
-// every 2 rows, 64-byte rows every 4. Read whole, MXFP6's 24-byte blocks would take three
+// second part b ^ (r / 4 % 8), to spread the lanes of each pass of a 64-lane read (one block of
+// 32 rows and the next of the same) over the banks: 128-byte rows repeat their banks every 2
+// rows, 64-byte rows every 4. In the whole kernel, conflicts take 13% of LDS's busy cycles on
+// MXFP4 rows and 33% on MXFP6 rows (H 4096, I 14336, gate/up). Read whole, MXFP6's 24-byte blocks would take three
 // 8-byte reads, at half the rate of 16-byte ones. Rows 32 apart lie at one distance.
 __device__ __forceinline__ int lds_place(int r, int b) {
   return (r * kStepBlocks + (b ^ ((r >> 1) & 7))) * 16;
@@ -272,11 +273,13 @@ __device__ bool find_tile(const MxProduct& p, int bm, int mt, int* e, int* m0, i
 // registers to one of two LDS buffers. Both are loaded one step of 256 K ahead: a row's 128
 // bytes of MXFP4 codes are then one whole cache line, where half steps asked L2 for every
 // line twice. Row scales, one byte a block, come 128 blocks at a time for the same reason.
-// Measured: gate/up, 16384 tokens, H = I = 2880, 4 of 32 experts: MXFP4 0.68 ms (3.2
-// PFLOP/s), MXFP6 0.80 ms. The chip's power bounds it: the clock falls from 2.4 to 1.4-1.8 GHz
-// with the matrix pipes busy 43-47% of the time, and tiles of 128 rows by four or eight waves
-// or of 256 rows all gain 3.6 PFLOP/s over a longer K; with the loads left out it is 5.3, at
-// what the instruction sustains on such operands.
+// Measured, 16384 tokens, H = I = 2880, 4 of 32 experts, skewed, in rows of calls: gate/up MXFP4
+// 0.70 ms (3.1 PFLOP/s), MXFP6 0.84 ms; down 0.43 and 0.48 ms. Over a longer K a tile gains 4.0
+// (MXFP4) and 3.3 PFLOP/s; what it costs before its first and after its last step is the rest,
+// 70 us over 32768 x 4096 fp32 outputs. The matrix pipes are busy 48-51% (MXFP6 37-39%) of the
+// cycles over K = 16384 and 41-44% (33-35%) of gate/up's over 2880, at a clock that the chip's
+// power takes from 2.4 down to 1.4-2.0 GHz; with the loads left out an earlier form reached 5.3
+// PFLOP/s, so the operands' way into registers costs as much as the clock.
 template <int FMT, bool GATED, int MF, int NW>
 __global__ __launch_bounds__(kWave * NW, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k_mx_gemm(
     MxProduct p, int n_mtiles, int n_ntiles, int first) {
@@ -289,7 +292,7 @@ __global__ __launch_bounds__(kWave * NW, MF == 4 ? 2 : MF == 2 ? 3 : 4) void k_m
   // two buffers of rows; the epilogue's fragments take their place
   constexpr int kBuf = BM * kStepBlocks * kBytes;
   constexpr int kPiece = GATED ? 2 : 4;                    // bytes of an output
-  constexpr int kOutRow = 32 * kPiece + 16;                // padded: no bank conflicts
+  constexpr int kOutRow = 32 * kPiece + 16;                // padded against bank conflicts
   constexpr int kTurn = kThreads / kWave * 32 * kOutRow;
   __shared__ __attribute__((aligned(16))) uint8_t lds_q[2 * kBuf > kTurn ? 2 * kBuf : kTurn];
   __shared__ __attribute__((aligned(16))) uint8_t lds_s[BM * kScaleRow];
@@ -564,15 +567,19 @@ hipError_t launch_gemm_t(const MxProduct& p, hipStream_t st) {
 
 // Rows a tile. A tall tile reads the weights less often and feeds more products per operand
 // read; a low one leaves fewer of its rows empty, and there are more of them to fill the CUs.
-// So by the mean rows of an expert: gate/up us with 32 / 64 / 128 rows, H = I = 2880, 32
-// experts, MXFP6, mean 41: 68 / 83 / 84; 125: 119 / 117 / 123; 250: 193 / 176 / 164; H 2048,
-// I 768, 128 experts, MXFP4, mean 62: 44 / 46 / 53; 125: 70 / 60 / 71. And by the tiles that
-// there are (256 CUs hold 512 of 128 rows at once): MXFP4, down, 188 tiles of 128 rows,
-// H 1024, I 1536: 18 / 14 / 22; 63 tiles, H = I = 1024: 9.0 / 12 / 16; gate/up, 564 tiles:
-// 32 / 29 / 31; 1000 tiles, H 256, I 512: 26 / 24 / 23.
+// So by the mean rows of an expert: gate/up, us with 32 / 64 / 128 rows, H = I = 2880, 32
+// experts, MXFP6, mean 41: 74 / 73 / 76; 62: 87 / 90 / 78; 125: 127 / 104 / 136; 250: 204 / 163
+// / 146; where the r-th expert is wanted r^-1.1 times as often: 74 / 86 / 76, 93 / 87 / 108, 127
+// / 111 / 133, 198 / 160 / 166; H 2048, I 768, 128 experts, MXFP4, mean 62: 62 / 56 / 61; 125: 87
+// / 68 / 72. And by the tiles that there are (256 CUs hold 512 of 128 rows at once): MXFP4, down,
+// 184 tiles of 128 rows, H 1024, I 1536: 18 / 15 / 22; 60 tiles, H = I = 1024: 9.7 / 12 / 17;
+// gate/up, 552 tiles: 31 / 27 / 30; 1000 tiles, H 256, I 512: 25 / 22 / 20. Where it loses: down,
+// H = I = 2880, mean 200 to 250, whose 600 to 744 tiles of 128 rows take 73-82 us (MXFP6 68-95)
+// against the 76-94 (83-102) of 64 rows. The height is the same for every expert of a launch.
 // MXFP6 rows take eight waves a tile of 128 x 512: half the row bytes and registers a wave
-// (four waves spill): gate/up, 16384 tokens, H = I = 2880: 939 against 900 us; 4096 tokens,
-// H 4096, I 14336: 763 against 711. MXFP4: 774 against 787 and 627 against 624, so four.
+// (four waves spill): 16384 tokens, H = I = 2880, gate/up 819 against 817 us, down 485 against
+// 466; 4096 tokens, H 4096, I 14336, 681 against 638 and 361 against 359. MXFP4, in the same
+// order: 705 against 724, 421 against 417, 572 against 568, 295 against 306, so four.
 template <int FMT, bool GATED>
 hipError_t launch_t(const MxProduct& p, bool gemv, hipStream_t st) {
   if (gemv) return launch_gemv_t<FMT, GATED>(p, st);

@@ -8,8 +8,9 @@
 // matrix instruction turns that scale into NaN in the rows that it belongs to, and only there.
 // Blocks lie flat in both planes (a row is a whole number of them), so rows do not matter.
 // Copy rate bounds these kernels; see each for its split. Measured on 92160 x 2880 values,
-// MXFP4 / MXFP6: quantise from bf16 114 / 143 us (5.9 / 5.2 TB/s), from fp32 208 / 224 us;
-// dequantise to bf16 158 / 153 us (4.3 / 4.8 TB/s), to fp32 235 / 256 us.
+// MXFP4 / MXFP6, in a kernel trace, three sets of inputs in turn: quantise from bf16 133 / 153 us
+// (5.1 / 4.8 TB/s), from fp32 244 / 259 us (4.9); dequantise to bf16 149 / 147 us (4.5 / 5.0), to
+// fp32 232 / 247 us (5.2 / 5.1).
 #include <algorithm>
 
 #include "common.hpp"
