@@ -8,6 +8,10 @@ is no fallback. If the library has not been built, importing this package raises
     import quantized_routed_expert_gemv_amd as moe
     pool = moe.Pool.from_canonical("mxfp4", H, I, planes)   # planes indexed by slot
     out = moe.layer(pool, slot_map, w_router, bias, x, k)
+
+Calls run on the current stream, or on the torch stream given as `stream`. Tensors that a call
+makes belong to the stream it runs on, as ones made under `with torch.cuda.stream(stream)` do:
+used on another stream, they need its wait, and Tensor.record_stream before they are let go.
 """
 from __future__ import annotations
 
@@ -512,8 +516,7 @@ class LayerCall:
 
 # --------------------------------------------- microscaled rows, and the block's two ends
 #
-# stream: the torch stream to run on, of the tensors' device (default: the current one). Outputs
-# that a call makes are that stream's, as tensors made under `with torch.cuda.stream(stream)` are.
+# A given stream has to be of the tensors' device.
 
 
 def _one_of(name, value, choices):
