@@ -479,6 +479,143 @@ moe_status moe_combine_norm(const float* y, const int32_t* inv_perm, const float
                             int32_t weight_type, float eps, void* resid_out, uint16_t* x,
                             void* stream);
 
+/*
+ * The attention half of the block, between moe_combine_norm's x (or an embedding) and
+ * moe_add_norm's delta: dense products, rotary positions, a paged cache of keys and values, and
+ * attention of new tokens over it ([T] "How it works": sink tokens with a sliding window, a
+ * static cache, 8-bit keys and values). All arithmetic is fp32 unless said otherwise, and each
+ * output is rounded once, to nearest even.
+ *
+ * Rows of heads: x [T][n_heads][D] are addressed by strides, value (t, h, d) at t * token +
+ * h * head + d elements, so q, k and v can be parts of the rows that one product wrote.
+ */
+typedef struct {
+  void* p;
+  int64_t token, head;   /* strides in elements, not negative */
+} moe_heads;
+
+/*
+ * moe_rope -- rotary positions. The first dim values of a head turn, the rest pass: pair i of
+ * dim / 2 turns by the angle a = position * freq[i],
+ *   (u, v) -> scale * (u cos a - v sin a, u sin a + v cos a)
+ * where (u, v) is (x[i], x[i + dim/2]) for MOE_ROPE_HALF and (x[2i], x[2i+1]) for
+ * MOE_ROPE_INTERLEAVED. Angles are formed in fp64, so far positions keep theirs. inverse turns
+ * by -a with the same scale: the transposed map, which is the rotation's gradient.
+ *   freq fp64 [dim/2] radians a position, 8-byte aligned; dim even, 2 <= dim <= D <= 1024
+ *   x, out of type (moe_dtype) [T][n_heads][D]; out is x itself (same strides) or apart from it
+ *   positions int32 [T]; n_heads * D <= 2^28, T * n_heads <= 2^30
+ */
+typedef enum { MOE_ROPE_HALF = 0, MOE_ROPE_INTERLEAVED = 1 } moe_rope_layout;
+typedef struct {
+  const double* freq;
+  int32_t dim;
+  int32_t layout;        /* moe_rope_layout */
+  float scale;
+} moe_rope_plan;
+moe_status moe_rope(const moe_rope_plan* plan, const moe_heads* x, int32_t type, int32_t T,
+                    int32_t n_heads, int32_t D, const int32_t* positions, int32_t inverse,
+                    const moe_heads* out, void* stream);
+
+/*
+ * Paged cache of keys and values: n_pages pages of page_size tokens, value (page, token, head, d)
+ * at page * k_page + token * k_token + head * k_head + d elements of k, likewise of v. k and v are
+ * 16-byte aligned and their strides multiples of 16 bytes, not negative.
+ *   type      MOE_T_BF16, MOE_T_FP16 or MOE_T_E4M3 (8 bits, OCP)
+ *   D         multiple of 16, at most 256;  page_size >= 1
+ *   k_scale, v_scale  fp32 [n_heads] or NULL (ones), MOE_T_E4M3 only: a key is code * k_scale[h]
+ *
+ * A batch: n_seq sequences, whose new tokens' rows stand one sequence after the other in T rows.
+ *   q_start    int32 [n_seq + 1]: rows q_start[b] .. q_start[b+1] - 1 are sequence b's, q_start[0]
+ *              = 0; rows from q_start[n_seq] on are padding
+ *   seq_len    int32 [n_seq]: keys of each sequence, its new tokens included: its new token i is
+ *              at position seq_len[b] - (q_start[b+1] - q_start[b]) + i
+ *   page_table int32 [n_seq] rows of max_pages entries, table_stride apart: entry p of row b is the
+ *              page of positions p * page_size .. of sequence b
+ *   max_q, max_len   the largest number of new tokens and of keys of a sequence, or 0 where they
+ *              are not known. They choose the launch; results do not depend on their truth.
+ * T * n_heads <= 2^30, n_seq < 2^24. Values outside these rules in device memory (rows past T, pages
+ * outside the cache, positions below zero or past the table) are never followed: what would be
+ * there is left out, and bit 0 of *err_flags is set (nullable uint32, atomic OR). Entries of pages
+ * that no key in sight lies on are not read.
+ */
+#define MOE_T_E4M3 4   /* a moe_dtype, of caches only */
+typedef struct {
+  int32_t type, n_pages, page_size, n_heads, D;
+  void* k; int64_t k_page, k_token, k_head;
+  void* v; int64_t v_page, v_token, v_head;
+  const float* k_scale;
+  const float* v_scale;
+} moe_kv_cache;
+typedef struct {
+  int32_t n_seq, T;
+  const int32_t* q_start;
+  const int32_t* seq_len;
+  const int32_t* page_table;
+  int32_t max_pages;
+  int64_t table_stride;
+  int32_t max_q, max_len;
+} moe_kv_batch;
+
+/*
+ * moe_kv_append -- the new tokens' keys and values go to their places in the cache, keys (and
+ * queries, where given) turned on the way.
+ *   k, v     rows of type (bf16 or fp16; fp32 too) [T][cache->n_heads][D]
+ *   rope     NULL: keys and queries do not turn
+ *   positions int32 [T] to turn by, or NULL: each token's place in its sequence
+ *   q, q_out rows [T][n_q_heads][D] of type, q_out may be q itself; both NULL: no queries
+ * Values are rounded to the cache's type; MOE_T_E4M3 codes are value / scale, saturated at 448 (NaN
+ * stays NaN). Two new tokens on one place of the cache are a caller error: either is kept.
+ * Padding rows of q_out are left as they are.
+ */
+moe_status moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_heads* k,
+                         const moe_heads* v, int32_t type, const moe_rope_plan* rope,
+                         const int32_t* positions, const moe_heads* q, int32_t n_q_heads,
+                         const moe_heads* q_out, uint32_t* err_flags, void* stream);
+
+/*
+ * moe_attend -- attention of the new tokens over the cache. Query head j reads KV head
+ * j / (n_q_heads / cache->n_heads). A token at position p sees key j of its sequence where
+ *   causal: j <= p;  window > 0 (causal only): also j > p - window or j < keep_first
+ *   not causal: j < seq_len[b]
+ * With s_j = scale * <q, k_j> over the keys in sight:
+ *   out = sum_j e^{s_j} v_j / (sum_j e^{s_j} + e^{sinks[head]})      (sinks fp32 [n_q_heads], or
+ *   NULL: no such term). A token that sees no key gets zeros. Keys and values out of sight do not
+ *   reach a row, whatever they hold, infinities and NaN among it.
+ *   q, out of type (bf16, fp16) [T][n_q_heads][D], 16-byte aligned, strides multiples of 8; a 16-bit
+ *   cache is of the same type; n_q_heads a multiple of cache->n_heads; scale is finite
+ *   Products are of 16-bit operands, summed in fp32; softmax statistics are fp32 and its weights
+ *   are rounded to type before they meet the values.
+ *   scratch: at least moe_attend_scratch_bytes(...) bytes, 16-byte aligned (NULL where that is 0);
+ *   calls that share it must not overlap in time. Padding rows of out are left as they are.
+ */
+size_t moe_attend_scratch_bytes(const moe_kv_cache* cache, const moe_kv_batch* batch,
+                                int32_t n_q_heads, int32_t window, int32_t keep_first);
+moe_status moe_attend(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_heads* q,
+                      int32_t type, int32_t n_q_heads, float scale, int32_t causal, int32_t window,
+                      int32_t keep_first, const float* sinks, const moe_heads* out, void* scratch,
+                      size_t scratch_bytes, uint32_t* err_flags, void* stream);
+
+/*
+ * moe_linear -- out = resid + act(x w^T + bias): the projections on both sides of attention, or a
+ * dense expert that every token takes.
+ *   x [M][K], w [N][K] of type (bf16 or fp16), rows x_stride and w_stride elements apart, both
+ *   16-byte aligned with strides and K multiples of 8; products are exact, sums fp32
+ *   bias  [N] of bias_type (moe_dtype), or NULL
+ *   resid [M][N] of out_type, rows resid_stride apart, or NULL
+ *   out   [M][N] of out_type (moe_dtype), rows out_stride apart; may be resid itself
+ *   act   moe_act: GELU is 0.5 v (1 + erf(v / sqrt 2)), GELU_TANH 0.5 v (1 + tanh(sqrt(2/pi)
+ *         (v + 0.044715 v^3))), SILU v / (1 + e^-v)
+ *   bias, resid and out need no alignment beyond their elements'. M, N < 2^30; M * N, M * x_stride and
+ *   N * w_stride below 2^40. K = 0 gives resid + act(bias).
+ */
+typedef enum {
+  MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_GELU = 2, MOE_ACT_GELU_TANH = 3, MOE_ACT_SILU = 4
+} moe_act;
+moe_status moe_linear(const void* x, int64_t x_stride, const void* w, int64_t w_stride,
+                      int32_t type, int32_t M, int32_t N, int32_t K, const void* bias,
+                      int32_t bias_type, int32_t act, const void* resid, int64_t resid_stride,
+                      void* out, int32_t out_type, int64_t out_stride, void* stream);
+
 const char* moe_status_string(moe_status s);
 const char* moe_last_error(void);
 

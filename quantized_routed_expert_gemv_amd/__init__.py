@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -107,6 +108,39 @@ _add_norm = _sig("moe_add_norm", _i32, _p, _i32, _p, _i32, _f32, _p, _i32, _f32,
                  _p, _p)
 _combine_norm = _sig("moe_combine_norm", _i32, _p, _p, _p, _i32, _i32, _i32, _p, _i32, _p, _p,
                      _i32, _f32, _p, _i32, _f32, _p, _p, _p)
+_i64 = ctypes.c_int64
+
+
+class HeadsStruct(ctypes.Structure):
+    _fields_ = [("p", _p), ("token", _i64), ("head", _i64)]
+
+
+class RopeStruct(ctypes.Structure):
+    _fields_ = [("freq", _p), ("dim", _i32), ("layout", _i32), ("scale", _f32)]
+
+
+class KvCacheStruct(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("type", "n_pages", "page_size", "n_heads", "D")] + \
+               [("k", _p), ("k_page", _i64), ("k_token", _i64), ("k_head", _i64),
+                ("v", _p), ("v_page", _i64), ("v_token", _i64), ("v_head", _i64),
+                ("k_scale", _p), ("v_scale", _p)]
+
+
+class KvBatchStruct(ctypes.Structure):
+    _fields_ = [("n_seq", _i32), ("T", _i32), ("q_start", _p), ("seq_len", _p), ("page_table", _p),
+                ("max_pages", _i32), ("table_stride", _i64), ("max_q", _i32), ("max_len", _i32)]
+
+
+_heads_p, _rope_p = ctypes.POINTER(HeadsStruct), ctypes.POINTER(RopeStruct)
+_cache_p, _batch_p = ctypes.POINTER(KvCacheStruct), ctypes.POINTER(KvBatchStruct)
+_rope = _sig("moe_rope", _i32, _rope_p, _heads_p, _i32, _i32, _i32, _i32, _p, _i32, _heads_p, _p)
+_kv_append = _sig("moe_kv_append", _i32, _cache_p, _batch_p, _heads_p, _heads_p, _i32, _rope_p, _p,
+                  _heads_p, _i32, _heads_p, _p, _p)
+_attend_scratch = _sig("moe_attend_scratch_bytes", _sz, _cache_p, _batch_p, _i32, _i32, _i32)
+_attend = _sig("moe_attend", _i32, _cache_p, _batch_p, _heads_p, _i32, _i32, _f32, _i32, _i32, _i32,
+               _p, _heads_p, _p, _sz, _p, _p)
+_linear = _sig("moe_linear", _i32, _p, _i64, _p, _i64, _i32, _i32, _i32, _i32, _p, _i32, _i32, _p,
+               _i64, _p, _i32, _i64, _p)
 _status_string = _sig("moe_status_string", ctypes.c_char_p, _i32)
 _last_error = _sig("moe_last_error", ctypes.c_char_p)
 
@@ -117,6 +151,7 @@ EXPORTED = ("moe_plane_bytes", "moe_pool_pack", "moe_route_scratch_bytes", "moe_
             "moe_layer_workspace", "moe_layer", "moe_layer_timed", "moe_layer_noalloc",
             "moe_mx_row_bytes", "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_expert_gate_up",
             "moe_mx_expert_down", "moe_mx_expert_ffn", "moe_add_norm", "moe_combine_norm",
+            "moe_rope", "moe_kv_append", "moe_attend_scratch_bytes", "moe_attend", "moe_linear",
             "moe_status_string", "moe_last_error")
 
 NOALLOC_WS_BYTES = 32 << 20   # MOE_NOALLOC_WS_BYTES
@@ -742,3 +777,293 @@ def combine_norm(y, inv_perm, w, resid, eps: float = 1e-6, post_weight=None, gat
          T if gate is not None and gate.dim() == 2 else 1, scale, _addr(next_weight),
          _DT[given[0].dtype] if given else _DT[torch.float32], eps, _addr(resid_out), _addr(x))
     return resid_out, x
+
+
+# ------------------------------------------------------- the attention half of the block
+
+
+_HALF_TYPES = (torch.bfloat16, torch.float16)
+_CACHE_TYPES = {torch.bfloat16: 1, torch.float16: 2, torch.float8_e4m3fn: 4}   # MOE_T_E4M3
+_LAYOUTS = {"half": 0, "interleaved": 1}                                       # moe_rope_layout
+_ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}           # moe_act
+
+
+def _strided(t, dtypes, shape, name, like):
+    """A device tensor of one of `dtypes` whose last dimension is dense, on the device of `like`."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be dense")
+    if not t.get_device() == like.get_device() >= 0:
+        raise ValueError(f"{name}: on {t.device}, expected " +
+                         (str(like.device) if like.is_cuda else "a device tensor"))
+
+
+def _stride(t, i):
+    return t.stride(i) if t.shape[i] > 1 else 0   # of one element: any, and it need not be aligned
+
+
+def _heads(t):
+    return HeadsStruct(t.data_ptr(), _stride(t, 0), _stride(t, 1))
+
+
+def _new_like(shape, dtype, like, stream):
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with _on(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _check_flags(err_flags, like):
+    if err_flags is not None and (err_flags.device != like.device or err_flags.numel() < 1 or
+                                  err_flags.element_size() != 4):
+        raise ValueError("err_flags: needs 32-bit words on the operands' device")
+
+
+class Rope:
+    """Rotary positions: freq float64 [dim/2] radians a position on the device, the layout of the
+    pairs ("half": values i and i + dim/2, "interleaved": 2i and 2i + 1), and a factor on the
+    turned values."""
+
+    def __init__(self, freq, layout: str = "half", scale: float = 1.0):
+        _one_of("layout", layout, _LAYOUTS)
+        _tensor(freq, (torch.float64,), (freq.numel(),), "freq", freq)
+        if freq.numel() > _SIZE // 2:
+            _too_large(2 * freq.numel())
+        self.freq, self.layout, self.scale = freq, layout, scale
+        self.struct = RopeStruct(freq.data_ptr(), 2 * freq.numel(), _LAYOUTS[layout], scale)
+
+    @classmethod
+    def make(cls, dim: int, base: float = 10000.0, layout: str = "half", scaling: str = "none",
+             factor: float = 1.0, original: int = 4096, beta_fast: float = 32.0,
+             beta_slow: float = 1.0, device="cuda"):
+        """Frequencies base^(-2i/dim), scaled for contexts `factor` times as long:
+        "linear"  all of them over factor;
+        "ntk"     base * factor^(dim/(dim-2)): the slowest pair over factor, the fastest kept;
+        "yarn"    pairs that turn more than beta_fast times over `original` positions kept, those
+                  below beta_slow over factor, a ramp between; turned values times
+                  0.1 ln(factor) + 1."""
+        _one_of("scaling", scaling, ("none", "linear", "ntk", "yarn"))
+        if dim < 2 or dim % 2:
+            raise ValueError(f"dim: {dim}, expected a positive even number")
+        if not base > 1 or not factor > 0:
+            raise ValueError(f"base {base}, factor {factor}: base > 1 and factor > 0")
+        if scaling == "ntk":
+            if dim == 2:
+                raise ValueError("ntk: needs dim > 2")
+            base = base * factor ** (dim / (dim - 2))
+        i = torch.arange(dim // 2, dtype=torch.float64)
+        freq, scale = base ** (-2 * i / dim), 1.0
+        if scaling == "linear":
+            freq = freq / factor
+        elif scaling == "yarn":
+            def pair(turns):   # the (fractional) pair that turns so often over `original` positions
+                return dim * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
+            lo, hi = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), dim - 1)
+            slow = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+            freq = freq * (1 - slow) + freq / factor * slow
+            scale = 0.1 * math.log(factor) + 1 if factor > 1 else 1.0
+        return cls(freq.to(device), layout, scale)
+
+
+class KvCache:
+    """Paged keys and values: k, v [n_pages, page_size, n_heads, D] bf16, fp16 or float8_e4m3fn, the
+    last dimension dense, the others with any strides of whole 16 bytes (a page's tokens or its
+    heads first, k and v in one tensor). k_scale, v_scale: float32 [n_heads] or None, of an 8-bit
+    cache: a key is code * k_scale[head]."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dim() != 4:
+            raise ValueError(f"k: {k.dim()} dimensions, expected [n_pages, page_size, n_heads, D]")
+        if max(k.shape) > _SIZE:
+            _too_large(*k.shape)
+        _strided(k, tuple(_CACHE_TYPES), k.shape, "k", k)
+        _strided(v, (k.dtype,), k.shape, "v", k)
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is not None:
+                _tensor(t, (torch.float32,), (k.shape[2],), name, k)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.page_size, self.n_heads, self.D = k.shape
+        self.struct = KvCacheStruct(_CACHE_TYPES[k.dtype], *k.shape,
+                                    k.data_ptr(), *(_stride(k, i) for i in range(3)),
+                                    v.data_ptr(), *(_stride(v, i) for i in range(3)),
+                                    _addr(k_scale), _addr(v_scale))
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, n_heads: int, D: int, dtype=torch.bfloat16,
+              k_scale=None, v_scale=None, device="cuda"):
+        """A cache whose pages hold one head after the other."""
+        k, v = (torch.empty(n_pages, n_heads, page_size, D, dtype=dtype, device=device)
+                .transpose(1, 2) for _ in range(2))
+        return cls(k, v, k_scale, v_scale)
+
+
+class KvBatch:
+    """The sequences of a step: q_start int32 [n_seq + 1], seq_len int32 [n_seq] (keys of each, its
+    new tokens included), page_table int32 [n_seq, max_pages]. max_q and max_len, the largest number
+    of new tokens and of keys of a sequence, choose the launch; results do not depend on them."""
+
+    def __init__(self, q_start, seq_len, page_table, max_q: int = 0, max_len: int = 0):
+        i32, n = (torch.int32,), seq_len.shape[0]
+        _tensor(seq_len, i32, (n,), "seq_len", seq_len)
+        _tensor(q_start, i32, (n + 1,), "q_start", seq_len)
+        if page_table.dim() != 2:
+            raise ValueError("page_table: expected [n_seq, max_pages]")
+        _strided(page_table, i32, (n, page_table.shape[1]), "page_table", seq_len)
+        if max(n, page_table.shape[1], max_q, max_len) > _SIZE:
+            _too_large(n, page_table.shape[1], max_q, max_len)
+        self.q_start, self.seq_len, self.page_table = q_start, seq_len, page_table
+        self.n_seq, self.max_q, self.max_len = n, max_q, max_len
+        self._structs, self._scratch = {}, {}
+
+    def struct(self, T: int):
+        """The C structure for T rows of new tokens."""
+        s = self._structs.get(T)
+        if s is None:
+            s = self._structs[T] = KvBatchStruct(
+                self.n_seq, T, self.q_start.data_ptr(), self.seq_len.data_ptr(),
+                self.page_table.data_ptr(), self.page_table.shape[1], _stride(self.page_table, 0),
+                self.max_q, self.max_len)
+        return s
+
+
+def _same_device(name, t, like):
+    if t.device != like.device:
+        raise ValueError(f"{name}: on {t.device}, expected {like.device}")
+
+
+def rope(x, positions, plan: Rope, inverse: bool = False, out=None, stream=None):
+    """x bf16, fp16 or fp32 [T, n_heads, D] (any strides, D dense) with the first plan dimensions of
+    each head turned by positions int32 [T] -> out like x. inverse: turned back, which is also the
+    gradient's map. out may be x."""
+    if x.dim() != 3:
+        raise ValueError(f"x: {x.dim()} dimensions, expected [T, n_heads, D]")
+    T, n, D = x.shape
+    if max(T, n, D) > _SIZE:
+        _too_large(T, n, D)
+    _strided(x, _DT, (T, n, D), "x", x)
+    _tensor(positions, (torch.int32,), (T,), "positions", x)
+    _same_device("plan", plan.freq, x)
+    if out is None:
+        out = _new_like((T, n, D), x.dtype, x, stream)
+    else:
+        _strided(out, (x.dtype,), (T, n, D), "out", x)
+    _run(_rope, x, stream, plan.struct, _heads(x), _DT[x.dtype], T, n, D, positions.data_ptr(),
+         int(inverse), _heads(out))
+    return out
+
+
+def kv_append(cache: KvCache, batch: KvBatch, k, v, rope: Rope = None, positions=None, q=None,
+              q_out=None, err_flags=None, stream=None):
+    """The new tokens' keys and values, bf16, fp16 or fp32 [T, n_heads, D] (any strides, D dense), go
+    to their places in the cache; keys, and queries q [T, n_q_heads, D], turn by the tokens' places
+    in their sequences, or by positions int32 [T] -> q_out like q, or None without q. q_out may be
+    q."""
+    if k.dim() != 3:
+        raise ValueError(f"k: {k.dim()} dimensions, expected [T, n_heads, D]")
+    T = k.shape[0]
+    if T > _SIZE:
+        _too_large(T)
+    _strided(k, _DT, (T, cache.n_heads, cache.D), "k", k)
+    _strided(v, (k.dtype,), k.shape, "v", k)
+    _same_device("cache", cache.k, k)
+    _same_device("batch", batch.seq_len, k)
+    if rope is not None:
+        _same_device("rope", rope.freq, k)
+    if positions is not None:
+        _tensor(positions, (torch.int32,), (T,), "positions", k)
+    _check_flags(err_flags, k)
+    n_q = 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[1] > _SIZE:
+            raise ValueError(f"q: shape {tuple(q.shape)}, expected [T, n_q_heads, D]")
+        n_q = q.shape[1]
+        _strided(q, (k.dtype,), (T, n_q, cache.D), "q", k)
+        if q_out is None:
+            q_out = _new_like(q.shape, q.dtype, q, stream)
+        else:
+            _strided(q_out, (k.dtype,), q.shape, "q_out", k)
+    elif q_out is not None:
+        raise ValueError("q_out: needs q")
+    _run(_kv_append, k, stream, cache.struct, batch.struct(T), _heads(k), _heads(v), _DT[k.dtype],
+         None if rope is None else rope.struct, _addr(positions), None if q is None else _heads(q),
+         n_q, None if q is None else _heads(q_out), _addr(err_flags))
+    return q_out
+
+
+def attend_scratch_bytes(cache: KvCache, batch: KvBatch, T: int, n_q_heads: int, window: int = 0,
+                         keep_first: int = 0) -> int:
+    if max(T, n_q_heads, window, keep_first) > _SIZE:
+        _too_large(T, n_q_heads, window, keep_first)
+    return _attend_scratch(cache.struct, batch.struct(T), n_q_heads, window, keep_first)
+
+
+def attend(q, cache: KvCache, batch: KvBatch, scale: float = None, causal: bool = True,
+           window: int = 0, keep_first: int = 0, sinks=None, out=None, scratch=None,
+           err_flags=None, stream=None):
+    """Attention of the new tokens q bf16 or fp16 [T, n_q_heads, D] over the cache -> out like q.
+
+    A token at position p sees the keys up to p of its sequence (causal), with a window those past
+    p - window and the first keep_first only. scale defaults to 1/sqrt(D); sinks float32 [n_q_heads]
+    are logits that take weight and have no value. scratch: uint8, attend_scratch_bytes of it."""
+    if q.dim() != 3:
+        raise ValueError(f"q: {q.dim()} dimensions, expected [T, n_q_heads, D]")
+    T, n, D = q.shape
+    if T > _SIZE or n > _SIZE:
+        _too_large(T, n)
+    _strided(q, _HALF_TYPES, (T, n, cache.D), "q", q)
+    _same_device("cache", cache.k, q)
+    _same_device("batch", batch.seq_len, q)
+    if sinks is not None:
+        _tensor(sinks, (torch.float32,), (n,), "sinks", q)
+    _check_flags(err_flags, q)
+    if out is None:
+        out = _new_like((T, n, D), q.dtype, q, stream)
+    else:
+        _strided(out, (q.dtype,), (T, n, D), "out", q)
+    key = (cache.n_heads, D, cache.page_size, T, n, window, keep_first)
+    need = batch._scratch.get(key)
+    if need is None:
+        need = batch._scratch[key] = attend_scratch_bytes(cache, batch, T, n, window, keep_first)
+    if scratch is not None:
+        _tensor(scratch, (torch.uint8,), (scratch.numel(),), "scratch", q)
+    elif need:
+        scratch = _new_like((need,), torch.uint8, q, stream)
+    _run(_attend, q, stream, cache.struct, batch.struct(T), _heads(q), _DT[q.dtype], n,
+         D ** -0.5 if scale is None else scale, int(causal), window, keep_first, _addr(sinks),
+         _heads(out), _addr(scratch), 0 if scratch is None else scratch.numel(), _addr(err_flags))
+    return out
+
+
+def linear(x, w, bias=None, act: str = "none", resid=None, out_dtype=None, out=None, stream=None):
+    """resid + act(x w^T + bias): x [M, K] and w [N, K] bf16 or fp16 (rows dense), bias [N] and resid
+    [M, N] of any float type, act "none", "relu", "gelu", "gelu_tanh" or "silu" -> out [M, N] of
+    out_dtype (resid's type, or x's without one). out may be resid."""
+    _one_of("act", act, _ACTS)
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x, w: expected [M, K] and [N, K]")
+    (M, K), N = x.shape, w.shape[0]
+    if max(M, N, K) > _SIZE:
+        _too_large(M, N, K)
+    _strided(x, _HALF_TYPES, (M, K), "x", x)
+    _strided(w, (x.dtype,), (N, K), "w", x)
+    if bias is not None:
+        _tensor(bias, _DT, (N,), "bias", x)
+    if out is not None and out_dtype is None:
+        out_dtype = out.dtype
+    if out_dtype is None:
+        out_dtype = x.dtype if resid is None else resid.dtype
+    _one_of("out_dtype", out_dtype, _DT)
+    if resid is not None:
+        _strided(resid, (out_dtype,), (M, N), "resid", x)
+    if out is None:
+        out = _new_like((M, N), out_dtype, x, stream)
+    else:
+        _strided(out, (out_dtype,), (M, N), "out", x)
+    _run(_linear, x, stream, x.data_ptr(), _stride(x, 0), w.data_ptr(), _stride(w, 0), _DT[x.dtype],
+         M, N, K, _addr(bias), 0 if bias is None else _DT[bias.dtype], _ACTS[act], _addr(resid),
+         0 if resid is None else _stride(resid, 0), out.data_ptr(), _DT[out_dtype],
+         out.stride(0) if M > 1 else N)
+    return out

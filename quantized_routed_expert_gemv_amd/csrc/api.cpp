@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cfloat>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -968,6 +969,286 @@ moe_status moe_combine_norm(const float* y, const int32_t* inv_perm, const float
   clear_stale_error();
   return hip_status(moe::launch_block_norm(a, true, resid_type == MOE_T_FP32, (hipStream_t)stream),
                     "combine + norm");
+}
+
+namespace {
+
+// The rows of the attention half of a block.
+moe_status check_heads(const char* name, const moe_heads* h, int align, int64_t stride) {
+  if (h == nullptr || h->p == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", name);
+  if ((uintptr_t)h->p & (align - 1))
+    return fail(MOE_ERR_INVALID_ARG, "%s is not %d-byte aligned", name, align);
+  if (h->token < 0 || h->head < 0 || h->token % stride || h->head % stride)
+    return fail(MOE_ERR_INVALID_ARG, "%s strides (%lld, %lld): not negative, multiples of %lld", name,
+                (long long)h->token, (long long)h->head, (long long)stride);
+  if (h->token >= (int64_t(1) << 32) || h->head >= (int64_t(1) << 32))
+    return fail(MOE_ERR_INVALID_ARG, "%s strides: limit 2^32", name);
+  return MOE_OK;
+}
+moe::HeadsView heads_view(const moe_heads* h) { return {(uint8_t*)h->p, h->token, h->head}; }
+bool same_heads(const moe_heads* a, const moe_heads* b) {
+  return a->p != b->p || (a->token == b->token && a->head == b->head);
+}
+
+int type_bytes(int32_t type) { return type == MOE_T_FP32 ? 4 : type == MOE_T_E4M3 ? 1 : 2; }
+
+moe_status check_rope(const moe_rope_plan* plan, int32_t D) {
+  if (plan == nullptr) return fail(MOE_ERR_INVALID_ARG, "plan is NULL");
+  if (plan->layout != MOE_ROPE_HALF && plan->layout != MOE_ROPE_INTERLEAVED)
+    return fail(MOE_ERR_UNSUPPORTED, "unknown rope layout %d", plan->layout);
+  if (plan->dim < 2 || plan->dim % 2 || plan->dim > D)
+    return fail(MOE_ERR_INVALID_ARG, "rope dim = %d: even, in [2, D = %d]", plan->dim, D);
+  if (plan->freq == nullptr || ((uintptr_t)plan->freq & 7))
+    return fail(MOE_ERR_INVALID_ARG, "rope freq is %s",
+                plan->freq ? "not 8-byte aligned" : "NULL");
+  return MOE_OK;
+}
+moe::RopeView rope_view(const moe_rope_plan* p) {
+  if (p == nullptr) return {nullptr, 0, false, 1.f};
+  return {p->freq, p->dim, p->layout == MOE_ROPE_INTERLEAVED, p->scale};
+}
+
+moe_status check_cache(const moe_kv_cache* c) {
+  if (c == nullptr) return fail(MOE_ERR_INVALID_ARG, "cache is NULL");
+  if (c->type != MOE_T_BF16 && c->type != MOE_T_FP16 && c->type != MOE_T_E4M3)
+    return fail(MOE_ERR_UNSUPPORTED, "unknown cache type %d", c->type);
+  if (c->n_pages < 1 || c->page_size < 1 || c->n_heads < 1)
+    return fail(MOE_ERR_INVALID_ARG, "cache of %d pages, %d tokens a page, %d heads", c->n_pages,
+                c->page_size, c->n_heads);
+  if (c->D < 16 || c->D > 256 || c->D % 16)
+    return fail(MOE_ERR_INVALID_ARG, "cache D = %d: a multiple of 16, at most 256", c->D);
+  CHECK_PTR(c->k);
+  CHECK_PTR(c->v);
+  const int64_t mult = 16 / type_bytes(c->type);
+  for (const int64_t st : {c->k_page, c->k_token, c->k_head, c->v_page, c->v_token, c->v_head})
+    if (st < 0 || st % mult || st >= (int64_t(1) << 32))
+      return fail(MOE_ERR_INVALID_ARG, "cache stride %lld: not negative, a multiple of %lld, below 2^32",
+                  (long long)st, (long long)mult);
+  if ((c->k_scale != nullptr || c->v_scale != nullptr) && c->type != MOE_T_E4M3)
+    return fail(MOE_ERR_INVALID_ARG, "scales go with an E4M3 cache");
+  if (((uintptr_t)c->k_scale | (uintptr_t)c->v_scale) & 3)
+    return fail(MOE_ERR_INVALID_ARG, "cache scales misaligned");
+  return MOE_OK;
+}
+moe::KvCacheView cache_view(const moe_kv_cache* c) {
+  return {(uint8_t*)c->k, (uint8_t*)c->v, c->k_page, c->k_token, c->k_head, c->v_page, c->v_token,
+          c->v_head, c->k_scale, c->v_scale, c->type, c->n_pages, c->page_size, c->n_heads, c->D,
+          0xFFFFFFFFu / (uint32_t)c->page_size};
+}
+
+// The sizes of a batch. Its pointers are checked where there are rows (check_batch_ptrs).
+moe_status check_batch(const moe_kv_batch* b, const moe_kv_cache* c, int64_t n_q_heads) {
+  if (b == nullptr) return fail(MOE_ERR_INVALID_ARG, "batch is NULL");
+  if (b->n_seq < 0 || b->n_seq >= (1 << 24))
+    return fail(MOE_ERR_INVALID_ARG, "n_seq = %d outside [0, 2^24)", b->n_seq);
+  if (b->T < 0) return fail(MOE_ERR_INVALID_ARG, "T = %d < 0", b->T);
+  const int64_t heads = n_q_heads > c->n_heads ? n_q_heads : c->n_heads;
+  if (heads * c->D > (1 << 28) || heads * (b->T > 0 ? b->T : 1) > (1 << 30))
+    return fail(MOE_ERR_INVALID_ARG, "%lld heads, D = %d, T = %d: heads * D <= 2^28, T * heads <= 2^30",
+                (long long)heads, c->D, b->T);
+  if (b->max_pages < 1 || (int64_t)b->max_pages * c->page_size > 0x7FFFF000)
+    return fail(MOE_ERR_INVALID_ARG, "page table of %d pages of %d tokens: 1 to 2^31 - 4096 tokens",
+                b->max_pages, c->page_size);
+  if (b->table_stride < 0 || b->table_stride >= (int64_t(1) << 32))
+    return fail(MOE_ERR_INVALID_ARG, "table_stride = %lld", (long long)b->table_stride);
+  if (b->max_q < 0 || b->max_len < 0)
+    return fail(MOE_ERR_INVALID_ARG, "max_q = %d, max_len = %d", b->max_q, b->max_len);
+  return MOE_OK;
+}
+moe_status check_batch_ptrs(const moe_kv_batch* b, const uint32_t* err_flags) {
+  const struct { const char* name; const void* p; } all[] = {
+      {"q_start", b->q_start}, {"seq_len", b->seq_len}, {"page_table", b->page_table}};
+  for (const auto& a : all) {
+    if (a.p == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", a.name);
+    if ((uintptr_t)a.p & 3) return fail(MOE_ERR_INVALID_ARG, "%s misaligned", a.name);
+  }
+  if ((uintptr_t)err_flags & 3) return fail(MOE_ERR_INVALID_ARG, "err_flags misaligned");
+  return MOE_OK;
+}
+moe::KvBatchView batch_view(const moe_kv_batch* b) {
+  return {b->q_start, b->seq_len, b->page_table, b->table_stride, b->n_seq, b->T, b->max_pages};
+}
+
+moe_status check_attend(const moe_kv_cache* c, const moe_kv_batch* b, int32_t n_q_heads,
+                        int32_t window, int32_t keep_first) {
+  moe_status s = check_cache(c);
+  if (s != MOE_OK) return s;
+  if (n_q_heads < 1 || n_q_heads % c->n_heads)
+    return fail(MOE_ERR_INVALID_ARG, "n_q_heads = %d is not a multiple of the cache's %d", n_q_heads,
+                c->n_heads);
+  s = check_batch(b, c, n_q_heads);
+  if (s != MOE_OK) return s;
+  if (window < 0 || keep_first < 0)
+    return fail(MOE_ERR_INVALID_ARG, "window = %d, keep_first = %d", window, keep_first);
+  return MOE_OK;
+}
+int splits_of(const moe_kv_cache* c, const moe_kv_batch* b, int32_t n_q_heads, int32_t window,
+              int32_t keep_first) {
+  return moe::attend_splits(cache_view(c), batch_view(b), n_q_heads, window, keep_first, b->max_q,
+                            b->max_len);
+}
+size_t attend_scratch(const moe_kv_cache* c, const moe_kv_batch* b, int32_t n_q_heads, int splits) {
+  if (splits <= 1) return 0;
+  return (size_t)splits * b->T * n_q_heads * (c->D + 2) * sizeof(float);
+}
+
+moe_status check_16bit(const char* name, int32_t type) {
+  if (type == MOE_T_BF16 || type == MOE_T_FP16) return MOE_OK;
+  return fail(MOE_ERR_UNSUPPORTED, "%s type %d", name, type);
+}
+
+}  // namespace
+
+moe_status moe_rope(const moe_rope_plan* plan, const moe_heads* x, int32_t type, int32_t T,
+                    int32_t n_heads, int32_t D, const int32_t* positions, int32_t inverse,
+                    const moe_heads* out, void* stream) {
+  moe_status s = check_type("x", type, true);
+  if (s != MOE_OK) return s;
+  if (T < 0 || n_heads < 1 || D < 2 || D > 1024 || (int64_t)n_heads * D > (1 << 28) ||
+      (int64_t)T * n_heads > (1 << 30))
+    return fail(MOE_ERR_INVALID_ARG,
+                "T = %d, n_heads = %d, D = %d: D in [2, 1024], n_heads * D <= 2^28, T * n_heads <= 2^30",
+                T, n_heads, D);
+  if ((s = check_rope(plan, D)) != MOE_OK) return s;
+  if (T == 0) return ok();
+  if ((s = check_heads("x", x, type_bytes(type), 1)) != MOE_OK) return s;
+  if ((s = check_heads("out", out, type_bytes(type), 1)) != MOE_OK) return s;
+  if (!same_heads(x, out)) return fail(MOE_ERR_INVALID_ARG, "out is x with other strides");
+  if (positions == nullptr || ((uintptr_t)positions & 3))
+    return fail(MOE_ERR_INVALID_ARG, "positions is %s", positions ? "misaligned" : "NULL");
+  moe::RopeCall a{};
+  a.rope = rope_view(plan);
+  a.x = heads_view(x), a.out = heads_view(out);
+  a.positions = positions;
+  a.type = type, a.T = T, a.n_heads = n_heads, a.D = D, a.inverse = inverse != 0;
+  clear_stale_error();
+  return hip_status(moe::launch_rope(a, (hipStream_t)stream), "rope");
+}
+
+moe_status moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_heads* k,
+                         const moe_heads* v, int32_t type, const moe_rope_plan* rope,
+                         const int32_t* positions, const moe_heads* q, int32_t n_q_heads,
+                         const moe_heads* q_out, uint32_t* err_flags, void* stream) {
+  moe_status s = check_cache(cache);
+  if (s != MOE_OK) return s;
+  if ((s = check_type("k", type, true)) != MOE_OK) return s;
+  if ((q == nullptr) != (q_out == nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "q and q_out go together: one of them is NULL");
+  if (q != nullptr && n_q_heads < 1)
+    return fail(MOE_ERR_INVALID_ARG, "n_q_heads = %d < 1", n_q_heads);
+  if ((s = check_batch(batch, cache, q ? n_q_heads : 0)) != MOE_OK) return s;
+  if (rope != nullptr && (s = check_rope(rope, cache->D)) != MOE_OK) return s;
+  if (batch->T == 0 || batch->n_seq == 0) return ok();
+  if ((s = check_batch_ptrs(batch, err_flags)) != MOE_OK) return s;
+  const int bytes = type_bytes(type);
+  if ((s = check_heads("k", k, bytes, 1)) != MOE_OK) return s;
+  if ((s = check_heads("v", v, bytes, 1)) != MOE_OK) return s;
+  if (q != nullptr) {
+    if ((s = check_heads("q", q, bytes, 1)) != MOE_OK) return s;
+    if ((s = check_heads("q_out", q_out, bytes, 1)) != MOE_OK) return s;
+    if (!same_heads(q, q_out)) return fail(MOE_ERR_INVALID_ARG, "q_out is q with other strides");
+  }
+  if ((uintptr_t)positions & 3) return fail(MOE_ERR_INVALID_ARG, "positions misaligned");
+  moe::AppendCall a{};
+  a.cache = cache_view(cache), a.batch = batch_view(batch);
+  a.rope = rope_view(rope);
+  a.k = heads_view(k), a.v = heads_view(v);
+  if (q != nullptr) a.q = heads_view(q), a.q_out = heads_view(q_out);
+  a.positions = positions;
+  a.type = type, a.n_q_heads = n_q_heads, a.err = err_flags;
+  clear_stale_error();
+  return hip_status(moe::launch_append(a, (hipStream_t)stream), "append to the cache");
+}
+
+size_t moe_attend_scratch_bytes(const moe_kv_cache* cache, const moe_kv_batch* batch,
+                                int32_t n_q_heads, int32_t window, int32_t keep_first) {
+  if (check_attend(cache, batch, n_q_heads, window, keep_first) != MOE_OK) return 0;
+  if (batch->T == 0 || batch->n_seq == 0) return 0;
+  return attend_scratch(cache, batch, n_q_heads,
+                        splits_of(cache, batch, n_q_heads, window, keep_first));
+}
+
+moe_status moe_attend(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_heads* q,
+                      int32_t type, int32_t n_q_heads, float scale, int32_t causal, int32_t window,
+                      int32_t keep_first, const float* sinks, const moe_heads* out, void* scratch,
+                      size_t scratch_bytes, uint32_t* err_flags, void* stream) {
+  moe_status s = check_attend(cache, batch, n_q_heads, window, keep_first);
+  if (s != MOE_OK) return s;
+  if ((s = check_16bit("q", type)) != MOE_OK) return s;
+  if (cache->type != MOE_T_E4M3 && cache->type != type)
+    return fail(MOE_ERR_UNSUPPORTED, "q of type %d on a cache of type %d", type, cache->type);
+  if (!std::isfinite(scale)) return fail(MOE_ERR_INVALID_ARG, "scale is not finite");
+  if (window > 0 && !causal) return fail(MOE_ERR_INVALID_ARG, "a window needs causal");
+  if (batch->T == 0 || batch->n_seq == 0) return ok();
+  if ((s = check_batch_ptrs(batch, err_flags)) != MOE_OK) return s;
+  if ((s = check_heads("q", q, 16, 8)) != MOE_OK) return s;
+  if ((s = check_heads("out", out, 16, 8)) != MOE_OK) return s;
+  if ((uintptr_t)sinks & 3) return fail(MOE_ERR_INVALID_ARG, "sinks misaligned");
+  moe::AttendCall a{};
+  a.splits = splits_of(cache, batch, n_q_heads, window, keep_first);
+  if (a.splits > 1) {
+    const size_t need = attend_scratch(cache, batch, n_q_heads, a.splits);
+    CHECK_PTR(scratch);
+    if (scratch_bytes < need)
+      return fail(MOE_ERR_INVALID_ARG, "scratch holds %zu bytes, %zu needed", scratch_bytes, need);
+    a.part = (float*)scratch;
+    a.stats = a.part + (size_t)a.splits * batch->T * n_q_heads * cache->D;
+  }
+  a.cache = cache_view(cache), a.batch = batch_view(batch);
+  a.q = heads_view(q), a.out = heads_view(out);
+  a.type = type, a.n_q_heads = n_q_heads, a.group = n_q_heads / cache->n_heads;
+  a.scale = scale, a.causal = causal != 0, a.window = window, a.keep_first = keep_first;
+  a.sinks = sinks, a.err = err_flags;
+  clear_stale_error();
+  return hip_status(moe::launch_attend(a, (hipStream_t)stream), "attention");
+}
+
+moe_status moe_linear(const void* x, int64_t x_stride, const void* w, int64_t w_stride,
+                      int32_t type, int32_t M, int32_t N, int32_t K, const void* bias,
+                      int32_t bias_type, int32_t act, const void* resid, int64_t resid_stride,
+                      void* out, int32_t out_type, int64_t out_stride, void* stream) {
+  moe_status s = check_16bit("x", type);
+  if (s != MOE_OK) return s;
+  if ((s = check_type("out", out_type, true)) != MOE_OK) return s;
+  if (bias != nullptr && (s = check_type("bias", bias_type, true)) != MOE_OK) return s;
+  if (act < MOE_ACT_NONE || act > MOE_ACT_SILU)
+    return fail(MOE_ERR_UNSUPPORTED, "unknown activation %d", act);
+  if (M < 0 || N < 0 || K < 0 || M >= (1 << 30) || N >= (1 << 30) || K >= (1 << 30) || K % 8)
+    return fail(MOE_ERR_INVALID_ARG, "M = %d, N = %d, K = %d: below 2^30, K a multiple of 8", M, N, K);
+  const int64_t limit = int64_t(1) << 40;
+  if ((int64_t)M * N >= limit) return fail(MOE_ERR_INVALID_ARG, "M * N: limit 2^40");
+  if (M == 0 || N == 0) return ok();
+  if (K > 0) {
+    CHECK_PTR(x);
+    CHECK_PTR(w);
+    if (x_stride < 0 || w_stride < 0 || x_stride % 8 || w_stride % 8 || x_stride >= limit / M ||
+        w_stride >= limit / N)
+      return fail(MOE_ERR_INVALID_ARG,
+                  "x_stride = %lld, w_stride = %lld: not negative, multiples of 8, rows * stride < 2^40",
+                  (long long)x_stride, (long long)w_stride);
+  }
+  const int bytes = type_bytes(out_type);
+  if (out == nullptr || ((uintptr_t)out & (bytes - 1)))
+    return fail(MOE_ERR_INVALID_ARG, "out is %s", out ? "misaligned" : "NULL");
+  if (((uintptr_t)resid & (bytes - 1)) || (bias && ((uintptr_t)bias & (type_bytes(bias_type) - 1))))
+    return fail(MOE_ERR_INVALID_ARG, "bias or resid misaligned");
+  if (out_stride < N || out_stride >= limit / M)
+    return fail(MOE_ERR_INVALID_ARG, "out_stride = %lld: at least N = %d, rows * stride < 2^40",
+                (long long)out_stride, N);
+  if (resid != nullptr && (resid_stride < 0 || resid_stride >= limit / M))
+    return fail(MOE_ERR_INVALID_ARG, "resid_stride = %lld: not negative, rows * stride < 2^40",
+                (long long)resid_stride);
+  if (resid == out && M > 1 && resid_stride != out_stride)
+    return fail(MOE_ERR_INVALID_ARG, "out is resid with another stride");
+  moe::LinearCall a{};
+  a.x = (const uint16_t*)x, a.w = (const uint16_t*)w;
+  a.x_stride = x_stride, a.w_stride = w_stride, a.resid_stride = resid_stride;
+  a.out_stride = out_stride;
+  a.type = type, a.M = M, a.N = N, a.K = K;
+  a.bias = bias, a.bias_type = bias_type, a.act = act;
+  a.resid = resid, a.out = out, a.out_type = out_type;
+  clear_stale_error();
+  return hip_status(moe::launch_linear(a, (hipStream_t)stream), "linear");
 }
 
 }  // extern "C"

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "common.hpp"
+#include "kv.hpp"
 
 namespace moe {
 
@@ -156,7 +157,7 @@ hipError_t launch_block_norm(const BlockNorm& a, bool exit, bool resid_f32, hipS
 
 // Microscaled formats (csrc/mxquant.hip): n values, a multiple of 32, flat.
 enum MxFmt : int { kMxFp4 = 1, kMxFp6 = 2 };
-enum DType : int { kBF16 = 1, kFP16 = 2, kFP32 = 3 };
+enum DType : int { kBF16 = 1, kFP16 = 2, kFP32 = 3, kE4M3 = 4 };
 __host__ __device__ constexpr int mx_block_bytes(int fmt) { return fmt == kMxFp4 ? 16 : 24; }
 hipError_t launch_mx_quantize(const void* src, int type, int64_t n, int fmt, uint8_t* q,
                               uint8_t* s, hipStream_t st);
@@ -179,5 +180,69 @@ struct MxProduct {
   uint32_t* err;
 };
 hipError_t launch_mx_product(const MxProduct& p, int fmt, bool gated, bool gemv, hipStream_t st);
+
+// Rotary positions and the append to a paged cache (csrc/rope.hip).
+struct RopeView {
+  const double* freq;
+  int dim;                  // 0: nothing turns
+  bool interleaved;
+  float scale;
+};
+struct RopeCall {
+  RopeView rope;
+  HeadsView x, out;
+  const int32_t* positions;
+  int type, T, n_heads, D;
+  bool inverse;
+  int block0;               // set by the launcher: first workgroup of a launch
+};
+hipError_t launch_rope(const RopeCall& a, hipStream_t stream);
+struct AppendCall {
+  KvCacheView cache;
+  KvBatchView batch;
+  RopeView rope;
+  HeadsView k, v, q, q_out;   // q.p NULL: no queries
+  const int32_t* positions;   // or NULL: places in the sequences
+  int type, n_q_heads;
+  uint32_t* err;
+  int block0;
+};
+hipError_t launch_append(const AppendCall& a, hipStream_t stream);
+
+// Attention over a paged cache (csrc/attend.hip). The keys of a sequence are shared out among
+// `splits` workgroups, whose sums meet in a second launch through `part`.
+struct AttendCall {
+  KvCacheView cache;
+  KvBatchView batch;
+  HeadsView q, out;
+  int type, n_q_heads, group;   // group: query heads a KV head
+  float scale;
+  bool causal;
+  int window, keep_first;
+  const float* sinks;
+  uint32_t* err;
+  int splits;
+  float* part;              // splits > 1: [splits][T * n_q_heads][D] sums of weighted values,
+  float* stats;             // [splits][T * n_q_heads][2] maximum (of log2 e s) and sum of weights
+  int64_t block0;           // set by the launcher: first workgroup of a launch
+};
+int attend_splits(const KvCacheView& c, const KvBatchView& b, int n_q_heads, int window,
+                  int keep_first, int max_q, int max_len);
+hipError_t launch_attend(const AttendCall& a, hipStream_t stream);
+
+// out = resid + act(x w^T + bias) (csrc/linear.hip).
+struct LinearCall {
+  const uint16_t* x;
+  const uint16_t* w;
+  int64_t x_stride, w_stride, resid_stride, out_stride;
+  int type, M, N, K;
+  const void* bias;
+  int bias_type, act;
+  const void* resid;
+  void* out;
+  int out_type;
+  int64_t tile0;            // set by the launcher: first tile of a launch
+};
+hipError_t launch_linear(const LinearCall& a, hipStream_t stream);
 
 }  // namespace moe
