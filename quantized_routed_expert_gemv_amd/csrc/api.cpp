@@ -1082,14 +1082,19 @@ moe_status check_attend(const moe_kv_cache* c, const moe_kv_batch* b, int32_t n_
     return fail(MOE_ERR_INVALID_ARG, "window = %d, keep_first = %d", window, keep_first);
   return MOE_OK;
 }
-int splits_of(const moe_kv_cache* c, const moe_kv_batch* b, int32_t n_q_heads, int32_t window,
-              int32_t keep_first) {
-  return moe::attend_splits(cache_view(c), batch_view(b), n_q_heads, window, keep_first, b->max_q,
-                            b->max_len);
+moe::AttendPlan plan_of(const moe_kv_cache* c, const moe_kv_batch* b, int32_t n_q_heads,
+                        int32_t window, int32_t keep_first) {
+  return moe::attend_plan(cache_view(c), batch_view(b), n_q_heads, window, keep_first, b->max_q,
+                          b->max_len);
 }
-size_t attend_scratch(const moe_kv_cache* c, const moe_kv_batch* b, int32_t n_q_heads, int splits) {
-  if (splits <= 1) return 0;
-  return (size_t)splits * b->T * n_q_heads * (c->D + 2) * sizeof(float);
+// Splits whose sums meet in scratch memory.
+int parts_of(const moe::AttendPlan& p) {
+  const int few = p.few || p.both ? p.splits_few : 1, many = p.few ? 1 : p.splits;
+  return few > many ? few : many;
+}
+size_t attend_scratch(const moe_kv_cache* c, const moe_kv_batch* b, int32_t n_q_heads, int parts) {
+  if (parts <= 1) return 0;
+  return (size_t)parts * b->T * n_q_heads * (c->D + 2) * sizeof(float);
 }
 
 moe_status check_16bit(const char* name, int32_t type) {
@@ -1165,7 +1170,7 @@ size_t moe_attend_scratch_bytes(const moe_kv_cache* cache, const moe_kv_batch* b
   if (check_attend(cache, batch, n_q_heads, window, keep_first) != MOE_OK) return 0;
   if (batch->T == 0 || batch->n_seq == 0) return 0;
   return attend_scratch(cache, batch, n_q_heads,
-                        splits_of(cache, batch, n_q_heads, window, keep_first));
+                        parts_of(plan_of(cache, batch, n_q_heads, window, keep_first)));
 }
 
 moe_status moe_attend(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_heads* q,
@@ -1185,14 +1190,16 @@ moe_status moe_attend(const moe_kv_cache* cache, const moe_kv_batch* batch, cons
   if ((s = check_heads("out", out, 16, 8)) != MOE_OK) return s;
   if ((uintptr_t)sinks & 3) return fail(MOE_ERR_INVALID_ARG, "sinks misaligned");
   moe::AttendCall a{};
-  a.splits = splits_of(cache, batch, n_q_heads, window, keep_first);
-  if (a.splits > 1) {
-    const size_t need = attend_scratch(cache, batch, n_q_heads, a.splits);
+  const moe::AttendPlan plan = plan_of(cache, batch, n_q_heads, window, keep_first);
+  const int parts = parts_of(plan);
+  a.splits = plan.splits, a.splits_few = plan.splits_few, a.few = plan.few, a.both = plan.both;
+  if (parts > 1) {
+    const size_t need = attend_scratch(cache, batch, n_q_heads, parts);
     CHECK_PTR(scratch);
     if (scratch_bytes < need)
       return fail(MOE_ERR_INVALID_ARG, "scratch holds %zu bytes, %zu needed", scratch_bytes, need);
     a.part = (float*)scratch;
-    a.stats = a.part + (size_t)a.splits * batch->T * n_q_heads * cache->D;
+    a.stats = a.part + (size_t)parts * batch->T * n_q_heads * cache->D;
   }
   a.cache = cache_view(cache), a.batch = batch_view(batch);
   a.q = heads_view(q), a.out = heads_view(out);

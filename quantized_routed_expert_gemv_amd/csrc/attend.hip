@@ -1,8 +1,8 @@
 // Attention of new tokens over a paged cache: with s_j = scale <q, k_j> over the keys in sight,
 //   out = sum_j e^{s_j} v_j / (sum_j e^{s_j} + e^{sink})
-// in one pass over the keys with a running maximum m and sum l: weights are 2^{s'_j - m} with
-// s' = s log2 e, and m is raised only where a score passes it by 8, so weights stay below 2^8
-// (exact scaling by a power of two changes no rounding) and the sums seldom have to be rescaled.
+// in one pass over the keys with a running reference m and sum l: weights are 2^{s'_j - m} with
+// s' = s log2 e. m is a whole number, so that rescaling is exact, and is raised only where a score
+// passes it by 8: weights stay below 2^8 and the sums seldom have to be rescaled.
 // m, l and the weighted sum are fp32; a weight is rounded to the queries' 16-bit type where it
 // meets the values in a matrix instruction, which adds half a step of that type to each term.
 //
@@ -22,6 +22,9 @@ namespace {
 typedef _Float16 f16x8 __attribute__((__vector_size__(8 * sizeof(_Float16))));
 typedef _Float16 f16x2 __attribute__((__vector_size__(2 * sizeof(_Float16))));
 
+typedef float f32x16 __attribute__((__vector_size__(16 * sizeof(float))));
+typedef short i16x4 __attribute__((__vector_size__(4 * sizeof(short))));
+
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kRaise = 8.f;   // by how much a score passes the running maximum before it moves
 
@@ -32,6 +35,16 @@ __device__ __forceinline__ f32x4 mma16(u32x4 a, u32x4 b, f32x4 c) {
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
   else
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+template <bool F16>
+__device__ __forceinline__ f32x16 mma32(u32x4 a, u32x4 b, f32x16 c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
@@ -52,13 +65,6 @@ __device__ __forceinline__ uint32_t widen2(uint32_t v) {
   else
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.f, HI));
 }
-// Whether either half of a dword of 16-bit values is an infinity or NaN.
-template <bool F16>
-__device__ __forceinline__ bool not_finite(uint32_t v) {
-  constexpr uint32_t e = F16 ? 0x7C00u : 0x7F80u;
-  return (v & e) == e || (v >> 16 & e) == e;
-}
-
 // 2N bytes of a 16-bit cache, or N of an 8-bit one, as N values of the 16-bit type.
 template <int N, bool F16, bool FP8>
 __device__ __forceinline__ void load_row(const uint8_t* plane, int64_t at, uint32_t* w) {
@@ -105,9 +111,13 @@ __device__ __forceinline__ int window_start(const AttendCall& a, int pos) {
   return a.window ? (int)max((int64_t)pos - a.window + 1, (int64_t)0) : 0;
 }
 
+// Sequences of up to this many rows (new tokens * group) go to the kernel for few rows.
+constexpr int kFewRows = 32;
+
 // The x-th tile of R rows: sequence b's begin at floor(q_start[b] * group / R) + b, which leaves
-// each sequence as many places as it can need.
-template <int R>
+// each sequence as many places as it can need. FEW: of the sequences with few rows; else of the
+// others, or of all where no second launch takes them.
+template <int R, bool FEW>
 __device__ __forceinline__ bool find_tile(const AttendCall& a, int64_t x, int head, Tile* t) {
   const KvBatchView& b = a.batch;
   const int seq = wave_find(b.n_seq, x, [&](int i) {
@@ -117,6 +127,7 @@ __device__ __forceinline__ bool find_tile(const AttendCall& a, int64_t x, int he
   const int64_t row0 = (x - (int64_t)lo * a.group / R - seq) * R;
   const int64_t rows = (int64_t)n * a.group - row0;
   if (n <= 0 || row0 < 0 || rows <= 0) return false;
+  if (a.both && ((int64_t)n * a.group <= kFewRows) != FEW) return false;
   const int64_t cap = (int64_t)b.max_pages * a.cache.page_size;
   const int len = max(b.seq_len[seq], 0);
   t->seq = seq;
@@ -178,12 +189,12 @@ __device__ __forceinline__ KeyRow key_row(const AttendCall& a, const Tile& t, in
 
 // Where a tile's sums go: out, or a split's part.
 template <bool F16, int N>
-__device__ __forceinline__ void store_row(const AttendCall& a, const Tile& t, int split, int r,
-                                          int d, float m, float l, const float* o) {
+__device__ __forceinline__ void store_row(const AttendCall& a, const Tile& t, int splits, int split,
+                                          int r, int d, float m, float l, const float* o) {
   const int tok = (t.row0 + r) / a.group, g = t.row0 + r - tok * a.group;
   const int64_t token = t.token0 + tok;
   const int head = t.head * a.group + g;
-  if (a.splits > 1) {
+  if (splits > 1) {
     const int64_t at = ((int64_t)split * a.batch.T + token) * a.n_q_heads + head;
     if (d == 0) {
       a.stats[2 * at] = m;
@@ -208,6 +219,59 @@ __device__ __forceinline__ void store_row(const AttendCall& a, const Tile& t, in
                              pack2<F16>(w == 0.f ? 0.f : o[i + 2] * w, w == 0.f ? 0.f : o[i + 3] * w)};
 }
 
+// Whether every row of the tile sees every key of key0 .. key0 + B - 1 (that is on a page).
+template <int B>
+__device__ __forceinline__ bool whole_block(const AttendCall& a, const Tile& t, int key0) {
+  return key0 + B - 1 <= t.last_of_first &&
+         (key0 >= t.first_of_last || (a.window && key0 + B - 1 < a.keep_first));
+}
+
+// A matrix instruction would multiply a weight of 0, of a row that does not see a key, by that key's
+// values. Where not every row sees a block, values that are infinite or NaN go into the product as 0,
+// and a workgroup that met one comes here when its rows are stored: each row takes the odd values of
+// the keys that it sees, times a weight that is not 0, which is adding them.
+template <bool F16, int B>
+__device__ void add_odd_values(const AttendCall& a, const Tile& t, const Blocks<B>& blocks, int b0,
+                               int b1, int splits, int split) {
+  __threadfence_block();
+  __syncthreads();   // the rows are stored
+  const int d = threadIdx.x;
+  if (d >= a.cache.D) return;
+  const float vs = a.cache.type == kE4M3 && a.cache.v_scale ? a.cache.v_scale[t.head] : 1.f;
+  for (int b = b0; b < b1; ++b) {
+    const int key0 = blocks.key(b);
+    if (whole_block<B>(a, t, key0)) continue;
+    for (int key = key0; key < key0 + B; ++key) {
+      const KeyRow kv = key_row<1>(a, t, key);
+      if (!kv.ok) continue;
+      const float v = plane_value(a.cache.v, kv.v + d, a.cache.type) * vs;
+      if (fabsf(v) < INFINITY) continue;
+      for (int r = 0; r < t.rows; ++r) {
+        const int tok = (t.row0 + r) / a.group, pos = t.pos0 + tok;
+        if (a.causal && key > pos) continue;
+        if (key < window_start(a, pos) && key >= a.keep_first) continue;
+        const int64_t token = t.token0 + tok;
+        const int head = t.head * a.group + t.row0 + r - tok * a.group;
+        if (splits > 1) {
+          a.part[(((int64_t)split * a.batch.T + token) * a.n_q_heads + head) * a.cache.D + d] += v;
+        } else {
+          uint16_t* p = (uint16_t*)a.out.p + token * a.out.token + head * a.out.head + d;
+          *p = (uint16_t)pack2<F16>(value<F16>(*p) + v, 0.f);
+        }
+      }
+    }
+  }
+}
+
+// Takes infinities and NaN out of a pair of 16-bit values; whether there were any.
+template <bool F16>
+__device__ __forceinline__ bool take_odd(uint32_t& v) {
+  constexpr uint32_t e = F16 ? 0x7C00u : 0x7F80u;
+  const bool lo = (v & e) == e, hi = (v >> 16 & e) == e;
+  v = (lo ? 0u : v & 0xFFFFu) | (hi ? 0u : v & 0xFFFF0000u);
+  return lo || hi;
+}
+
 constexpr int kRowTile = 16;
 constexpr int kRowThreads = 256;
 
@@ -225,18 +289,20 @@ __global__ __launch_bounds__(kRowThreads) void k_attend_rows(AttendCall a) {
   constexpr int OS = DV + 4;
   __shared__ float so[NW][kRowTile][OS];
   __shared__ float sm[NW][kRowTile], sl[NW][kRowTile];
-  __shared__ float sp[NW][kRowTile][33];
+  __shared__ int s_odd;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int n = lane & 15, g = lane >> 4;
   const int64_t id = a.block0 + blockIdx.x;
-  const int split = (int)(id % a.splits);
-  const int64_t th = id / a.splits;
+  const int split = (int)(id % a.splits_few);
+  const int64_t th = id / a.splits_few;
   Tile t;
-  if (!find_tile<kRowTile>(a, th / a.cache.n_heads, (int)(th % a.cache.n_heads), &t)) return;
+  if (!find_tile<kRowTile, true>(a, th / a.cache.n_heads, (int)(th % a.cache.n_heads), &t)) return;
   const Blocks<32> blocks(t);
-  const int b0 = (int)((int64_t)blocks.count * split / a.splits);
-  const int b1 = (int)((int64_t)blocks.count * (split + 1) / a.splits);
+  const int b0 = (int)((int64_t)blocks.count * split / a.splits_few);
+  const int b1 = (int)((int64_t)blocks.count * (split + 1) / a.splits_few);
   const int D = a.cache.D;
+  if (threadIdx.x == 0) s_odd = 0;
+  __syncthreads();
 
   // this lane's query: the keys that it sees, and its row of q as an operand
   const int tok = (t.row0 + n) / a.group;
@@ -314,31 +380,40 @@ __global__ __launch_bounds__(kRowThreads) void k_attend_rows(AttendCall a) {
       for (int k = 0; k < NK; ++k) s[u] = mma16<F16>(kf[u][k], q[k], s[u]);
     }
     // lane (n, g): s[u][i] is the score of query n and key key0 + 8 g + 4 u + i
-    const bool whole = key0 + 31 <= t.last_of_first &&
-                       (key0 >= t.first_of_last || key0 + 31 < keep) && __all(v_ok == 0xFFu);
-    if (!whole) {
+    float x[8];   // scores, then weights
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = s[j / 4][j % 4];
+    const bool seen = whole_block<32>(a, t, key0);
+    if (!seen || !__all(v_ok == 0xFFu)) {
+      bool odd = false;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int key = key0 + 8 * g + j;
-        const bool in = key <= see_last && (key >= see_first || key < keep) && (v_ok >> j & 1);
-        if (!in) s[j / 4][j % 4] = -INFINITY;
+        const bool ok = v_ok >> j & 1;
+        // selects of scalars, no branches (see k_attend_tiles)
+        const bool out = (key > see_last) | ((key < see_first) & (key >= keep)) | !ok;
+        x[j] = out ? -INFINITY : x[j];
         // values behind the end, before the window, or on no page: anything may stand there
-        if (!(key < t.end && (key >= t.first || key < t.kept) && (v_ok >> j & 1)))
+        const bool some = ok & (key < t.end) & ((key >= t.first) | (key < t.kept));
 #pragma unroll
-          for (int h = 0; h < NH; ++h)
+        for (int h = 0; h < NH; ++h)
 #pragma unroll
-            for (int i = 0; i < E / 2; ++i) vf[j][h][i] = 0;
+          for (int i = 0; i < E / 2; ++i) {
+            vf[j][h][i] = some ? vf[j][h][i] : 0;
+            if (!seen) odd |= take_odd<F16>(vf[j][h][i]);
+          }
       }
+      if (odd) s_odd = 1;
     }
-    float top = s[0][0];
+    float top = x[0];
 #pragma unroll
-    for (int j = 1; j < 8; ++j) top = fmaxf(top, s[j / 4][j % 4]);
+    for (int j = 1; j < 8; ++j) top = fmaxf(top, x[j]);
     top *= c;
     if (__any(top > m + kRaise)) {
       top = fmaxf(top, wave_xor(top, 16));
       top = fmaxf(top, wave_xor(top, 32));
-      const float to = fmaxf(m, top);
-      const float f = m == -INFINITY ? 0.f : exp2f(m - to);
+      const float to = top > m + kRaise ? ceilf(top) : m;   // by a row's own scores alone
+      const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - to);
       m = to;
       l *= f;
 #pragma unroll
@@ -347,59 +422,24 @@ __global__ __launch_bounds__(kRowThreads) void k_attend_rows(AttendCall a) {
         for (int i = 0; i < E; ++i) o[h][i] *= f;
     }
     const float base = m == -INFINITY ? 0.f : m;
-    float p[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      p[j] = exp2f(fmaf(s[j / 4][j % 4], c, -base));
-      l += p[j];
+      x[j] = __builtin_amdgcn_exp2f(fmaf(x[j], c, -base));
+      l += x[j];
     }
-    const u32x4 pf = {pack2<F16>(p[0], p[1]), pack2<F16>(p[2], p[3]), pack2<F16>(p[4], p[5]),
-                      pack2<F16>(p[6], p[7])};
-    bool odd = false;
-    if (!whole) {   // a value that some rows see and others do not must not be 0 * infinity there
-      bool bad = false;
+    const u32x4 pf = {pack2<F16>(x[0], x[1]), pack2<F16>(x[2], x[3]), pack2<F16>(x[4], x[5]),
+                      pack2<F16>(x[6], x[7])};
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+    for (int h = 0; h < NH; ++h)
 #pragma unroll
-        for (int h = 0; h < NH; ++h)
+      for (int i = 0; i < E; ++i) {
+        u32x4 vt;
+        const uint32_t sel = i & 1 ? 0x07060302u : 0x05040100u;
 #pragma unroll
-          for (int i = 0; i < E / 2; ++i) bad |= not_finite<F16>(vf[j][h][i]);
-      odd = __any(bad);
-    }
-    if (!odd) {
-#pragma unroll
-      for (int h = 0; h < NH; ++h)
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          u32x4 vt;
-          const uint32_t sel = i & 1 ? 0x07060302u : 0x05040100u;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            vt[j] = __builtin_amdgcn_perm(vf[2 * j + 1][h][i / 2], vf[2 * j][h][i / 2], sel);
-          o[h][i] = mma16<F16>(vt, pf, o[h][i]);
-        }
-    } else {   // key by key, each row with the keys that it sees
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float r = value<F16>(pf[j / 2] >> 16 * (j & 1));
-        sp[wave][n][8 * g + j] = s[j / 4][j % 4] == -INFINITY ? -1.f : r;
+        for (int j = 0; j < 4; ++j)
+          vt[j] = __builtin_amdgcn_perm(vf[2 * j + 1][h][i / 2], vf[2 * j][h][i / 2], sel);
+        o[h][i] = mma16<F16>(vt, pf, o[h][i]);
       }
-      __builtin_amdgcn_wave_barrier();
-      for (int k = 0; k < 32; ++k) {
-        const KeyRow r = key_row<1>(a, t, key0 + k);
-        const float w = sp[wave][n][k];
-#pragma unroll
-        for (int h = 0; h < NH; ++h)
-#pragma unroll
-          for (int i = 0; i < E; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int d = 16 * E * h + E * (4 * g + e) + i;
-              const float v = plane_value(a.cache.v, r.v + (d < D ? d : 0), a.cache.type);
-              if (!(w < 0.f) && r.ok) o[h][i][e] = fmaf(w, v, o[h][i][e]);
-            }
-      }
-    }
   }
 
   l += wave_xor(l, 16);
@@ -416,7 +456,6 @@ __global__ __launch_bounds__(kRowThreads) void k_attend_rows(AttendCall a) {
       for (int e = 0; e < 4; ++e) so[wave][n][16 * E * h + E * (4 * g + e) + i] = o[h][i][e];
   __syncthreads();
   const int r = threadIdx.x / 16, col = threadIdx.x % 16;
-  if (r >= t.rows) return;
   float top = sm[0][r];
 #pragma unroll
   for (int w = 1; w < NW; ++w) top = fmaxf(top, sm[w][r]);
@@ -431,7 +470,7 @@ __global__ __launch_bounds__(kRowThreads) void k_attend_rows(AttendCall a) {
 #pragma unroll
   for (int h = 0; h < NH; ++h) {
     const int d = 16 * E * h + E * col;
-    if (d >= D) continue;
+    if (d >= D || r >= t.rows) continue;
     float v[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -440,8 +479,302 @@ __global__ __launch_bounds__(kRowThreads) void k_attend_rows(AttendCall a) {
       for (int w = 0; w < NW; ++w) v[i] = fmaf(f[w], so[w][r][d + i], v[i]);
       v[i] *= vs;
     }
-    store_row<F16, E>(a, t, split, r, d, sum != sum ? fmaxf(top, 0.f) : top, sum, v);
+    store_row<F16, E>(a, t, a.splits_few, split, r, d, sum != sum ? fmaxf(top, 0.f) : top, sum, v);
   }
+  if (s_odd) add_odd_values<F16>(a, t, blocks, b0, b1, a.splits_few, split);
+}
+
+constexpr int kTileThreads = 256;
+constexpr int kTileRows = 128;   // 32 a wave
+constexpr int kTileKeys = 64;
+
+// Row strides, in 16-bit values, of a tile's keys and values in LDS: keys are read 16 bytes a lane
+// over 32 rows (rows 4 banks apart: no conflict), values through the transposing read, 4 rows of 32
+// bytes for 16 lanes (rows 16 banks apart: none either).
+template <int DV> constexpr int kKeyStride = DV + 8;
+template <int DV> constexpr int kValueStride = DV + 32;
+
+template <int DV> struct alignas(16) TileBuffer {
+  uint16_t k[kTileKeys][kKeyStride<DV>];
+  uint16_t v[kTileKeys][kValueStride<DV>];
+};
+
+// The transposing LDS read: of 16 lanes, lane i reads 8 bytes (its address) of row i / 4, columns
+// 4 (i % 4) on, and is left with column i of the four rows.
+__device__ __forceinline__ u32x2 read_columns(const uint16_t* p) {
+  typedef __attribute__((address_space(3))) i16x4* lds_p;
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)p));
+}
+
+// Many rows a sequence: the matrix instructions bound it. Four waves of 32 rows (columns of
+// 32x32x16 instructions) share tiles of 64 keys and values, which go through registers into two LDS
+// buffers, the next tile's loads in flight behind the products of this one. Values reach the second
+// product through the transposing LDS read, in the order of keys in which the first left the
+// weights: 16 s + {4 h .. + 3, 8 + 4 h .. + 3} for k-step s and lane half h.
+// U16: pages hold a multiple of 16 tokens, so the 16 rows of a tile that a wave loads are on one.
+template <bool F16, bool FP8, int DV, bool U16>
+__global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles(AttendCall a) {
+  constexpr int NK = DV / 16, ND = DV / 32;
+  constexpr int CH = DV * (FP8 ? 1 : 2) / 16;          // 16-byte chunks of a row
+  constexpr int RP = kWave / CH, NP = 16 / RP;         // rows a wave loads at once; passes
+  constexpr int CV = FP8 ? 16 : 8;                     // values of a chunk
+  __shared__ TileBuffer<DV> buf[2];
+  __shared__ uint64_t s_ok[2];                         // rows of the tile that are on a page
+  __shared__ int s_odd;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int n = lane & 31, hf = lane >> 5;
+  const int64_t id = a.block0 + blockIdx.x;
+  const int head = (int)(id % a.cache.n_heads);
+  const int64_t th = id / a.cache.n_heads;
+  const int split = (int)(th % a.splits);
+  Tile t;
+  // later tiles, which see more keys, first
+  if (!find_tile<kTileRows, false>(a, a.tiles - 1 - th / a.splits, head, &t)) return;
+  const Blocks<kTileKeys> blocks(t);
+  const int b0 = (int)((int64_t)blocks.count * split / a.splits);
+  const int b1 = (int)((int64_t)blocks.count * (split + 1) / a.splits);
+  const int D = a.cache.D;
+  if (threadIdx.x == 0) s_odd = 0;
+  __syncthreads();
+
+  const int r = 32 * wave + n;
+  const int tok = (t.row0 + r) / a.group;
+  const bool row_ok = r < t.rows;
+  const int pos = t.pos0 + tok;
+  const int see_last = !row_ok ? -1 : a.causal ? min(pos, t.end - 1) : t.end - 1;
+  const int see_first = window_start(a, pos);
+  const int keep = a.window ? a.keep_first : 0;
+  // of the wave's rows: what all of them and any of them sees last, and sees first
+  const int w_rows = min(max(t.rows - 32 * wave, 0), 32);
+  const int w_first = t.pos0 + (t.row0 + 32 * wave) / a.group;
+  const int w_last = t.pos0 + (t.row0 + 32 * wave + max(w_rows, 1) - 1) / a.group;
+  const int w_all = a.causal ? min(w_first, t.end - 1) : t.end - 1;
+  const int w_any = w_rows == 0 ? -1 : a.causal ? min(w_last, t.end - 1) : t.end - 1;
+  const int w_begin = window_start(a, w_first), w_from = window_start(a, w_last);
+  float c = a.scale * kLog2e;
+  if (FP8 && a.cache.k_scale) c *= a.cache.k_scale[t.head];
+  const uint32_t flip = c < 0.f ? 0x80008000u : 0u;
+  c = fabsf(c) < 1e-37f ? 1e-37f : fabsf(c);
+  u32x4 q[NK];
+  {
+    const uint16_t* p = (const uint16_t*)a.q.p + (int64_t)(t.token0 + tok) * a.q.token +
+                        (int64_t)(t.head * a.group + t.row0 + r - tok * a.group) * a.q.head;
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+      const int d = 16 * k + 8 * hf;
+      q[k] = u32x4{0, 0, 0, 0};
+      if (row_ok && d < D) q[k] = *(const u32x4*)(p + d) ^ flip;
+    }
+  }
+  f32x16 o[ND];
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+  float m = -INFINITY, l = 0.f;
+
+  // loads: this lane's chunk of a row, and its row of each pass
+  const int chunk = lane % CH, rsub = lane / CH;
+  const bool chunk_ok = chunk * CV < D;
+  u32x4 kr[NP], vr[NP];
+  uint32_t ok16 = 0;       // rows of this wave's 16 whose keys are in sight and on a page
+  int page = 0;            // U16: table entry of the next tile's rows
+  auto in_sight = [&](int p) { return p < t.end && (p >= t.first || p < t.kept); };
+  auto lookup = [&](int b) {   // entries are asked for a tile ahead of their use
+    if constexpr (U16) {
+      const int p = blocks.key(b) + 16 * wave;
+      if (b < b1 && p < t.end && (p + 16 > t.first || p < t.kept)) {
+        int row;
+        page = a.batch.table[t.seq * a.batch.table_stride +
+                             page_of((uint32_t)p, a.cache.page_size, a.cache.page_inv, &row)];
+      }
+    }
+  };
+  auto load_tile = [&](int b) {
+    const int p0 = blocks.key(b) + 16 * wave;
+    ok16 = 0;
+    if constexpr (U16) {
+      int row;
+      page_of((uint32_t)p0, a.cache.page_size, a.cache.page_inv, &row);
+      const bool seen = p0 < t.end && (p0 + 16 > t.first || p0 < t.kept);
+      const bool good = seen && (unsigned)page < (unsigned)a.cache.n_pages;
+      if (seen && !good && a.err && lane == 0) atomicOr(a.err, 1u);
+      const int64_t pg = __builtin_amdgcn_readfirstlane(good ? page : 0);
+      row = __builtin_amdgcn_readfirstlane(good ? row : 0);
+      const bool one = !good;   // no such page: row 0 of page 0, over and over
+      const int64_t kb = pg * a.cache.k_page + row * a.cache.k_token + t.head * a.cache.k_head;
+      const int64_t vb = pg * a.cache.v_page + row * a.cache.v_token + t.head * a.cache.v_head;
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const int rr = one ? 0 : j * RP + rsub;
+        const int64_t d = chunk_ok ? chunk * CV : 0;
+        kr[j] = *(const u32x4*)(a.cache.k + (kb + rr * a.cache.k_token + d) * (FP8 ? 1 : 2));
+        vr[j] = *(const u32x4*)(a.cache.v + (vb + rr * a.cache.v_token + d) * (FP8 ? 1 : 2));
+      }
+      if (good) {
+        const uint32_t below = t.end - p0 >= 16 ? 0xFFFFu : (1u << (t.end - p0)) - 1;
+        const uint32_t from = p0 >= t.first ? 0xFFFFu : (0xFFFFu << min(t.first - p0, 16)) & 0xFFFFu;
+        const uint32_t kept = p0 >= t.kept ? 0u
+                              : t.kept - p0 >= 16 ? 0xFFFFu : (1u << (t.kept - p0)) - 1;
+        ok16 = below & (from | kept);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const KeyRow kv = key_row<1>(a, t, p0 + j * RP + rsub);
+        const int64_t d = chunk_ok ? chunk * CV : 0;
+        kr[j] = *(const u32x4*)(a.cache.k + (kv.k + d) * (FP8 ? 1 : 2));
+        vr[j] = *(const u32x4*)(a.cache.v + (kv.v + d) * (FP8 ? 1 : 2));
+        const uint64_t rows = __ballot(kv.ok);
+#pragma unroll
+        for (int i = 0; i < RP; ++i) ok16 |= (uint32_t)(rows >> (i * CH) & 1) << (j * RP + i);
+      }
+    }
+    ok16 = __builtin_amdgcn_readfirstlane(ok16);
+  };
+  auto store_tile = [&](int b, int to) {
+    const bool seen = whole_block<kTileKeys>(a, t, blocks.key(b));
+    bool odd = false;
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int row = j * RP + rsub;
+      uint32_t k[2 * 4], v[2 * 4];
+      if constexpr (FP8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          k[2 * i] = widen2<F16, false>(kr[j][i]), k[2 * i + 1] = widen2<F16, true>(kr[j][i]);
+          v[2 * i] = widen2<F16, false>(vr[j][i]), v[2 * i + 1] = widen2<F16, true>(vr[j][i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k[i] = kr[j][i], v[i] = vr[j][i];
+      }
+      constexpr int NW = CV / 2;
+      if (DV != D && !chunk_ok) {
+#pragma unroll
+        for (int i = 0; i < NW; ++i) k[i] = v[i] = 0;
+      }
+      if (!seen || ok16 != 0xFFFFu) {
+        const bool some = ok16 >> row & 1;   // out of sight: zeros
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+          v[i] = some ? v[i] : 0;
+          if (!seen) odd |= take_odd<F16>(v[i]);
+        }
+      }
+      uint16_t* kp = &buf[to].k[16 * wave + row][chunk * CV];
+      uint16_t* vp = &buf[to].v[16 * wave + row][chunk * CV];
+#pragma unroll
+      for (int i = 0; i < NW; i += 4) {
+        *(u32x4*)(kp + 2 * i) = u32x4{k[i], k[i + 1], k[i + 2], k[i + 3]};
+        *(u32x4*)(vp + 2 * i) = u32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+      }
+    }
+    if (odd) s_odd = 1;
+    if (lane == 0) ((uint16_t*)&s_ok[to])[wave] = (uint16_t)ok16;
+  };
+
+  if (b0 < b1) {
+    lookup(b0);
+    load_tile(b0);
+    lookup(b0 + 1);
+    store_tile(b0, 0);
+  }
+  __syncthreads();
+  for (int b = b0; b < b1; ++b) {
+    const int at = (b - b0) & 1;
+    if (b + 1 < b1) {
+      load_tile(b + 1);
+      lookup(b + 2);
+    }
+    const int key0 = blocks.key(b);
+    const uint64_t ok = s_ok[at];
+    if (key0 <= w_any && (key0 + kTileKeys > w_begin || key0 < keep)) {
+      f32x16 s[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[u][i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+          s[u] = mma32<F16>(*(const u32x4*)&buf[at].k[32 * u + n][16 * k + 8 * hf], q[k], s[u]);
+      }
+      // s[u][i]: the score of query n and key key0 + 32 u + 8 (i / 4) + 4 hf + i % 4
+      const int key_l = key0 + 4 * hf;
+      const int to_last = see_last - key_l, to_first = see_first - key_l, to_keep = keep - key_l;
+      float x[32];   // scores, then weights
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = s[i / 16][i % 16];
+      // Selects of scalars, no branches: with a branch a mask, or a store into an element of s, was
+      // compiled to code that left the first element as it was.
+      if (!(key0 + kTileKeys - 1 <= w_all && (key0 >= w_from || key0 + kTileKeys - 1 < keep))) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const int k = 32 * (i / 16) + 8 * (i % 16 / 4) + i % 4;   // of key key_l + k
+          const bool out = (k > to_last) | ((k < to_first) & (k >= to_keep));
+          x[i] = out ? -INFINITY : x[i];
+        }
+      }
+      if (ok != ~0ull) {
+        const uint64_t ok_l = ok >> 4 * hf;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const int k = 32 * (i / 16) + 8 * (i % 16 / 4) + i % 4;
+          x[i] = ok_l >> k & 1 ? x[i] : -INFINITY;
+        }
+      }
+      float top = x[0];
+#pragma unroll
+      for (int i = 1; i < 32; ++i) top = fmaxf(top, x[i]);
+      top *= c;
+      if (__any(top > m + kRaise)) {
+        top = fmaxf(top, wave_xor(top, 32));
+        const float to = top > m + kRaise ? ceilf(top) : m;   // by a row's own scores alone
+        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - to);
+        m = to;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[d][i] *= f;
+      }
+      const float base = m == -INFINITY ? 0.f : m;
+      u32x4 p[4];
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], c, -base));
+        x[i + 1] = __builtin_amdgcn_exp2f(fmaf(x[i + 1], c, -base));
+        l += x[i] + x[i + 1];
+        p[i / 8][i % 8 / 2] = pack2<F16>(x[i], x[i + 1]);
+      }
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint16_t* v = &buf[at].v[16 * k + 4 * hf + (lane & 15) / 4]
+                                        [32 * d + 16 * (n / 16) + 4 * (lane & 3)];
+          const u32x2 lo = read_columns(v), hi = read_columns(v + 8 * kValueStride<DV>);
+          o[d] = mma32<F16>(u32x4{lo[0], lo[1], hi[0], hi[1]}, p[k], o[d]);
+        }
+    }
+    if (b + 1 < b1) store_tile(b + 1, at ^ 1);
+    __syncthreads();
+  }
+
+  l += wave_xor(l, 32);
+  const float vs = FP8 && a.cache.v_scale ? a.cache.v_scale[t.head] : 1.f;
+  const float top = l != l ? fmaxf(m, 0.f) : m;   // scores of NaN alone leave m where it was
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int at_d = 32 * d + 8 * (i / 4) + 4 * hf;
+      if (at_d >= D || !row_ok) continue;
+      const float v[4] = {o[d][i] * vs, o[d][i + 1] * vs, o[d][i + 2] * vs, o[d][i + 3] * vs};
+      store_row<F16, 4>(a, t, a.splits, split, r, at_d, top, l, v);
+    }
+  if (s_odd) add_odd_values<F16>(a, t, blocks, b0, b1, a.splits, split);
 }
 
 // The splits of a row meet: one wave a row, in the splits' order.
@@ -451,16 +784,23 @@ __global__ __launch_bounds__(kRowThreads) void k_attend_join(AttendCall a) {
   const int64_t row = (a.block0 + blockIdx.x) * (kRowThreads / kWave) + threadIdx.x / kWave;
   const int64_t token = row / a.n_q_heads;
   if (token < first_row(a.batch, 0) || token >= first_row(a.batch, a.batch.n_seq)) return;
+  int splits = a.few ? a.splits_few : a.splits;
+  if (a.both) {
+    const int seq = wave_find(a.batch.n_seq, token, [&](int i) { return first_row(a.batch, i); });
+    const int64_t n = first_row(a.batch, seq + 1) - first_row(a.batch, seq);
+    splits = n * a.group <= kFewRows ? a.splits_few : a.splits;
+    if (splits == 1) return;   // written already
+  }
   const int head = (int)(row - token * a.n_q_heads);
   const int64_t all = (int64_t)a.batch.T * a.n_q_heads;
   float top = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.stats[2 * (s * all + row)]);
+  for (int s = 0; s < splits; ++s) top = fmaxf(top, a.stats[2 * (s * all + row)]);
   const float sink = a.sinks ? a.sinks[head] * kLog2e : -INFINITY;
   const float high = fmaxf(top, sink);
   float l = a.sinks ? exp2f(sink - high) : 0.f;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
   const int d = 4 * lane;
-  for (int s = 0; s < a.splits; ++s) {
+  for (int s = 0; s < splits; ++s) {
     const float m = a.stats[2 * (s * all + row)];
     if (m == -INFINITY) continue;   // nothing in sight there
     const float f = exp2f(m - high);
@@ -494,43 +834,62 @@ hipError_t launch_blocks(AttendCall a, int64_t blocks, K kernel, int threads, hi
 }
 
 template <bool F16, bool FP8, int DV>
-hipError_t launch_rows(const AttendCall& a, hipStream_t stream) {
-  const int64_t tiles = (int64_t)a.batch.T * a.group / kRowTile + a.batch.n_seq;
-  const int64_t blocks = tiles * a.cache.n_heads * a.splits;
-  if (a.cache.page_size % 8 == 0)
-    return launch_blocks(a, blocks, k_attend_rows<F16, FP8, DV, true>, kRowThreads, stream);
-  return launch_blocks(a, blocks, k_attend_rows<F16, FP8, DV, false>, kRowThreads, stream);
+hipError_t launch_depth(AttendCall a, hipStream_t stream) {
+  hipError_t e = hipSuccess;
+  const bool tiles = a.both || !a.few, rows = a.both || a.few;
+  if (tiles) {
+    a.tiles = (int64_t)a.batch.T * a.group / kTileRows + a.batch.n_seq;
+    const int64_t blocks = a.tiles * a.cache.n_heads * a.splits;
+    e = a.cache.page_size % 16 == 0
+            ? launch_blocks(a, blocks, k_attend_tiles<F16, FP8, DV, true>, kTileThreads, stream)
+            : launch_blocks(a, blocks, k_attend_tiles<F16, FP8, DV, false>, kTileThreads, stream);
+  }
+  if (rows && e == hipSuccess) {
+    a.tiles = (int64_t)a.batch.T * a.group / kRowTile + a.batch.n_seq;
+    const int64_t blocks = a.tiles * a.cache.n_heads * a.splits_few;
+    e = a.cache.page_size % 8 == 0
+            ? launch_blocks(a, blocks, k_attend_rows<F16, FP8, DV, true>, kRowThreads, stream)
+            : launch_blocks(a, blocks, k_attend_rows<F16, FP8, DV, false>, kRowThreads, stream);
+  }
+  const bool join = (tiles && a.splits > 1) || (rows && a.splits_few > 1);
+  if (!join || e != hipSuccess) return e;
+  const int64_t n = (int64_t)a.batch.T * a.n_q_heads, per = kRowThreads / kWave;
+  return launch_blocks(a, (n + per - 1) / per, k_attend_join<F16>, kRowThreads, stream);
 }
 
 template <bool F16, bool FP8>
-hipError_t launch_depth(const AttendCall& a, hipStream_t stream) {
-  if (a.cache.D <= 64) return launch_rows<F16, FP8, 64>(a, stream);
-  if (a.cache.D <= 128) return launch_rows<F16, FP8, 128>(a, stream);
-  return launch_rows<F16, FP8, 256>(a, stream);
+hipError_t launch_type(const AttendCall& a, hipStream_t stream) {
+  if (a.cache.D <= 64) return launch_depth<F16, FP8, 64>(a, stream);
+  if (a.cache.D <= 128) return launch_depth<F16, FP8, 128>(a, stream);
+  return launch_depth<F16, FP8, 256>(a, stream);
 }
 
 }  // namespace
 
-int attend_splits(const KvCacheView& c, const KvBatchView& b, int n_q_heads, int window,
-                  int keep_first, int max_q, int max_len) {
+AttendPlan attend_plan(const KvCacheView& c, const KvBatchView& b, int n_q_heads, int window,
+                       int keep_first, int max_q, int max_len) {
+  AttendPlan p;
   const int64_t group = n_q_heads / c.n_heads;
-  const int64_t tiles = ((int64_t)b.T * group / kRowTile + b.n_seq) * c.n_heads;
+  // new tokens of the longest chunk; where that is not known, as if all rows were one's
+  const int64_t chunk = max_q > 0 ? min(max_q, b.T) : b.T;
+  p.few = chunk * group <= kFewRows;
+  p.both = !p.few && b.n_seq > 1;
   int64_t keys = (int64_t)b.max_pages * c.page_size;
   if (max_len > 0) keys = min(keys, (int64_t)max_len);
-  if (window) keys = min(keys, (int64_t)window + keep_first + max(max_q, 1));
-  const int64_t want = 1024 / max(tiles, (int64_t)1);   // four workgroups a CU
-  return (int)max(min(want, keys / 256), (int64_t)1);   // of two blocks a wave at least
+  if (window) keys = min(keys, (int64_t)window + keep_first + chunk);
+  const int64_t few_tiles = (p.both ? b.n_seq : (b.T * group / kRowTile + b.n_seq)) * c.n_heads;
+  const int64_t tiles = (b.T * group / kTileRows + 1) * c.n_heads;
+  // four workgroups a CU, of two blocks a wave at least
+  p.splits_few = (int)max(min(1024 / max(few_tiles, (int64_t)1), keys / 256), (int64_t)1);
+  // two workgroups a CU, twice over, of eight blocks at least
+  p.splits = (int)max(min(1024 / max(tiles, (int64_t)1), keys / 512), (int64_t)1);
+  return p;
 }
 
 hipError_t launch_attend(const AttendCall& a, hipStream_t stream) {
   const bool f16 = a.type == kFP16, fp8 = a.cache.type == kE4M3;
-  const hipError_t e = f16 ? (fp8 ? launch_depth<true, true>(a, stream) : launch_depth<true, false>(a, stream))
-                           : (fp8 ? launch_depth<false, true>(a, stream)
-                                  : launch_depth<false, false>(a, stream));
-  if (e != hipSuccess || a.splits == 1) return e;
-  const int64_t rows = (int64_t)a.batch.T * a.n_q_heads, per = kRowThreads / kWave;
-  return f16 ? launch_blocks(a, (rows + per - 1) / per, k_attend_join<true>, kRowThreads, stream)
-             : launch_blocks(a, (rows + per - 1) / per, k_attend_join<false>, kRowThreads, stream);
+  if (f16) return fp8 ? launch_type<true, true>(a, stream) : launch_type<true, false>(a, stream);
+  return fp8 ? launch_type<false, true>(a, stream) : launch_type<false, false>(a, stream);
 }
 
 }  // namespace moe

@@ -221,13 +221,18 @@ struct AttendCall {
   int window, keep_first;
   const float* sinks;
   uint32_t* err;
-  int splits;
+  int splits, splits_few;   // of sequences with many rows (new tokens * group) and with few
+  bool few, both;           // sequences with few rows only; with few and with many
   float* part;              // splits > 1: [splits][T * n_q_heads][D] sums of weighted values,
   float* stats;             // [splits][T * n_q_heads][2] maximum (of log2 e s) and sum of weights
-  int64_t block0;           // set by the launcher: first workgroup of a launch
+  int64_t tiles, block0;    // set by the launcher: tiles, and first workgroup, of a launch
 };
-int attend_splits(const KvCacheView& c, const KvBatchView& b, int n_q_heads, int window,
-                  int keep_first, int max_q, int max_len);
+struct AttendPlan {
+  int splits, splits_few;
+  bool few, both;
+};
+AttendPlan attend_plan(const KvCacheView& c, const KvBatchView& b, int n_q_heads, int window,
+                       int keep_first, int max_q, int max_len);
 hipError_t launch_attend(const AttendCall& a, hipStream_t stream);
 
 // out = resid + act(x w^T + bias) (csrc/linear.hip).
