@@ -777,11 +777,16 @@ __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles
   if (s_odd) add_odd_values<F16>(a, t, blocks, b0, b1, a.splits, split);
 }
 
-// The splits of a row meet: one wave a row, in the splits' order.
+// The splits of a row meet: one workgroup a row. Each wave adds every fourth split's sums, several of
+// them in flight at once, and the four meet in LDS; the order depends on the sizes alone.
+constexpr int kMaxSplits = 256;
 template <bool F16>
 __global__ __launch_bounds__(kRowThreads) void k_attend_join(AttendCall a) {
-  const int lane = threadIdx.x & (kWave - 1);
-  const int64_t row = (a.block0 + blockIdx.x) * (kRowThreads / kWave) + threadIdx.x / kWave;
+  constexpr int NW = kRowThreads / kWave;
+  __shared__ float weight[kMaxSplits];
+  __shared__ f32x4 sums[NW][kWave];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int64_t row = a.block0 + blockIdx.x;
   const int64_t token = row / a.n_q_heads;
   if (token < first_row(a.batch, 0) || token >= first_row(a.batch, a.batch.n_seq)) return;
   int splits = a.few ? a.splits_few : a.splits;
@@ -793,25 +798,49 @@ __global__ __launch_bounds__(kRowThreads) void k_attend_join(AttendCall a) {
   }
   const int head = (int)(row - token * a.n_q_heads);
   const int64_t all = (int64_t)a.batch.T * a.n_q_heads;
+  typedef float f32x2 __attribute__((__vector_size__(8)));
+  f32x2 st[kMaxSplits / kWave];
   float top = -INFINITY;
-  for (int s = 0; s < splits; ++s) top = fmaxf(top, a.stats[2 * (s * all + row)]);
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / kWave; ++i) {
+    const int s = i * kWave + lane;
+    st[i] = s < splits ? *(const f32x2*)(a.stats + 2 * (s * all + row)) : f32x2{-INFINITY, 0.f};
+    top = fmaxf(top, st[i][0]);
+  }
+#pragma unroll
+  for (int x = kWave / 2; x; x >>= 1) top = fmaxf(top, wave_xor(top, x));
   const float sink = a.sinks ? a.sinks[head] * kLog2e : -INFINITY;
   const float high = fmaxf(top, sink);
-  float l = a.sinks ? exp2f(sink - high) : 0.f;
+  float l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / kWave; ++i) {
+    const int s = i * kWave + lane;
+    // a split with nothing in sight has m = -infinity, l = 0
+    const float f = st[i][0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(st[i][0] - high);
+    l = fmaf(f, st[i][1], l);
+    if (wave == 0 && s < splits) weight[s] = f;
+  }
+#pragma unroll
+  for (int x = kWave / 2; x; x >>= 1) l += wave_xor(l, x);
+  if (a.sinks) l += __builtin_amdgcn_exp2f(sink - high);
+  __syncthreads();
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
   const int d = 4 * lane;
-  for (int s = 0; s < splits; ++s) {
-    const float m = a.stats[2 * (s * all + row)];
-    if (m == -INFINITY) continue;   // nothing in sight there
-    const float f = exp2f(m - high);
-    l = fmaf(f, a.stats[2 * (s * all + row) + 1], l);
-    if (d < a.cache.D) {
-      const f32x4 v = *(const f32x4*)(a.part + (s * all + row) * a.cache.D + d);
+  if (d < a.cache.D) {
+    const float* part = a.part + row * a.cache.D + d;
+#pragma unroll 8
+    for (int s = wave; s < splits; s += NW) {
+      const f32x4 v = *(const f32x4*)(part + s * all * a.cache.D);
+      const float f = weight[s];
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] = fmaf(f, v[i], o[i]);
     }
   }
-  if (d >= a.cache.D) return;
+  sums[wave][lane] = o;
+  __syncthreads();
+  if (wave || d >= a.cache.D) return;
+#pragma unroll
+  for (int w = 1; w < NW; ++w) o += sums[w][lane];
   const bool none = top == -INFINITY;
   uint16_t* p = (uint16_t*)a.out.p + token * a.out.token + head * a.out.head + d;
 #pragma unroll
@@ -853,8 +882,7 @@ hipError_t launch_depth(AttendCall a, hipStream_t stream) {
   }
   const bool join = (tiles && a.splits > 1) || (rows && a.splits_few > 1);
   if (!join || e != hipSuccess) return e;
-  const int64_t n = (int64_t)a.batch.T * a.n_q_heads, per = kRowThreads / kWave;
-  return launch_blocks(a, (n + per - 1) / per, k_attend_join<F16>, kRowThreads, stream);
+  return launch_blocks(a, (int64_t)a.batch.T * a.n_q_heads, k_attend_join<F16>, kRowThreads, stream);
 }
 
 template <bool F16, bool FP8>
@@ -879,10 +907,11 @@ AttendPlan attend_plan(const KvCacheView& c, const KvBatchView& b, int n_q_heads
   if (window) keys = min(keys, (int64_t)window + keep_first + chunk);
   const int64_t few_tiles = (p.both ? b.n_seq : (b.T * group / kRowTile + b.n_seq)) * c.n_heads;
   const int64_t tiles = (b.T * group / kTileRows + 1) * c.n_heads;
-  // four workgroups a CU, of two blocks a wave at least
-  p.splits_few = (int)max(min(1024 / max(few_tiles, (int64_t)1), keys / 256), (int64_t)1);
-  // two workgroups a CU, twice over, of eight blocks at least
-  p.splits = (int)max(min(1024 / max(tiles, (int64_t)1), keys / 512), (int64_t)1);
+  // enough workgroups for the CUs, with enough keys each: two blocks a wave, or eight tiles
+  p.splits_few = (int)max(min(min(1024 / max(few_tiles, (int64_t)1), keys / 256),
+                              (int64_t)kMaxSplits), (int64_t)1);
+  p.splits = (int)max(min(min(1024 / max(tiles, (int64_t)1), keys / 512), (int64_t)kMaxSplits),
+                      (int64_t)1);
   return p;
 }
 
