@@ -65,25 +65,29 @@ __device__ __forceinline__ uint32_t widen2(uint32_t v) {
   else
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.f, HI));
 }
-// 2N bytes of a 16-bit cache, or N of an 8-bit one, as N values of the 16-bit type.
-template <int N, bool F16, bool FP8>
-__device__ __forceinline__ void load_row(const uint8_t* plane, int64_t at, uint32_t* w) {
-  if constexpr (!FP8) {
-    if constexpr (N == 8) {
-      const u32x4 v = *(const u32x4*)(plane + 2 * at);
+// N values of a cache's row as they lie there: N / 2 dwords of a 16-bit cache, N / 4 of an 8-bit one.
+template <int N, bool FP8>
+__device__ __forceinline__ void load_raw(const uint8_t* plane, int64_t at, uint32_t* w) {
+  constexpr int DW = FP8 ? N / 4 : N / 2;
+  const uint8_t* p = plane + at * (FP8 ? 1 : 2);
+  if constexpr (DW == 4) {
+    const u32x4 v = *(const u32x4*)p;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = v[i];
-    } else {
-      const u32x2 v = *(const u32x2*)(plane + 2 * at);
-      w[0] = v[0], w[1] = v[1];
-    }
+    for (int i = 0; i < 4; ++i) w[i] = v[i];
+  } else if constexpr (DW == 2) {
+    const u32x2 v = *(const u32x2*)p;
+    w[0] = v[0], w[1] = v[1];
   } else {
+    w[0] = *(const uint32_t*)p;
+  }
+}
+// The same as values of the 16-bit type, two a dword.
+template <int N, bool F16, bool FP8>
+__device__ __forceinline__ void widen(const uint32_t* raw, uint32_t* w) {
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const uint32_t v = ((const uint32_t*)(plane + at))[i];
-      w[2 * i] = widen2<F16, false>(v);
-      w[2 * i + 1] = widen2<F16, true>(v);
-    }
+  for (int i = 0; i < N / 2; ++i) {
+    if constexpr (!FP8) w[i] = raw[i];
+    else w[i] = i & 1 ? widen2<F16, true>(raw[i / 2]) : widen2<F16, false>(raw[i / 2]);
   }
 }
 
@@ -265,9 +269,9 @@ __device__ void add_odd_values(const AttendCall& a, const Tile& t, const Blocks<
 
 // Takes infinities and NaN out of a pair of 16-bit values; whether there were any.
 template <bool F16>
-__device__ __forceinline__ bool take_odd(uint32_t& v) {
+__device__ __forceinline__ bool take_odd(uint32_t& v, bool take = true) {
   constexpr uint32_t e = F16 ? 0x7C00u : 0x7F80u;
-  const bool lo = (v & e) == e, hi = (v >> 16 & e) == e;
+  const bool lo = take & ((v & e) == e), hi = take & ((v >> 16 & e) == e);
   v = (lo ? 0u : v & 0xFFFFu) | (hi ? 0u : v & 0xFFFF0000u);
   return lo || hi;
 }
@@ -283,7 +287,7 @@ constexpr int kRowThreads = 256;
 // scores are those of eight neighbouring keys, 8 (lane / 16) on.
 // P8: pages hold a multiple of 8 tokens, so such a run of keys is on one page.
 template <bool F16, bool FP8, int DV, bool P8>
-__global__ __launch_bounds__(kRowThreads) void k_attend_rows(AttendCall a) {
+__global__ __launch_bounds__(kRowThreads, DV > 128 ? 1 : 2) void k_attend_rows(AttendCall a) {
   constexpr int NW = kRowThreads / kWave;
   constexpr int E = DV >= 128 ? 8 : DV / 16, NH = DV / (16 * E), NK = DV / 32;
   constexpr int OS = DV + 4;
@@ -315,15 +319,17 @@ __global__ __launch_bounds__(kRowThreads) void k_attend_rows(AttendCall a) {
   if (FP8 && a.cache.k_scale) c *= a.cache.k_scale[t.head];
   const uint32_t flip = c < 0.f ? 0x80008000u : 0u;   // scores are scaled by a positive number
   c = fabsf(c) < 1e-37f ? 1e-37f : fabsf(c);
+  // Where in a row a lane's operand of k-step k begins: any order serves that is the same for
+  // queries and keys, and an 8-bit cache's lane takes 16 bytes, two steps, at once.
+  auto depth = [&](int k) { return FP8 ? 64 * (k / 2) + 16 * g + 8 * (k & 1) : 32 * k + 8 * g; };
   u32x4 q[NK];
   {
-    const uint16_t* p = (const uint16_t*)a.q.p + (t.token0 + tok) * a.q.token +
-                        (t.head * a.group + t.row0 + n - tok * a.group) * a.q.head;
+    const uint16_t* p = (const uint16_t*)a.q.p + (int64_t)(t.token0 + tok) * a.q.token +
+                        (int64_t)(t.head * a.group + t.row0 + n - tok * a.group) * a.q.head;
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
-      const int d = 32 * k + 8 * g;
       q[k] = u32x4{0, 0, 0, 0};
-      if (row_ok && d < D) q[k] = *(const u32x4*)(p + d) ^ flip;
+      if (row_ok && depth(k) < D) q[k] = *(const u32x4*)(p + depth(k)) ^ flip;
     }
   }
   f32x4 o[NH][E];
@@ -333,45 +339,73 @@ __global__ __launch_bounds__(kRowThreads) void k_attend_rows(AttendCall a) {
     for (int i = 0; i < E; ++i) o[h][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   float m = -INFINITY, l = 0.f;
 
-  for (int b = b0 + wave; b < b1; b += NW) {
+  // A block's loads, as they lie in the cache; those of the next block are under way while one is
+  // computed. ok: of this lane's eight keys, those on a page and in sight.
+  constexpr int KS = FP8 ? 16 : 8, NL = DV / (4 * KS), KW = 4, VW = FP8 ? E / 4 : E / 2;
+  struct Raw {
+    uint32_t k[2][NL][KW], v[8][NH][VW], ok;
+  };
+  auto load_k = [&](Raw& raw, int u, int64_t at) {
+#pragma unroll
+    for (int k = 0; k < NL; ++k) {
+      const int d = 4 * KS * k + KS * g;
+      load_raw<KS, FP8>(a.cache.k, at + (d < D ? d : 0), raw.k[u][k]);
+    }
+  };
+  auto load_v = [&](Raw& raw, int j, int64_t at) {
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      const int d = 16 * E * h + E * n;
+      load_raw<E, FP8>(a.cache.v, at + (d < D ? d : 0), raw.v[j][h]);
+    }
+  };
+  auto load = [&](Raw& raw, int b) {
     const int key0 = blocks.key(b);
-    u32x4 kf[2][NK];
-    uint32_t vf[8][NH][E / 2];
-    uint32_t v_ok = 0;   // of this lane's eight keys, those whose values are read
-    auto load_k = [&](int u, const KeyRow& r) {
-#pragma unroll
-      for (int k = 0; k < NK; ++k) {
-        const int d = 32 * k + 8 * g;
-        load_row<8, F16, FP8>(a.cache.k, r.k + (d < D ? d : 0), (uint32_t*)&kf[u][k]);
-        if (d >= D) kf[u][k] = u32x4{0, 0, 0, 0};
-      }
-    };
-    auto load_v = [&](int j, int64_t at) {
-#pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        const int d = 16 * E * h + E * n;
-        load_row<E, F16, FP8>(a.cache.v, at + (d < D ? d : 0), vf[j][h]);
-      }
-    };
     if constexpr (P8) {
       const KeyRow rk = key_row<8>(a, t, key0 + 8 * (n >> 2));
 #pragma unroll
       for (int u = 0; u < 2; ++u)
-        load_k(u, {rk.k + (rk.ok ? (4 * u + (n & 3)) * a.cache.k_token : 0), 0, rk.ok});
+        load_k(raw, u, rk.k + (rk.ok ? (4 * u + (n & 3)) * a.cache.k_token : 0));
       const KeyRow rv = key_row<8>(a, t, key0 + 8 * g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) load_v(j, rv.v + (rv.ok ? j * a.cache.v_token : 0));
-      v_ok = rv.ok ? 0xFFu : 0u;
+      for (int j = 0; j < 8; ++j) load_v(raw, j, rv.v + (rv.ok ? j * a.cache.v_token : 0));
+      raw.ok = rv.ok ? 0xFFu : 0u;
     } else {
+      raw.ok = 0;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) load_k(u, key_row<1>(a, t, key0 + 8 * (n >> 2) + 4 * u + (n & 3)));
+      for (int u = 0; u < 2; ++u)
+        load_k(raw, u, key_row<1>(a, t, key0 + 8 * (n >> 2) + 4 * u + (n & 3)).k);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const KeyRow rv = key_row<1>(a, t, key0 + 8 * g + j);
-        load_v(j, rv.v);
-        v_ok |= (uint32_t)rv.ok << j;
+        load_v(raw, j, rv.v);
+        raw.ok |= (uint32_t)rv.ok << j;
       }
     }
+  };
+
+  Raw raw;
+  if (b0 + wave < b1) load(raw, b0 + wave);
+  for (int b = b0 + wave; b < b1; b += NW) {
+    const int key0 = blocks.key(b);
+    Raw next;
+    if (b + NW < b1) load(next, b + NW);
+    u32x4 kf[2][NK];
+    uint32_t vf[8][NH][E / 2];
+    const uint32_t v_ok = raw.ok;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int k = 0; k < NL; ++k) {
+        widen<KS, F16, FP8>(raw.k[u][k], (uint32_t*)&kf[u][k * NK / NL]);
+        if (4 * KS * k + KS * g >= D)
+#pragma unroll
+          for (int i = 0; i < NK / NL; ++i) kf[u][k * NK / NL + i] = u32x4{0, 0, 0, 0};
+      }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int h = 0; h < NH; ++h) widen<E, F16, FP8>(raw.v[j][h], vf[j][h]);
     f32x4 s[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -440,6 +474,7 @@ __global__ __launch_bounds__(kRowThreads) void k_attend_rows(AttendCall a) {
           vt[j] = __builtin_amdgcn_perm(vf[2 * j + 1][h][i / 2], vf[2 * j][h][i / 2], sel);
         o[h][i] = mma16<F16>(vt, pf, o[h][i]);
       }
+    raw = next;
   }
 
   l += wave_xor(l, 16);
@@ -545,13 +580,12 @@ __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles
   const int see_last = !row_ok ? -1 : a.causal ? min(pos, t.end - 1) : t.end - 1;
   const int see_first = window_start(a, pos);
   const int keep = a.window ? a.keep_first : 0;
-  // of the wave's rows: what all of them and any of them sees last, and sees first
+  // what all of the wave's rows see last, and first
   const int w_rows = min(max(t.rows - 32 * wave, 0), 32);
   const int w_first = t.pos0 + (t.row0 + 32 * wave) / a.group;
   const int w_last = t.pos0 + (t.row0 + 32 * wave + max(w_rows, 1) - 1) / a.group;
   const int w_all = a.causal ? min(w_first, t.end - 1) : t.end - 1;
-  const int w_any = w_rows == 0 ? -1 : a.causal ? min(w_last, t.end - 1) : t.end - 1;
-  const int w_begin = window_start(a, w_first), w_from = window_start(a, w_last);
+  const int w_from = window_start(a, w_last);
   float c = a.scale * kLog2e;
   if (FP8 && a.cache.k_scale) c *= a.cache.k_scale[t.head];
   const uint32_t flip = c < 0.f ? 0x80008000u : 0u;
@@ -574,191 +608,263 @@ __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles
     for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
   float m = -INFINITY, l = 0.f;
 
-  // loads: this lane's chunk of a row, and its row of each pass
+  // Loads: this lane's chunk of a row, and the rows of each pass, j RP + rsub.
   const int chunk = lane % CH, rsub = lane / CH;
   const bool chunk_ok = chunk * CV < D;
+  constexpr int kSize = FP8 ? 1 : 2;
+  const uint32_t k_off = (uint32_t)(rsub * a.cache.k_token + (chunk_ok ? chunk * CV : 0)) * kSize;
+  const uint32_t v_off = (uint32_t)(rsub * a.cache.v_token + (chunk_ok ? chunk * CV : 0)) * kSize;
   u32x4 kr[NP], vr[NP];
-  uint32_t ok16 = 0;       // rows of this wave's 16 whose keys are in sight and on a page
-  int page = 0;            // U16: table entry of the next tile's rows
-  auto in_sight = [&](int p) { return p < t.end && (p >= t.first || p < t.kept); };
-  auto lookup = [&](int b) {   // entries are asked for a tile ahead of their use
+  // Of this wave's 16 rows of a block: U16, their page (asked for a block ahead of its use) and the
+  // row of it, and which are on a page and in sight.
+  struct Rows {
+    int page, row;
+    uint32_t ok;
+  };
+  auto lookup = [&](int b) {
+    Rows r = {0, 0, 0};
     if constexpr (U16) {
       const int p = blocks.key(b) + 16 * wave;
       if (b < b1 && p < t.end && (p + 16 > t.first || p < t.kept)) {
-        int row;
-        page = a.batch.table[t.seq * a.batch.table_stride +
-                             page_of((uint32_t)p, a.cache.page_size, a.cache.page_inv, &row)];
+        const int e = page_of((uint32_t)p, a.cache.page_size, a.cache.page_inv, &r.row);
+        r.page = a.batch.table[t.seq * a.batch.table_stride + e];
+        const uint32_t below = t.end - p >= 16 ? 0xFFFFu : (1u << (t.end - p)) - 1;
+        const uint32_t from = p >= t.first ? 0xFFFFu : (0xFFFFu << min(t.first - p, 16)) & 0xFFFFu;
+        const uint32_t kept = p >= t.kept ? 0u
+                              : t.kept - p >= 16 ? 0xFFFFu : (1u << (t.kept - p)) - 1;
+        r.ok = below & (from | kept);
       }
     }
+    return r;
   };
-  auto load_tile = [&](int b) {
-    const int p0 = blocks.key(b) + 16 * wave;
-    ok16 = 0;
+  auto checked = [&](Rows r) {   // U16: a page outside the cache is page 0, with no row in sight
     if constexpr (U16) {
-      int row;
-      page_of((uint32_t)p0, a.cache.page_size, a.cache.page_inv, &row);
-      const bool seen = p0 < t.end && (p0 + 16 > t.first || p0 < t.kept);
-      const bool good = seen && (unsigned)page < (unsigned)a.cache.n_pages;
-      if (seen && !good && a.err && lane == 0) atomicOr(a.err, 1u);
-      const int64_t pg = __builtin_amdgcn_readfirstlane(good ? page : 0);
-      row = __builtin_amdgcn_readfirstlane(good ? row : 0);
-      const bool one = !good;   // no such page: row 0 of page 0, over and over
-      const int64_t kb = pg * a.cache.k_page + row * a.cache.k_token + t.head * a.cache.k_head;
-      const int64_t vb = pg * a.cache.v_page + row * a.cache.v_token + t.head * a.cache.v_head;
+      r.page = __builtin_amdgcn_readfirstlane(r.page);
+      if ((unsigned)r.page >= (unsigned)a.cache.n_pages) {
+        if (a.err && lane == 0) atomicOr(a.err, 1u);
+        r = {0, 0, 0};
+      }
+    }
+    return r;
+  };
+  auto load_k = [&](int b, Rows& r) {
+    if constexpr (U16) {
+      const uint8_t* base = a.cache.k + (r.page * a.cache.k_page + r.row * a.cache.k_token +
+                                         t.head * a.cache.k_head) * kSize;
+#pragma unroll
+      for (int j = 0; j < NP; ++j)
+        kr[j] = *(const u32x4*)(base + j * RP * a.cache.k_token * kSize + k_off);
+    } else {
+      r.ok = 0;
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
-        const int rr = one ? 0 : j * RP + rsub;
-        const int64_t d = chunk_ok ? chunk * CV : 0;
-        kr[j] = *(const u32x4*)(a.cache.k + (kb + rr * a.cache.k_token + d) * (FP8 ? 1 : 2));
-        vr[j] = *(const u32x4*)(a.cache.v + (vb + rr * a.cache.v_token + d) * (FP8 ? 1 : 2));
+        const KeyRow kv = key_row<1>(a, t, blocks.key(b) + 16 * wave + j * RP + rsub);
+        kr[j] = *(const u32x4*)(a.cache.k + (kv.k + (chunk_ok ? chunk * CV : 0)) * kSize);
+        const uint64_t rows = __ballot(kv.ok);
+#pragma unroll
+        for (int i = 0; i < RP; ++i) r.ok |= (uint32_t)(rows >> (i * CH) & 1) << (j * RP + i);
       }
-      if (good) {
-        const uint32_t below = t.end - p0 >= 16 ? 0xFFFFu : (1u << (t.end - p0)) - 1;
-        const uint32_t from = p0 >= t.first ? 0xFFFFu : (0xFFFFu << min(t.first - p0, 16)) & 0xFFFFu;
-        const uint32_t kept = p0 >= t.kept ? 0u
-                              : t.kept - p0 >= 16 ? 0xFFFFu : (1u << (t.kept - p0)) - 1;
-        ok16 = below & (from | kept);
-      }
+      r.ok = __builtin_amdgcn_readfirstlane(r.ok);
+    }
+  };
+  auto load_v = [&](int b, const Rows& r) {
+    if constexpr (U16) {
+      const uint8_t* base = a.cache.v + (r.page * a.cache.v_page + r.row * a.cache.v_token +
+                                         t.head * a.cache.v_head) * kSize;
+#pragma unroll
+      for (int j = 0; j < NP; ++j)
+        vr[j] = *(const u32x4*)(base + j * RP * a.cache.v_token * kSize + v_off);
     } else {
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
-        const KeyRow kv = key_row<1>(a, t, p0 + j * RP + rsub);
-        const int64_t d = chunk_ok ? chunk * CV : 0;
-        kr[j] = *(const u32x4*)(a.cache.k + (kv.k + d) * (FP8 ? 1 : 2));
-        vr[j] = *(const u32x4*)(a.cache.v + (kv.v + d) * (FP8 ? 1 : 2));
-        const uint64_t rows = __ballot(kv.ok);
-#pragma unroll
-        for (int i = 0; i < RP; ++i) ok16 |= (uint32_t)(rows >> (i * CH) & 1) << (j * RP + i);
+        const KeyRow kv = key_row<1>(a, t, blocks.key(b) + 16 * wave + j * RP + rsub);
+        vr[j] = *(const u32x4*)(a.cache.v + (kv.v + (chunk_ok ? chunk * CV : 0)) * kSize);
       }
     }
-    ok16 = __builtin_amdgcn_readfirstlane(ok16);
   };
-  auto store_tile = [&](int b, int to) {
+  constexpr int NW = CV / 2;   // dwords of a chunk's 16-bit values
+  auto widened = [&](const u32x4& raw, uint32_t* w) {
+    widen<CV, F16, FP8>((const uint32_t*)&raw, w);
+    if (D != DV) {
+#pragma unroll
+      for (int i = 0; i < NW; ++i) w[i] = chunk_ok ? w[i] : 0;
+    }
+  };
+  auto store_k = [&](int to) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      uint32_t w[8];
+      widened(kr[j], w);
+      uint16_t* p = &buf[to].k[16 * wave + j * RP + rsub][chunk * CV];
+#pragma unroll
+      for (int i = 0; i < NW; i += 4) *(u32x4*)(p + 2 * i) = u32x4{w[i], w[i + 1], w[i + 2], w[i + 3]};
+    }
+  };
+  auto store_v = [&](int b, int to, const Rows& r) {
     const bool seen = whole_block<kTileKeys>(a, t, blocks.key(b));
+    const bool plain = seen && r.ok == 0xFFFFu;
     bool odd = false;
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       const int row = j * RP + rsub;
-      uint32_t k[2 * 4], v[2 * 4];
-      if constexpr (FP8) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          k[2 * i] = widen2<F16, false>(kr[j][i]), k[2 * i + 1] = widen2<F16, true>(kr[j][i]);
-          v[2 * i] = widen2<F16, false>(vr[j][i]), v[2 * i + 1] = widen2<F16, true>(vr[j][i]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) k[i] = kr[j][i], v[i] = vr[j][i];
-      }
-      constexpr int NW = CV / 2;
-      if (DV != D && !chunk_ok) {
-#pragma unroll
-        for (int i = 0; i < NW; ++i) k[i] = v[i] = 0;
-      }
-      if (!seen || ok16 != 0xFFFFu) {
-        const bool some = ok16 >> row & 1;   // out of sight: zeros
+      uint32_t w[8];
+      widened(vr[j], w);
+      if (!plain) {
+        const bool some = r.ok >> row & 1;   // out of sight: zeros
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
-          v[i] = some ? v[i] : 0;
-          if (!seen) odd |= take_odd<F16>(v[i]);
+          w[i] = some ? w[i] : 0;
+          odd |= take_odd<F16>(w[i], !seen);
         }
       }
-      uint16_t* kp = &buf[to].k[16 * wave + row][chunk * CV];
-      uint16_t* vp = &buf[to].v[16 * wave + row][chunk * CV];
+      uint16_t* p = &buf[to].v[16 * wave + row][chunk * CV];
 #pragma unroll
-      for (int i = 0; i < NW; i += 4) {
-        *(u32x4*)(kp + 2 * i) = u32x4{k[i], k[i + 1], k[i + 2], k[i + 3]};
-        *(u32x4*)(vp + 2 * i) = u32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
-      }
+      for (int i = 0; i < NW; i += 4) *(u32x4*)(p + 2 * i) = u32x4{w[i], w[i + 1], w[i + 2], w[i + 3]};
     }
     if (odd) s_odd = 1;
-    if (lane == 0) ((uint16_t*)&s_ok[to])[wave] = (uint16_t)ok16;
+    if (lane == 0) ((uint16_t*)&s_ok[to])[wave] = (uint16_t)r.ok;
   };
 
-  if (b0 < b1) {
-    lookup(b0);
-    load_tile(b0);
-    lookup(b0 + 1);
-    store_tile(b0, 0);
-  }
-  __syncthreads();
-  for (int b = b0; b < b1; ++b) {
-    const int at = (b - b0) & 1;
-    if (b + 1 < b1) {
-      load_tile(b + 1);
-      lookup(b + 2);
-    }
-    const int key0 = blocks.key(b);
-    const uint64_t ok = s_ok[at];
-    if (key0 <= w_any && (key0 + kTileKeys > w_begin || key0 < keep)) {
-      f32x16 s[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[u][i] = 0.f;
-#pragma unroll
-        for (int k = 0; k < NK; ++k)
-          s[u] = mma32<F16>(*(const u32x4*)&buf[at].k[32 * u + n][16 * k + 8 * hf], q[k], s[u]);
-      }
-      // s[u][i]: the score of query n and key key0 + 32 u + 8 (i / 4) + 4 hf + i % 4
-      const int key_l = key0 + 4 * hf;
-      const int to_last = see_last - key_l, to_first = see_first - key_l, to_keep = keep - key_l;
-      float x[32];   // scores, then weights
-#pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = s[i / 16][i % 16];
-      // Selects of scalars, no branches: with a branch a mask, or a store into an element of s, was
-      // compiled to code that left the first element as it was.
-      if (!(key0 + kTileKeys - 1 <= w_all && (key0 >= w_from || key0 + kTileKeys - 1 < keep))) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int k = 32 * (i / 16) + 8 * (i % 16 / 4) + i % 4;   // of key key_l + k
-          const bool out = (k > to_last) | ((k < to_first) & (k >= to_keep));
-          x[i] = out ? -INFINITY : x[i];
-        }
-      }
-      if (ok != ~0ull) {
-        const uint64_t ok_l = ok >> 4 * hf;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int k = 32 * (i / 16) + 8 * (i % 16 / 4) + i % 4;
-          x[i] = ok_l >> k & 1 ? x[i] : -INFINITY;
-        }
-      }
-      float top = x[0];
-#pragma unroll
-      for (int i = 1; i < 32; ++i) top = fmaxf(top, x[i]);
-      top *= c;
-      if (__any(top > m + kRaise)) {
-        top = fmaxf(top, wave_xor(top, 32));
-        const float to = top > m + kRaise ? ceilf(top) : m;   // by a row's own scores alone
-        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - to);
-        m = to;
-        l *= f;
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[d][i] *= f;
-      }
-      const float base = m == -INFINITY ? 0.f : m;
-      u32x4 p[4];
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], c, -base));
-        x[i + 1] = __builtin_amdgcn_exp2f(fmaf(x[i + 1], c, -base));
-        l += x[i] + x[i + 1];
-        p[i / 8][i % 8 / 2] = pack2<F16>(x[i], x[i + 1]);
-      }
+  // Whether all rows of this wave see all of a block. (A wave none of whose rows sees any of it goes
+  // through it with the others: leaving the products out cost more registers than it saved time.)
+  auto whole = [&](int key0) {
+    return key0 + kTileKeys - 1 <= w_all && (key0 >= w_from || key0 + kTileKeys - 1 < keep);
+  };
+  auto key_frag = [&](int at, int u, int k) {   // operand of k-step k of the scores of half u
+    return *(const u32x4*)&buf[at].k[32 * u + n][16 * k + 8 * hf];
+  };
+  auto value_frag = [&](int at, int k, int d) {   // of keys 16 k on, values 32 d on
+    const uint16_t* v = &buf[at].v[16 * k + 4 * hf + (lane & 15) / 4]
+                                  [32 * d + 16 * (n / 16) + 4 * (lane & 3)];
+    const u32x2 lo = read_columns(v), hi = read_columns(v + 8 * kValueStride<DV>);
+    return u32x4{lo[0], lo[1], hi[0], hi[1]};
+  };
+  auto raise = [&](float top) {
+    top *= c;
+    if (__any(top > m + kRaise)) {
+      top = fmaxf(top, wave_xor(top, 32));
+      const float to = top > m + kRaise ? ceilf(top) : m;   // by a row's own scores alone
+      const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - to);
+      m = to;
+      l *= f;
 #pragma unroll
       for (int d = 0; d < ND; ++d)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint16_t* v = &buf[at].v[16 * k + 4 * hf + (lane & 15) / 4]
-                                        [32 * d + 16 * (n / 16) + 4 * (lane & 3)];
-          const u32x2 lo = read_columns(v), hi = read_columns(v + 8 * kValueStride<DV>);
-          o[d] = mma32<F16>(u32x4{lo[0], lo[1], hi[0], hi[1]}, p[k], o[d]);
-        }
+        for (int i = 0; i < 16; ++i) o[d][i] *= f;
     }
-    if (b + 1 < b1) store_tile(b + 1, at ^ 1);
+    return m == -INFINITY ? 0.f : -m;
+  };
+
+  // A step takes 32 keys, half a block: the next half's scores beside this one's weights, then the
+  // weighted values. So the second half's keys are wanted with a block's values and the first half's
+  // a step before them: of two buffers, block b writes the second half of b + 1 and the first half of
+  // b + 2, which `low` waves load, over keys that were last read before the barrier.
+  const bool low = wave < 2;
+  Rows now = {0, 0, 0}, next = {0, 0, 0}, far = {0, 0, 0};
+  if (b0 < b1) {
+    now = checked(lookup(b0));
+    load_k(b0, now);
+    load_v(b0, now);
+    next = lookup(b0 + 1);
+    store_k(0);
+    store_v(b0, 0, now);
+    next = checked(next);
+    if (low && b0 + 1 < b1) {
+      load_k(b0 + 1, next);
+      store_k(1);
+    }
+    far = lookup(b0 + 2);
+  }
+  __syncthreads();
+  // Scores of the blocks' first and second halves: [i] of key 8 (i / 4) + 4 hf + i % 4 of the half.
+  f32x16 s0, s1;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s0[i] = 0.f;
+#pragma unroll
+  for (int k = 0; k < NK; ++k) s0 = mma32<F16>(key_frag(0, 0, k), q[k], s0);
+  auto step = [&](auto half, int key0, uint32_t ok, bool all, int at, const f32x16& in, f32x16& out) {
+    constexpr int U = decltype(half)::value;
+    float x[16];   // scores, then weights
+    u32x4 p[2];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = in[i];
+    // Selects of scalars, no branches: with a branch a mask, or a store into an element of a
+    // vector, was compiled to code that left the first element as it was.
+    if (!all) {
+      const int key_l = key0 + 32 * U + 4 * hf;
+      const int to_last = see_last - key_l, to_first = see_first - key_l, to_keep = keep - key_l;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int k = 8 * (i / 4) + i % 4;   // of key key_l + k
+        const bool no = (k > to_last) | ((k < to_first) & (k >= to_keep));
+        x[i] = no ? -INFINITY : x[i];
+      }
+    }
+    if (ok != ~0u) {
+      const uint32_t ok_l = ok >> 4 * hf;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = ok_l >> (8 * (i / 4) + i % 4) & 1 ? x[i] : -INFINITY;
+    }
+    float top = x[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
+    const float base = raise(top);
+    auto weights = [&](int i) {   // of two keys
+      x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], c, base));
+      x[i + 1] = __builtin_amdgcn_exp2f(fmaf(x[i + 1], c, base));
+      l += x[i] + x[i + 1];
+      asm("" : "+v"(l));   // here, not behind the loop's end: the weights would stay in registers
+      p[i / 8][i % 8 / 2] = pack2<F16>(x[i], x[i + 1]);
+    };
+    // Each matrix instruction has weights to run beside it. (Behind the last block the scores are of
+    // what lies in LDS, and are dropped.)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) out[i] = 0.f;
+    constexpr int NV = 2 * ND, AHEAD = 2;
+    u32x4 kf[AHEAD + 1], vf[AHEAD + 1];
+    const int k_at = U ? at ^ 1 : at;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) kf[i] = key_frag(k_at, 1 - U, i);
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      if (i + AHEAD < NK) kf[(i + AHEAD) % (AHEAD + 1)] = key_frag(k_at, 1 - U, i + AHEAD);
+      out = mma32<F16>(kf[i % (AHEAD + 1)], q[i], out);
+      if constexpr (NK <= 8) {
+#pragma unroll
+        for (int e = 0; e < 8 / NK; ++e) weights(2 * (i * (8 / NK) + e));
+      } else if (i % (NK / 8) == 0) {
+        weights(2 * (i / (NK / 8)));
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) vf[i] = value_frag(at, 2 * U + i / ND, i % ND);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int f = i + AHEAD;
+      if (f < NV) vf[f % (AHEAD + 1)] = value_frag(at, 2 * U + f / ND, f % ND);
+      o[i % ND] = mma32<F16>(vf[i % (AHEAD + 1)], p[i / ND], o[i % ND]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  for (int b = b0; b < b1; ++b) {
+    const int at = (b - b0) & 1;
+    Rows last = checked(far);
+    far = lookup(b + 3);
+    const int kb = low ? b + 2 : b + 1;   // whose keys this wave loads
+    if (kb < b1) {
+      if (low) load_k(kb, last);
+      else load_k(kb, next);
+    }
+    if (b + 1 < b1) load_v(b + 1, next);
+    const int key0 = blocks.key(b);
+    const uint64_t ok = s_ok[at];
+    const bool all = whole(key0);
+    step(std::integral_constant<int, 0>{}, key0, (uint32_t)ok, all, at, s0, s1);
+    step(std::integral_constant<int, 1>{}, key0, (uint32_t)(ok >> 32), all, at, s1, s0);
+    if (kb < b1) store_k(low ? at : at ^ 1);
+    if (b + 1 < b1) store_v(b + 1, at ^ 1, next);
+    next = last;
     __syncthreads();
   }
 
@@ -869,7 +975,9 @@ hipError_t launch_depth(AttendCall a, hipStream_t stream) {
   if (tiles) {
     a.tiles = (int64_t)a.batch.T * a.group / kTileRows + a.batch.n_seq;
     const int64_t blocks = a.tiles * a.cache.n_heads * a.splits;
-    e = a.cache.page_size % 16 == 0
+    // a page's 16 rows have to be within 32-bit offsets of the first
+    const bool near = max(a.cache.k_token, a.cache.v_token) < (int64_t(1) << 26);
+    e = a.cache.page_size % 16 == 0 && near
             ? launch_blocks(a, blocks, k_attend_tiles<F16, FP8, DV, true>, kTileThreads, stream)
             : launch_blocks(a, blocks, k_attend_tiles<F16, FP8, DV, false>, kTileThreads, stream);
   }
@@ -908,7 +1016,7 @@ AttendPlan attend_plan(const KvCacheView& c, const KvBatchView& b, int n_q_heads
   const int64_t few_tiles = (p.both ? b.n_seq : (b.T * group / kRowTile + b.n_seq)) * c.n_heads;
   const int64_t tiles = (b.T * group / kTileRows + 1) * c.n_heads;
   // enough workgroups for the CUs, with enough keys each: two blocks a wave, or eight tiles
-  p.splits_few = (int)max(min(min(1024 / max(few_tiles, (int64_t)1), keys / 256),
+  p.splits_few = (int)max(min(min(512 / max(few_tiles, (int64_t)1), keys / 256),
                               (int64_t)kMaxSplits), (int64_t)1);
   p.splits = (int)max(min(min(1024 / max(tiles, (int64_t)1), keys / 512), (int64_t)kMaxSplits),
                       (int64_t)1);
