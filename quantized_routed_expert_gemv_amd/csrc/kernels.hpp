@@ -246,7 +246,10 @@ struct LinearCall {
   const void* resid;
   void* out;
   int out_type;
-  int64_t tile0;            // set by the launcher: first tile of a launch
+  // set by the launcher: whether four neighbouring outputs and residuals lie on whole vectors; the
+  // first tile of a launch
+  bool vec4;
+  int64_t tile0;
 };
 hipError_t launch_linear(const LinearCall& a, hipStream_t stream);
 

@@ -100,13 +100,169 @@ __global__ __launch_bounds__(kThreads) void k_linear_rows(LinearCall a) {
   }
 }
 
+// Four neighbouring outputs of row m, n on: whole vectors where the caller's rows allow it.
+__device__ __forceinline__ void finish4(const LinearCall& a, int64_t m, int64_t n, f32x4 v) {
+  if (!a.vec4 || n + 4 > a.N) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < a.N) finish(a, m, n + e, v[e]);
+    return;
+  }
+  if (a.bias) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += load1(a.bias, n + e, a.bias_type);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = activate(v[e], a.act);
+  if (a.resid) {
+    const int64_t at = m * a.resid_stride + n;
+    if (a.out_type == kFP32) {
+      v += *(const f32x4*)((const float*)a.resid + at);
+    } else {
+      const u32x2 r = *(const u32x2*)((const uint16_t*)a.resid + at);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint16_t h = uint16_t(r[e / 2] >> 16 * (e & 1));
+        v[e] += a.out_type == kFP16 ? fp16_to_f32(h) : bf16_to_f32(h);
+      }
+    }
+  }
+  const int64_t at = m * a.out_stride + n;
+  if (a.out_type == kFP32) {
+    *(f32x4*)((float*)a.out + at) = v;
+  } else {
+    u32x2 w;
+    if (a.out_type == kFP16) {
+      typedef _Float16 f16x2 __attribute__((__vector_size__(4)));
+      w = u32x2{__builtin_bit_cast(uint32_t, f16x2{(_Float16)v[0], (_Float16)v[1]}),
+                __builtin_bit_cast(uint32_t, f16x2{(_Float16)v[2], (_Float16)v[3]})};
+    } else {
+      w = u32x2{__builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[0], (__bf16)v[1]}),
+                __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[2], (__bf16)v[3]})};
+    }
+    *(u32x2*)((uint16_t*)a.out + at) = w;
+  }
+}
+
+typedef __attribute__((address_space(3))) void* lds_ptr;
+typedef __attribute__((address_space(1))) const void* global_ptr;
+
+// The waves meet: their LDS accesses are done, and of their loads into LDS all but the newest N. A
+// fence would wait for all of them.
+template <int N>
+__device__ __forceinline__ void meet() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// Many rows: the matrix instructions bound it. A workgroup of WM x WN waves makes a tile of BM rows
+// of x and BN of w, 64 values of K a step. Steps land in LDS straight from memory, S - 1 of them
+// under way; a row's 16-byte pieces lie there in the order piece ^ (row % 8), so that the 16 rows
+// that an operand's lanes read fall on different banks.
+template <bool F16, int BM, int BN, int WM, int WN, int S>
+__global__ __launch_bounds__(WM * WN * kWave) void k_linear_tile(LinearCall a) {
+  constexpr int NW = WM * WN, BK = 64;
+  constexpr int TM = BM / WM / 16, TN = BN / WN / 16;      // 16 x 16 products of a wave
+  constexpr int LM = BM / 8 / NW, LN = BN / 8 / NW;        // loads of 8 rows, of a wave and step
+  static_assert(LM * 8 * NW == BM && LN * 8 * NW == BN, "rows share out among the waves");
+  constexpr int kStage = (BM + BN) * BK * 2;
+  __shared__ __align__(16) uint8_t lds[S * kStage];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int r = lane & 15, g = lane >> 4;
+
+  // an eighth of the tiles to each XCD (workgroups go round them), 8 tiles of M by N at a time
+  const int64_t tm = ((int64_t)a.M + BM - 1) / BM, tn = ((int64_t)a.N + BN - 1) / BN;
+  int64_t id = a.tile0 + blockIdx.x;
+  {
+    const int64_t all = tm * tn, per = (all + 7) / 8, x = id % 8, full = all - 8 * (per - 1);
+    id = id / 8 + (x < full ? x * per : full * per + (x - full) * (per - 1));
+  }
+  const int64_t band = id / (8 * tn), left = id % (8 * tn), high = min(tm - 8 * band, (int64_t)8);
+  const int64_t m0 = (8 * band + left % high) * BM, n0 = left / high * BN;
+
+  // this wave's rows to load, 8 at a time: lane -> row lane / 8, piece (lane % 8) ^ row
+  const int piece = (lane & 7) ^ (lane >> 3);
+  const uint16_t* src[LM + LN];
+#pragma unroll
+  for (int i = 0; i < LM + LN; ++i) {
+    const int row = 8 * ((i < LM ? i : i - LM) * NW + wave) + (lane >> 3);
+    src[i] = (i < LM ? a.x + min(m0 + row, (int64_t)a.M - 1) * a.x_stride
+                     : a.w + min(n0 + row, (int64_t)a.N - 1) * a.w_stride) + 8 * piece;
+  }
+  auto place = [&](int stage, int i) {   // of load i's eight rows in LDS
+    return lds + stage * kStage + (i < LM ? 0 : BM * BK * 2) + ((i < LM ? i : i - LM) * NW + wave) * 1024;
+  };
+  auto load = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < LM + LN; ++i)
+      __builtin_amdgcn_global_load_lds((global_ptr)(src[i] + (int64_t)c * BK), (lds_ptr)place(c % S, i),
+                                       16, 0, 0);
+  };
+  f32x4 acc[TN][TM];
+#pragma unroll
+  for (int i = 0; i < TN; ++i)
+#pragma unroll
+    for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int wm = wave / WN, wn = wave % WN;
+  auto compute = [&](int stage) {
+    const uint8_t* xs = lds + stage * kStage + wm * (BM / WM) * BK * 2;
+    const uint8_t* ws = lds + stage * kStage + (BM + wn * (BN / WN)) * BK * 2;
+#pragma unroll
+    for (int k = 0; k < BK / 32; ++k) {
+      const int at = r * BK * 2 + (((4 * k + g) ^ (r & 7)) * 16);
+      u32x4 xf[TM], wf[TN];
+#pragma unroll
+      for (int j = 0; j < TM; ++j) xf[j] = *(const u32x4*)(xs + j * 16 * BK * 2 + at);
+#pragma unroll
+      for (int i = 0; i < TN; ++i) wf[i] = *(const u32x4*)(ws + i * 16 * BK * 2 + at);
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int j = 0; j < TM; ++j) acc[i][j] = mma16<F16>(wf[i], xf[j], acc[i][j]);
+    }
+  };
+  const int steps = a.K / BK;   // whole ones
+#pragma unroll
+  for (int c = 0; c < S - 1; ++c)
+    if (c < steps) load(c);
+  for (int c = 0; c < steps; ++c) {
+    // step c is there: of the loads under way only those of the S - 2 steps behind it are left
+    if (c + S - 1 <= steps) meet<(S - 2) * (LM + LN)>();
+    else meet<0>();
+    if (c + S - 1 < steps) load(c + S - 1);
+    compute(c % S);
+  }
+  if (steps * BK < a.K) {   // the rest of K, with zeros behind it
+    meet<0>();
+#pragma unroll
+    for (int i = 0; i < LM + LN; ++i) {
+      u32x4 v = {0, 0, 0, 0};
+      if (steps * BK + 8 * piece < a.K) v = *(const u32x4*)(src[i] + (int64_t)steps * BK);
+      *(u32x4*)(place(0, i) + 16 * lane) = v;
+    }
+    meet<0>();
+    compute(0);
+  }
+  // lane: row r of x, rows 4 g .. + 3 of w of each product
+#pragma unroll
+  for (int j = 0; j < TM; ++j) {
+    const int64_t m = m0 + wm * (BM / WM) + 16 * j + r;
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      const int64_t n = n0 + wn * (BN / WN) + 16 * i + 4 * g;
+      if (m < a.M && n < a.N) finish4(a, m, n, acc[i][j]);
+    }
+  }
+}
+
 constexpr int64_t kMaxTiles = 1 << 22;   // a launch holds fewer than 2^32 threads
 
 template <typename K>
-hipError_t launch_tiles(LinearCall a, int64_t tiles, K kernel, hipStream_t stream) {
+hipError_t launch_tiles(LinearCall a, int64_t tiles, K kernel, int threads,
+                        hipStream_t stream) {
   for (int64_t t = 0; t < tiles; t += kMaxTiles) {
     a.tile0 = t;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)min(tiles - t, kMaxTiles)), dim3(kThreads), 0, stream,
+    hipLaunchKernelGGL(kernel, dim3((unsigned)min(tiles - t, kMaxTiles)), dim3(threads), 0, stream,
                        a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -114,12 +270,25 @@ hipError_t launch_tiles(LinearCall a, int64_t tiles, K kernel, hipStream_t strea
   return hipSuccess;
 }
 
+template <bool F16, int BM, int BN, int WM, int WN, int S>
+hipError_t launch_tile(const LinearCall& a, hipStream_t stream) {
+  const int64_t tiles = (((int64_t)a.M + BM - 1) / BM) * (((int64_t)a.N + BN - 1) / BN);
+  return launch_tiles(a, tiles, k_linear_tile<F16, BM, BN, WM, WN, S>, WM * WN * kWave, stream);
+}
+
 template <bool F16>
-hipError_t launch_t(const LinearCall& a, hipStream_t stream) {
+hipError_t launch_t(LinearCall a, hipStream_t stream) {
   const int64_t n = ((int64_t)a.N + 15) / 16;
-  if (a.M <= 16) return launch_tiles(a, n, k_linear_rows<F16, 1>, stream);
-  if (a.M <= 32) return launch_tiles(a, n, k_linear_rows<F16, 2>, stream);
-  return launch_tiles(a, n * (((int64_t)a.M + 63) / 64), k_linear_rows<F16, 4>, stream);
+  const int bytes = a.out_type == kFP32 ? 4 : 2;
+  a.vec4 = ((uintptr_t)a.out & (4 * bytes - 1)) == 0 && a.out_stride % 4 == 0 &&
+           (!a.resid || (((uintptr_t)a.resid & (4 * bytes - 1)) == 0 && a.resid_stride % 4 == 0));
+  if (a.M <= 16) return launch_tiles(a, n, k_linear_rows<F16, 1>, kThreads, stream);
+  if (a.M <= 32) return launch_tiles(a, n, k_linear_rows<F16, 2>, kThreads, stream);
+  if (a.M <= 64) return launch_tiles(a, n, k_linear_rows<F16, 4>, kThreads, stream);
+  auto tiles = [&](int64_t b) { return (a.M + b - 1) / b * ((a.N + b - 1) / b); };
+  if (tiles(256) >= 200) return launch_tile<F16, 256, 256, 2, 4, 2>(a, stream);
+  if (tiles(128) >= 200) return launch_tile<F16, 128, 128, 2, 2, 2>(a, stream);
+  return launch_tile<F16, 64, 64, 2, 2, 4>(a, stream);
 }
 
 }  // namespace
