@@ -52,54 +52,6 @@ __device__ __forceinline__ void finish(const LinearCall& a, int64_t m, int64_t n
   store1(a.out, m * a.out_stride + n, a.out_type, v);
 }
 
-// Few rows: one workgroup 16 rows of w; its four waves share K, 64 values at a time, and add
-// their sums in LDS. Up to 16 MT rows of x ride along as the instruction's columns.
-constexpr int kThreads = 256;
-template <bool F16, int MT>
-__global__ __launch_bounds__(kThreads) void k_linear_rows(LinearCall a) {
-  constexpr int NW = kThreads / kWave;
-  __shared__ f32x4 red[NW][MT][kWave];
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const int r = lane & 15, g = lane >> 4;
-  const int64_t tile = a.tile0 + blockIdx.x, ntiles = ((int64_t)a.N + 15) / 16;
-  const int64_t n0 = tile % ntiles * 16, m0 = tile / ntiles * (16 * MT);
-  const uint16_t* w = a.w + min(n0 + r, (int64_t)a.N - 1) * a.w_stride;
-  const uint16_t* x[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) x[i] = a.x + min(m0 + 16 * i + r, (int64_t)a.M - 1) * a.x_stride;
-  f32x4 acc[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-  for (int k0 = 64 * wave; k0 < a.K; k0 += 64 * NW) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int k = k0 + 32 * u + 8 * g;
-      const bool in = k < a.K;
-      const u32x4 zero = {0, 0, 0, 0};
-      const u32x4 wf = in ? *(const u32x4*)(w + k) : zero;
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const u32x4 xf = in ? *(const u32x4*)(x[i] + k) : zero;
-        acc[i] = mma16<F16>(wf, xf, acc[i]);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < MT; ++i) red[wave][i][lane] = acc[i];
-  __syncthreads();
-  // lane: rows n0 + 4 g .. + 3 of w, row m0 + 16 i + r of x
-  for (int i = wave; i < MT; i += NW) {
-    f32x4 v = red[0][i][lane];
-#pragma unroll
-    for (int q = 1; q < NW; ++q) v += red[q][i][lane];
-    const int64_t m = m0 + 16 * i + r;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (m < a.M && n0 + 4 * g + e < a.N) finish(a, m, n0 + 4 * g + e, v[e]);
-  }
-}
-
 // Four neighbouring outputs of row m, n on: whole vectors where the caller's rows allow it.
 __device__ __forceinline__ void finish4(const LinearCall& a, int64_t m, int64_t n, f32x4 v) {
   if (!a.vec4 || n + 4 > a.N) {
@@ -144,6 +96,64 @@ __device__ __forceinline__ void finish4(const LinearCall& a, int64_t m, int64_t 
   }
 }
 
+// Few rows: the weights' bytes bound it. One workgroup 16 rows of w; its NW waves share K, 64 values
+// (a cache line of each row) at a time, with kAhead such loads of w under way each, and add their sums
+// in LDS, in order. Up to 16 MT rows of x ride along as the instruction's columns.
+constexpr int kAhead = 4;
+template <bool F16, int MT, int NW>
+__global__ __launch_bounds__(NW * kWave) void k_linear_rows(LinearCall a) {
+  __shared__ f32x4 red[NW][MT][kWave];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int r = lane & 15, g = lane >> 4;
+  const int64_t tile = a.tile0 + blockIdx.x, ntiles = ((int64_t)a.N + 15) / 16;
+  const int64_t n0 = tile % ntiles * 16, m0 = tile / ntiles * (16 * MT);
+  const uint16_t* w = a.w + min(n0 + r, (int64_t)a.N - 1) * a.w_stride + 8 * g;
+  const uint16_t* x[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+    x[i] = a.x + min(m0 + 16 * i + r, (int64_t)a.M - 1) * a.x_stride + 8 * g;
+  f32x4 acc[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int whole = a.K / 64;
+  int c = wave;
+  for (; c + (kAhead - 1) * NW < whole; c += kAhead * NW) {
+    u32x4 wf[2 * kAhead];
+#pragma unroll
+    for (int u = 0; u < 2 * kAhead; ++u)
+      wf[u] = *(const u32x4*)(w + 64 * (c + u / 2 * NW) + 32 * (u & 1));
+#pragma unroll
+    for (int u = 0; u < 2 * kAhead; ++u)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        acc[i] = mma16<F16>(wf[u], *(const u32x4*)(x[i] + 64 * (c + u / 2 * NW) + 32 * (u & 1)), acc[i]);
+  }
+  for (; 64 * c < a.K; c += NW) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int k = 64 * c + 32 * u;
+      const bool in = k + 8 * g < a.K;   // behind K: zeros
+      const u32x4 zero = {0, 0, 0, 0};
+      const u32x4 wf = in ? *(const u32x4*)(w + k) : zero;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        acc[i] = mma16<F16>(wf, in ? *(const u32x4*)(x[i] + k) : zero, acc[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) red[wave][i][lane] = acc[i];
+  __syncthreads();
+  // lane: rows n0 + 4 g .. + 3 of w, row m0 + 16 i + r of x
+  for (int i = wave; i < MT; i += NW) {
+    f32x4 v = red[0][i][lane];
+#pragma unroll
+    for (int q = 1; q < NW; ++q) v += red[q][i][lane];
+    const int64_t m = m0 + 16 * i + r;
+    if (m < a.M && n0 + 4 * g < a.N) finish4(a, m, n0 + 4 * g, v);
+  }
+}
+
 typedef __attribute__((address_space(3))) void* lds_ptr;
 typedef __attribute__((address_space(1))) const void* global_ptr;
 
@@ -152,6 +162,19 @@ typedef __attribute__((address_space(1))) const void* global_ptr;
 template <int N>
 __device__ __forceinline__ void meet() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// The workgroup's tile: an eighth of them to each XCD (workgroups go round the XCDs), and there 8
+// tiles of rows of x side by side, column by column.
+template <int BM, int BN>
+__device__ __forceinline__ void find_tile(const LinearCall& a, int64_t* m0, int64_t* n0) {
+  const int64_t tm = ((int64_t)a.M + BM - 1) / BM, tn = ((int64_t)a.N + BN - 1) / BN;
+  int64_t id = a.tile0 + blockIdx.x;
+  const int64_t all = tm * tn, per = (all + 7) / 8, x = id % 8, full = all - 8 * (per - 1);
+  id = id / 8 + (x < full ? x * per : full * per + (x - full) * (per - 1));
+  const int64_t band = id / (8 * tn), left = id % (8 * tn), high = min(tm - 8 * band, (int64_t)8);
+  *m0 = (8 * band + left % high) * BM;
+  *n0 = left / high * BN;
 }
 
 // Many rows: the matrix instructions bound it. A workgroup of WM x WN waves makes a tile of BM rows
@@ -170,15 +193,8 @@ __global__ __launch_bounds__(WM * WN * kWave) void k_linear_tile(LinearCall a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int r = lane & 15, g = lane >> 4;
 
-  // an eighth of the tiles to each XCD (workgroups go round them), 8 tiles of M by N at a time
-  const int64_t tm = ((int64_t)a.M + BM - 1) / BM, tn = ((int64_t)a.N + BN - 1) / BN;
-  int64_t id = a.tile0 + blockIdx.x;
-  {
-    const int64_t all = tm * tn, per = (all + 7) / 8, x = id % 8, full = all - 8 * (per - 1);
-    id = id / 8 + (x < full ? x * per : full * per + (x - full) * (per - 1));
-  }
-  const int64_t band = id / (8 * tn), left = id % (8 * tn), high = min(tm - 8 * band, (int64_t)8);
-  const int64_t m0 = (8 * band + left % high) * BM, n0 = left / high * BN;
+  int64_t m0, n0;
+  find_tile<BM, BN>(a, &m0, &n0);
 
   // this wave's rows to load, 8 at a time: lane -> row lane / 8, piece (lane % 8) ^ row
   const int piece = (lane & 7) ^ (lane >> 3);
@@ -255,6 +271,120 @@ __global__ __launch_bounds__(WM * WN * kWave) void k_linear_tile(LinearCall a) {
   }
 }
 
+// The largest products: 256 x 256 tiles of eight waves in two groups that take turns, one at the
+// matrix pipes while the other reads its next operands from LDS. A barrier ends each turn; the
+// second group is one turn behind. A step's 64 values of K are two turns of products of each group.
+//   turn        4c          4c + 1      4c + 2      4c + 3      4c + 4
+//   group 0     read c, 0   products    read c, 1   products    read c + 1, 0
+//   group 1     products    read c, 0   products    read c, 1   products
+// Step c + 1 is loaded, over step c - 1, from turn 4c on, when all have read that, and is there by
+// the end of turn 4c + 3.
+template <bool F16>
+__global__ __launch_bounds__(512) void k_linear_turns(LinearCall a) {
+  constexpr int BM = 256, BN = 256, BK = 64, TM = 8, TN = 4, NW = 8, L = 4;
+  constexpr int kStage = (BM + BN) * BK * 2;
+  __shared__ __align__(16) uint8_t lds[2 * kStage];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int r = lane & 15, g = lane >> 4;
+  int64_t m0, n0;
+  find_tile<BM, BN>(a, &m0, &n0);
+  const int piece = (lane & 7) ^ (lane >> 3);
+  const uint16_t* src[2 * L];
+#pragma unroll
+  for (int i = 0; i < 2 * L; ++i) {
+    const int row = 8 * ((i < L ? i : i - L) * NW + wave) + (lane >> 3);
+    src[i] = (i < L ? a.x + min(m0 + row, (int64_t)a.M - 1) * a.x_stride
+                    : a.w + min(n0 + row, (int64_t)a.N - 1) * a.w_stride) + 8 * piece;
+  }
+  auto place = [&](int stage, int i) {
+    return lds + stage * kStage + (i < L ? 0 : BM * BK * 2) + ((i < L ? i : i - L) * NW + wave) * 1024;
+  };
+  auto load = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < 2 * L; ++i)
+      __builtin_amdgcn_global_load_lds((global_ptr)(src[i] + (int64_t)c * BK), (lds_ptr)place(c & 1, i),
+                                       16, 0, 0);
+  };
+  f32x4 acc[TN][TM];
+#pragma unroll
+  for (int i = 0; i < TN; ++i)
+#pragma unroll
+    for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int group = wave >> 2, wn = wave & 3;   // a group is a half of the tile's rows of x
+  const int at0 = r * BK * 2 + ((g ^ (r & 7)) * 16), at1 = r * BK * 2 + (((4 + g) ^ (r & 7)) * 16);
+  u32x4 xf[TM], wf[TN];
+  auto read = [&](int stage, int at) {
+    const uint8_t* xs = lds + stage * kStage + group * (BM / 2) * BK * 2 + at;
+    const uint8_t* ws = lds + stage * kStage + (BM + wn * (BN / 4)) * BK * 2 + at;
+#pragma unroll
+    for (int i = 0; i < TN; ++i) wf[i] = *(const u32x4*)(ws + i * 16 * BK * 2);
+#pragma unroll
+    for (int j = 0; j < TM; ++j) xf[j] = *(const u32x4*)(xs + j * 16 * BK * 2);
+  };
+  auto products = [&] {
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int j = 0; j < TM; ++j)
+#pragma unroll
+      for (int i = 0; i < TN; ++i) acc[i][j] = mma16<F16>(wf[i], xf[j], acc[i][j]);
+    __builtin_amdgcn_s_setprio(0);
+  };
+  auto turn = [] {   // ends one; what was read from LDS is there
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto turn_landed = [] {   // and this wave's loads into LDS, too
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const int steps = a.K / BK;
+  if (steps > 0) {
+    load(0);
+    turn_landed();
+    if (group == 1) turn();
+    for (int c = 0; c < steps; ++c) {
+      read(c & 1, at0);
+      if (c + 1 < steps) load(c + 1);
+      turn();
+      products();
+      turn();
+      read(c & 1, at1);
+      if (group == 1) turn_landed();
+      else turn();
+      products();
+      if (group == 0) turn_landed();
+      else turn();
+    }
+    if (group == 0) turn();
+  }
+  if (steps * BK < a.K) {   // the rest of K, with zeros behind it
+    turn();
+#pragma unroll
+    for (int i = 0; i < 2 * L; ++i) {
+      u32x4 v = {0, 0, 0, 0};
+      if (steps * BK + 8 * piece < a.K) v = *(const u32x4*)(src[i] + (int64_t)steps * BK);
+      *(u32x4*)(place(0, i) + 16 * lane) = v;
+    }
+    turn();
+    read(0, at0);
+    products();
+    read(0, at1);
+    products();
+  }
+#pragma unroll
+  for (int j = 0; j < TM; ++j) {
+    const int64_t m = m0 + group * (BM / 2) + 16 * j + r;
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      const int64_t n = n0 + wn * (BN / 4) + 16 * i + 4 * g;
+      if (m < a.M && n < a.N) finish4(a, m, n, acc[i][j]);
+    }
+  }
+}
+
 constexpr int64_t kMaxTiles = 1 << 22;   // a launch holds fewer than 2^32 threads
 
 template <typename K>
@@ -282,12 +412,12 @@ hipError_t launch_t(LinearCall a, hipStream_t stream) {
   const int bytes = a.out_type == kFP32 ? 4 : 2;
   a.vec4 = ((uintptr_t)a.out & (4 * bytes - 1)) == 0 && a.out_stride % 4 == 0 &&
            (!a.resid || (((uintptr_t)a.resid & (4 * bytes - 1)) == 0 && a.resid_stride % 4 == 0));
-  if (a.M <= 16) return launch_tiles(a, n, k_linear_rows<F16, 1>, kThreads, stream);
-  if (a.M <= 32) return launch_tiles(a, n, k_linear_rows<F16, 2>, kThreads, stream);
-  if (a.M <= 64) return launch_tiles(a, n, k_linear_rows<F16, 4>, kThreads, stream);
+  if (a.M <= 16) return launch_tiles(a, n, k_linear_rows<F16, 1, 8>, 512, stream);
+  if (a.M <= 32) return launch_tiles(a, n, k_linear_rows<F16, 2, 8>, 512, stream);
+  if (a.M <= 64) return launch_tiles(a, n, k_linear_rows<F16, 4, 8>, 512, stream);
   auto tiles = [&](int64_t b) { return (a.M + b - 1) / b * ((a.N + b - 1) / b); };
-  if (tiles(256) >= 200) return launch_tile<F16, 256, 256, 2, 4, 2>(a, stream);
-  if (tiles(128) >= 200) return launch_tile<F16, 128, 128, 2, 2, 2>(a, stream);
+  if (tiles(256) >= 200) return launch_tiles(a, tiles(256), k_linear_turns<F16>, 512, stream);
+  if (tiles(128) >= 200) return launch_tile<F16, 128, 128, 2, 2, 4>(a, stream);
   return launch_tile<F16, 64, 64, 2, 2, 4>(a, stream);
 }
 
