@@ -154,6 +154,41 @@ __global__ __launch_bounds__(NW * kWave) void k_linear_rows(LinearCall a) {
   }
 }
 
+// A wave's 16 TM x 16 TN outputs: 32 rows at a time through LDS of its own, so that rows leave in
+// whole lines, and so that what is done to an output stands once in the code: unrolled over all
+// products of a tile it came to more than the instruction cache holds, and took as long as the tile.
+constexpr int kOutRows = 32;
+template <int TN> constexpr int kOutStride = 16 * TN + 4;
+template <int TM, int TN>
+__device__ __forceinline__ void store_tile(const LinearCall& a, const f32x4 (&acc)[TN][TM], float* out,
+                                           int64_t m0, int64_t n0) {
+  constexpr int ST = kOutStride<TN>, JR = kOutRows / 16;
+  const int lane = threadIdx.x & (kWave - 1), r = lane & 15, g = lane >> 4;
+#pragma unroll 1
+  for (int c = 0; c < TM / JR; ++c) {
+    if (m0 + kOutRows * c >= a.M) return;
+#pragma unroll
+    for (int q = 0; q < TM / JR; ++q)
+      if (q == c) {
+#pragma unroll
+        for (int j = 0; j < JR; ++j)
+#pragma unroll
+          for (int i = 0; i < TN; ++i)
+            *(f32x4*)(out + (16 * j + r) * ST + 16 * i + 4 * g) = acc[i][JR * q + j];
+      }
+    __builtin_amdgcn_wave_barrier();
+    constexpr int RL = kWave / (4 * TN);   // rows at once, of four values a lane
+    const int row = lane / (4 * TN), col = lane % (4 * TN) * 4;
+#pragma unroll 1
+    for (int k = 0; k < kOutRows; k += RL) {
+      const int64_t m = m0 + kOutRows * c + k + row;
+      const f32x4 v = *(const f32x4*)(out + (k + row) * ST + col);
+      if (m < a.M && n0 + col < a.N) finish4(a, m, n0 + col, v);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
 typedef __attribute__((address_space(3))) void* lds_ptr;
 typedef __attribute__((address_space(1))) const void* global_ptr;
 
@@ -188,6 +223,7 @@ __global__ __launch_bounds__(WM * WN * kWave) void k_linear_tile(LinearCall a) {
   constexpr int LM = BM / 8 / NW, LN = BN / 8 / NW;        // loads of 8 rows, of a wave and step
   static_assert(LM * 8 * NW == BM && LN * 8 * NW == BN, "rows share out among the waves");
   constexpr int kStage = (BM + BN) * BK * 2;
+  static_assert(NW * kOutRows * kOutStride<TN> * 4 <= S * kStage, "outputs fit");
   __shared__ __align__(16) uint8_t lds[S * kStage];
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -259,16 +295,9 @@ __global__ __launch_bounds__(WM * WN * kWave) void k_linear_tile(LinearCall a) {
     meet<0>();
     compute(0);
   }
-  // lane: row r of x, rows 4 g .. + 3 of w of each product
-#pragma unroll
-  for (int j = 0; j < TM; ++j) {
-    const int64_t m = m0 + wm * (BM / WM) + 16 * j + r;
-#pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      const int64_t n = n0 + wn * (BN / WN) + 16 * i + 4 * g;
-      if (m < a.M && n < a.N) finish4(a, m, n, acc[i][j]);
-    }
-  }
+  meet<0>();   // the operands' places are free
+  store_tile<TM, TN>(a, acc, (float*)lds + wave * kOutRows * kOutStride<TN>, m0 + wm * (BM / WM),
+                     n0 + wn * (BN / WN));
 }
 
 // The largest products: 256 x 256 tiles of eight waves in two groups that take turns, one at the
@@ -374,15 +403,9 @@ __global__ __launch_bounds__(512) void k_linear_turns(LinearCall a) {
     read(0, at1);
     products();
   }
-#pragma unroll
-  for (int j = 0; j < TM; ++j) {
-    const int64_t m = m0 + group * (BM / 2) + 16 * j + r;
-#pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      const int64_t n = n0 + wn * (BN / 4) + 16 * i + 4 * g;
-      if (m < a.M && n < a.N) finish4(a, m, n, acc[i][j]);
-    }
-  }
+  turn();   // the operands' places are free
+  store_tile<TM, TN>(a, acc, (float*)lds + wave * kOutRows * kOutStride<TN>, m0 + group * (BM / 2),
+                     n0 + wn * (BN / 4));
 }
 
 constexpr int64_t kMaxTiles = 1 << 22;   // a launch holds fewer than 2^32 threads
