@@ -192,6 +192,8 @@ __device__ __forceinline__ void store_tile(const LinearCall& a, const f32x4 (&ac
 typedef __attribute__((address_space(3))) void* lds_ptr;
 typedef __attribute__((address_space(1))) const void* global_ptr;
 
+__device__ __align__(16) const uint32_t g_zero[4] = {0, 0, 0, 0};   // read in place of what is behind K
+
 // The waves meet: their LDS accesses are done, and of their loads into LDS all but the newest N. A
 // fence would wait for all of them.
 template <int N>
@@ -212,43 +214,50 @@ __device__ __forceinline__ void find_tile(const LinearCall& a, int64_t* m0, int6
   *n0 = left / high * BN;
 }
 
-// Many rows: the matrix instructions bound it. A workgroup of WM x WN waves makes a tile of BM rows
-// of x and BN of w, 64 values of K a step. Steps land in LDS straight from memory, S - 1 of them
-// under way; a row's 16-byte pieces lie there in the order piece ^ (row % 8), so that the 16 rows
-// that an operand's lanes read fall on different banks.
-template <bool F16, int BM, int BN, int WM, int WN, int S>
-__global__ __launch_bounds__(WM * WN * kWave) void k_linear_tile(LinearCall a) {
-  constexpr int NW = WM * WN, BK = 64;
+// Many rows. A workgroup of KG groups of WM x WN waves makes a tile of BM rows of x and BN of w; each
+// group takes a part of K, BK values a step, and the groups' sums meet in LDS. Steps land in LDS straight
+// from memory, S - 1 of them under way. A row's 16-byte pieces lie there in the order piece ^ row (BK
+// 64) or piece ^ row / 4 (BK 32), so that eight neighbouring rows of a read fall on different banks.
+template <bool F16, int BM, int BN, int BK, int WM, int WN, int S, int KG>
+__global__ __launch_bounds__(WM * WN * KG * kWave) void k_linear_tile(LinearCall a) {
+  constexpr int NW = WM * WN, PR = BK / 8;                 // waves of a group; pieces of a row
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;      // 16 x 16 products of a wave
-  constexpr int LM = BM / 8 / NW, LN = BN / 8 / NW;        // loads of 8 rows, of a wave and step
-  static_assert(LM * 8 * NW == BM && LN * 8 * NW == BN, "rows share out among the waves");
+  constexpr int RL = kWave / PR;                           // rows of a load
+  constexpr int LM = BM / RL / NW, LN = BN / RL / NW;      // loads of a wave and step
+  static_assert(BK == 64 || BK == 32, "swizzle");
+  static_assert(LM * RL * NW == BM && LN * RL * NW == BN, "rows share out among the waves");
   constexpr int kStage = (BM + BN) * BK * 2;
-  static_assert(NW * kOutRows * kOutStride<TN> * 4 <= S * kStage, "outputs fit");
-  __shared__ __align__(16) uint8_t lds[S * kStage];
+  // the steps, then the other groups' sums, then outputs
+  constexpr int kSums = (KG - 1) * NW * TM * TN * 1024, kOut = NW * kOutRows * kOutStride<TN> * 4;
+  constexpr int kSteps = KG * S * kStage, kMost = kSums > kOut ? kSums : kOut;
+  __shared__ __align__(16) uint8_t lds[kSteps > kMost ? kSteps : kMost];
   const int lane = threadIdx.x & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int all = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int group = all / NW, wave = all % NW;
   const int r = lane & 15, g = lane >> 4;
-
   int64_t m0, n0;
   find_tile<BM, BN>(a, &m0, &n0);
 
-  // this wave's rows to load, 8 at a time: lane -> row lane / 8, piece (lane % 8) ^ row
-  const int piece = (lane & 7) ^ (lane >> 3);
+  // this wave's rows to load, RL at a time: the lane's row and piece
+  auto swizzle = [](int row) { return BK == 64 ? row & 7 : row >> 2 & 3; };
+  const int lrow = lane / PR, piece = (lane % PR) ^ swizzle(lrow);
+  const int steps = ((a.K + BK - 1) / BK + KG - 1) / KG, k0 = group * steps * BK + 8 * piece;
   const uint16_t* src[LM + LN];
 #pragma unroll
   for (int i = 0; i < LM + LN; ++i) {
-    const int row = 8 * ((i < LM ? i : i - LM) * NW + wave) + (lane >> 3);
+    const int row = RL * ((i < LM ? i : i - LM) * NW + wave) + lrow;
     src[i] = (i < LM ? a.x + min(m0 + row, (int64_t)a.M - 1) * a.x_stride
-                     : a.w + min(n0 + row, (int64_t)a.N - 1) * a.w_stride) + 8 * piece;
+                     : a.w + min(n0 + row, (int64_t)a.N - 1) * a.w_stride) + k0;
   }
-  auto place = [&](int stage, int i) {   // of load i's eight rows in LDS
-    return lds + stage * kStage + (i < LM ? 0 : BM * BK * 2) + ((i < LM ? i : i - LM) * NW + wave) * 1024;
-  };
-  auto load = [&](int c) {
+  uint8_t* const mine = lds + group * S * kStage;
+  auto load = [&](int c, int stage) {   // behind K: zeros
+    const bool in = k0 + c * BK < a.K;
 #pragma unroll
     for (int i = 0; i < LM + LN; ++i)
-      __builtin_amdgcn_global_load_lds((global_ptr)(src[i] + (int64_t)c * BK), (lds_ptr)place(c % S, i),
-                                       16, 0, 0);
+      __builtin_amdgcn_global_load_lds(
+          in ? (global_ptr)(src[i] + (int64_t)c * BK) : (global_ptr)g_zero,
+          (lds_ptr)(mine + stage * kStage + (i < LM ? 0 : BM * BK * 2) +
+                    ((i < LM ? i : i - LM) * NW + wave) * 1024), 16, 0, 0);
   };
   f32x4 acc[TN][TM];
 #pragma unroll
@@ -257,11 +266,11 @@ __global__ __launch_bounds__(WM * WN * kWave) void k_linear_tile(LinearCall a) {
     for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int wm = wave / WN, wn = wave % WN;
   auto compute = [&](int stage) {
-    const uint8_t* xs = lds + stage * kStage + wm * (BM / WM) * BK * 2;
-    const uint8_t* ws = lds + stage * kStage + (BM + wn * (BN / WN)) * BK * 2;
+    const uint8_t* xs = mine + stage * kStage + wm * (BM / WM) * BK * 2;
+    const uint8_t* ws = mine + stage * kStage + (BM + wn * (BN / WN)) * BK * 2;
 #pragma unroll
     for (int k = 0; k < BK / 32; ++k) {
-      const int at = r * BK * 2 + (((4 * k + g) ^ (r & 7)) * 16);
+      const int at = r * BK * 2 + (((4 * k + g) ^ swizzle(r)) * 16);
       u32x4 xf[TM], wf[TN];
 #pragma unroll
       for (int j = 0; j < TM; ++j) xf[j] = *(const u32x4*)(xs + j * 16 * BK * 2 + at);
@@ -273,29 +282,37 @@ __global__ __launch_bounds__(WM * WN * kWave) void k_linear_tile(LinearCall a) {
         for (int j = 0; j < TM; ++j) acc[i][j] = mma16<F16>(wf[i], xf[j], acc[i][j]);
     }
   };
-  const int steps = a.K / BK;   // whole ones
 #pragma unroll
-  for (int c = 0; c < S - 1; ++c)
-    if (c < steps) load(c);
+  for (int c = 0; c < S - 1; ++c) load(c, c);
+  int stage = 0, over = S - 1;   // of step c, and of step c - 1
   for (int c = 0; c < steps; ++c) {
-    // step c is there: of the loads under way only those of the S - 2 steps behind it are left
-    if (c + S - 1 <= steps) meet<(S - 2) * (LM + LN)>();
-    else meet<0>();
-    if (c + S - 1 < steps) load(c + S - 1);
-    compute(c % S);
-  }
-  if (steps * BK < a.K) {   // the rest of K, with zeros behind it
-    meet<0>();
-#pragma unroll
-    for (int i = 0; i < LM + LN; ++i) {
-      u32x4 v = {0, 0, 0, 0};
-      if (steps * BK + 8 * piece < a.K) v = *(const u32x4*)(src[i] + (int64_t)steps * BK);
-      *(u32x4*)(place(0, i) + 16 * lane) = v;
-    }
-    meet<0>();
-    compute(0);
+    meet<(S - 2) * (LM + LN)>();   // step c is there; the loads of the S - 2 steps behind it may not be
+    load(c + S - 1, over);
+    compute(stage);
+    over = stage;
+    stage = stage + 1 == S ? 0 : stage + 1;
   }
   meet<0>();   // the operands' places are free
+  if constexpr (KG > 1) {
+    f32x4* sums = (f32x4*)lds + wave * TM * TN * kWave + lane;
+    if (group > 0) {
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int j = 0; j < TM; ++j) sums[((group - 1) * NW * TM * TN + i * TM + j) * kWave] = acc[i][j];
+    }
+    meet<0>();
+    if (group > 0) return;
+#pragma unroll
+    for (int q = 0; q < KG - 1; ++q)
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int j = 0; j < TM; ++j) acc[i][j] += sums[(q * NW * TM * TN + i * TM + j) * kWave];
+    // a wave's outputs go where another's sums may still be read: not before it has them
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+  }
   store_tile<TM, TN>(a, acc, (float*)lds + wave * kOutRows * kOutStride<TN>, m0 + wm * (BM / WM),
                      n0 + wn * (BN / WN));
 }
@@ -329,11 +346,13 @@ __global__ __launch_bounds__(512) void k_linear_turns(LinearCall a) {
   auto place = [&](int stage, int i) {
     return lds + stage * kStage + (i < L ? 0 : BM * BK * 2) + ((i < L ? i : i - L) * NW + wave) * 1024;
   };
+  const int steps = (a.K + BK - 1) / BK;
   auto load = [&](int c) {
+    const bool in = c * BK + 8 * piece < a.K;
 #pragma unroll
     for (int i = 0; i < 2 * L; ++i)
-      __builtin_amdgcn_global_load_lds((global_ptr)(src[i] + (int64_t)c * BK), (lds_ptr)place(c & 1, i),
-                                       16, 0, 0);
+      __builtin_amdgcn_global_load_lds(in ? (global_ptr)(src[i] + (int64_t)c * BK) : (global_ptr)g_zero,
+                                       (lds_ptr)place(c & 1, i), 16, 0, 0);
   };
   f32x4 acc[TN][TM];
 #pragma unroll
@@ -369,7 +388,6 @@ __global__ __launch_bounds__(512) void k_linear_turns(LinearCall a) {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
   };
-  const int steps = a.K / BK;
   if (steps > 0) {
     load(0);
     turn_landed();
@@ -388,20 +406,6 @@ __global__ __launch_bounds__(512) void k_linear_turns(LinearCall a) {
       else turn();
     }
     if (group == 0) turn();
-  }
-  if (steps * BK < a.K) {   // the rest of K, with zeros behind it
-    turn();
-#pragma unroll
-    for (int i = 0; i < 2 * L; ++i) {
-      u32x4 v = {0, 0, 0, 0};
-      if (steps * BK + 8 * piece < a.K) v = *(const u32x4*)(src[i] + (int64_t)steps * BK);
-      *(u32x4*)(place(0, i) + 16 * lane) = v;
-    }
-    turn();
-    read(0, at0);
-    products();
-    read(0, at1);
-    products();
   }
   turn();   // the operands' places are free
   store_tile<TM, TN>(a, acc, (float*)lds + wave * kOutRows * kOutStride<TN>, m0 + group * (BM / 2),
@@ -423,10 +427,11 @@ hipError_t launch_tiles(LinearCall a, int64_t tiles, K kernel, int threads,
   return hipSuccess;
 }
 
-template <bool F16, int BM, int BN, int WM, int WN, int S>
+template <bool F16, int BM, int BN, int BK, int WM, int WN, int S, int KG>
 hipError_t launch_tile(const LinearCall& a, hipStream_t stream) {
   const int64_t tiles = (((int64_t)a.M + BM - 1) / BM) * (((int64_t)a.N + BN - 1) / BN);
-  return launch_tiles(a, tiles, k_linear_tile<F16, BM, BN, WM, WN, S>, WM * WN * kWave, stream);
+  return launch_tiles(a, tiles, k_linear_tile<F16, BM, BN, BK, WM, WN, S, KG>, WM * WN * KG * kWave,
+                      stream);
 }
 
 template <bool F16>
@@ -440,8 +445,8 @@ hipError_t launch_t(LinearCall a, hipStream_t stream) {
   if (a.M <= 64) return launch_tiles(a, n, k_linear_rows<F16, 4, 8>, 512, stream);
   auto tiles = [&](int64_t b) { return (a.M + b - 1) / b * ((a.N + b - 1) / b); };
   if (tiles(256) >= 200) return launch_tiles(a, tiles(256), k_linear_turns<F16>, 512, stream);
-  if (tiles(128) >= 200) return launch_tile<F16, 128, 128, 2, 2, 4>(a, stream);
-  return launch_tile<F16, 64, 64, 2, 2, 4>(a, stream);
+  if (tiles(128) >= 200) return launch_tile<F16, 128, 128, 64, 2, 2, 2, 1>(a, stream);
+  return launch_tile<F16, 64, 64, 64, 2, 2, 4, 1>(a, stream);
 }
 
 }  // namespace
