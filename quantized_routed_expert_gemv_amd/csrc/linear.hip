@@ -1,4 +1,6 @@
 // Dense products: out = resid + act(x w^T + bias), x [M][K], w [N][K], 16-bit operands, fp32 sums.
+// Few rows are bound by w's bytes, many by the matrix instructions. One kernel, whose tile, steps under
+// way and groups follow the sizes.
 #include <type_traits>
 
 #include "common.hpp"
@@ -96,64 +98,6 @@ __device__ __forceinline__ void finish4(const LinearCall& a, int64_t m, int64_t 
   }
 }
 
-// Few rows: the weights' bytes bound it. One workgroup 16 rows of w; its NW waves share K, 64 values
-// (a cache line of each row) at a time, with kAhead such loads of w under way each, and add their sums
-// in LDS, in order. Up to 16 MT rows of x ride along as the instruction's columns.
-constexpr int kAhead = 4;
-template <bool F16, int MT, int NW>
-__global__ __launch_bounds__(NW * kWave) void k_linear_rows(LinearCall a) {
-  __shared__ f32x4 red[NW][MT][kWave];
-  const int lane = threadIdx.x & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int r = lane & 15, g = lane >> 4;
-  const int64_t tile = a.tile0 + blockIdx.x, ntiles = ((int64_t)a.N + 15) / 16;
-  const int64_t n0 = tile % ntiles * 16, m0 = tile / ntiles * (16 * MT);
-  const uint16_t* w = a.w + min(n0 + r, (int64_t)a.N - 1) * a.w_stride + 8 * g;
-  const uint16_t* x[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-    x[i] = a.x + min(m0 + 16 * i + r, (int64_t)a.M - 1) * a.x_stride + 8 * g;
-  f32x4 acc[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int whole = a.K / 64;
-  int c = wave;
-  for (; c + (kAhead - 1) * NW < whole; c += kAhead * NW) {
-    u32x4 wf[2 * kAhead];
-#pragma unroll
-    for (int u = 0; u < 2 * kAhead; ++u)
-      wf[u] = *(const u32x4*)(w + 64 * (c + u / 2 * NW) + 32 * (u & 1));
-#pragma unroll
-    for (int u = 0; u < 2 * kAhead; ++u)
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-        acc[i] = mma16<F16>(wf[u], *(const u32x4*)(x[i] + 64 * (c + u / 2 * NW) + 32 * (u & 1)), acc[i]);
-  }
-  for (; 64 * c < a.K; c += NW) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int k = 64 * c + 32 * u;
-      const bool in = k + 8 * g < a.K;   // behind K: zeros
-      const u32x4 zero = {0, 0, 0, 0};
-      const u32x4 wf = in ? *(const u32x4*)(w + k) : zero;
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-        acc[i] = mma16<F16>(wf, in ? *(const u32x4*)(x[i] + k) : zero, acc[i]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < MT; ++i) red[wave][i][lane] = acc[i];
-  __syncthreads();
-  // lane: rows n0 + 4 g .. + 3 of w, row m0 + 16 i + r of x
-  for (int i = wave; i < MT; i += NW) {
-    f32x4 v = red[0][i][lane];
-#pragma unroll
-    for (int q = 1; q < NW; ++q) v += red[q][i][lane];
-    const int64_t m = m0 + 16 * i + r;
-    if (m < a.M && n0 + 4 * g < a.N) finish4(a, m, n0 + 4 * g, v);
-  }
-}
-
 // A wave's 16 TM x 16 TN outputs: 32 rows at a time through LDS of its own, so that rows leave in
 // whole lines, and so that what is done to an output stands once in the code: unrolled over all
 // products of a tile it came to more than the instruction cache holds, and took as long as the tile.
@@ -162,11 +106,11 @@ template <int TN> constexpr int kOutStride = 16 * TN + 4;
 template <int TM, int TN>
 __device__ __forceinline__ void store_tile(const LinearCall& a, const f32x4 (&acc)[TN][TM], float* out,
                                            int64_t m0, int64_t n0) {
-  constexpr int ST = kOutStride<TN>, JR = kOutRows / 16;
+  constexpr int ST = kOutStride<TN>, JR = TM < 2 ? TM : kOutRows / 16, OR = 16 * JR;
   const int lane = threadIdx.x & (kWave - 1), r = lane & 15, g = lane >> 4;
 #pragma unroll 1
   for (int c = 0; c < TM / JR; ++c) {
-    if (m0 + kOutRows * c >= a.M) return;
+    if (m0 + OR * c >= a.M) return;
 #pragma unroll
     for (int q = 0; q < TM / JR; ++q)
       if (q == c) {
@@ -180,8 +124,8 @@ __device__ __forceinline__ void store_tile(const LinearCall& a, const f32x4 (&ac
     constexpr int RL = kWave / (4 * TN);   // rows at once, of four values a lane
     const int row = lane / (4 * TN), col = lane % (4 * TN) * 4;
 #pragma unroll 1
-    for (int k = 0; k < kOutRows; k += RL) {
-      const int64_t m = m0 + kOutRows * c + k + row;
+    for (int k = 0; k < OR; k += RL) {
+      const int64_t m = m0 + OR * c + k + row;
       const f32x4 v = *(const f32x4*)(out + (k + row) * ST + col);
       if (m < a.M && n0 + col < a.N) finish4(a, m, n0 + col, v);
     }
@@ -317,101 +261,6 @@ __global__ __launch_bounds__(WM * WN * KG * kWave) void k_linear_tile(LinearCall
                      n0 + wn * (BN / WN));
 }
 
-// The largest products: 256 x 256 tiles of eight waves in two groups that take turns, one at the
-// matrix pipes while the other reads its next operands from LDS. A barrier ends each turn; the
-// second group is one turn behind. A step's 64 values of K are two turns of products of each group.
-//   turn        4c          4c + 1      4c + 2      4c + 3      4c + 4
-//   group 0     read c, 0   products    read c, 1   products    read c + 1, 0
-//   group 1     products    read c, 0   products    read c, 1   products
-// Step c + 1 is loaded, over step c - 1, from turn 4c on, when all have read that, and is there by
-// the end of turn 4c + 3.
-template <bool F16>
-__global__ __launch_bounds__(512) void k_linear_turns(LinearCall a) {
-  constexpr int BM = 256, BN = 256, BK = 64, TM = 8, TN = 4, NW = 8, L = 4;
-  constexpr int kStage = (BM + BN) * BK * 2;
-  __shared__ __align__(16) uint8_t lds[2 * kStage];
-  const int lane = threadIdx.x & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int r = lane & 15, g = lane >> 4;
-  int64_t m0, n0;
-  find_tile<BM, BN>(a, &m0, &n0);
-  const int piece = (lane & 7) ^ (lane >> 3);
-  const uint16_t* src[2 * L];
-#pragma unroll
-  for (int i = 0; i < 2 * L; ++i) {
-    const int row = 8 * ((i < L ? i : i - L) * NW + wave) + (lane >> 3);
-    src[i] = (i < L ? a.x + min(m0 + row, (int64_t)a.M - 1) * a.x_stride
-                    : a.w + min(n0 + row, (int64_t)a.N - 1) * a.w_stride) + 8 * piece;
-  }
-  auto place = [&](int stage, int i) {
-    return lds + stage * kStage + (i < L ? 0 : BM * BK * 2) + ((i < L ? i : i - L) * NW + wave) * 1024;
-  };
-  const int steps = (a.K + BK - 1) / BK;
-  auto load = [&](int c) {
-    const bool in = c * BK + 8 * piece < a.K;
-#pragma unroll
-    for (int i = 0; i < 2 * L; ++i)
-      __builtin_amdgcn_global_load_lds(in ? (global_ptr)(src[i] + (int64_t)c * BK) : (global_ptr)g_zero,
-                                       (lds_ptr)place(c & 1, i), 16, 0, 0);
-  };
-  f32x4 acc[TN][TM];
-#pragma unroll
-  for (int i = 0; i < TN; ++i)
-#pragma unroll
-    for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int group = wave >> 2, wn = wave & 3;   // a group is a half of the tile's rows of x
-  const int at0 = r * BK * 2 + ((g ^ (r & 7)) * 16), at1 = r * BK * 2 + (((4 + g) ^ (r & 7)) * 16);
-  u32x4 xf[TM], wf[TN];
-  auto read = [&](int stage, int at) {
-    const uint8_t* xs = lds + stage * kStage + group * (BM / 2) * BK * 2 + at;
-    const uint8_t* ws = lds + stage * kStage + (BM + wn * (BN / 4)) * BK * 2 + at;
-#pragma unroll
-    for (int i = 0; i < TN; ++i) wf[i] = *(const u32x4*)(ws + i * 16 * BK * 2);
-#pragma unroll
-    for (int j = 0; j < TM; ++j) xf[j] = *(const u32x4*)(xs + j * 16 * BK * 2);
-  };
-  auto products = [&] {
-    __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-    for (int j = 0; j < TM; ++j)
-#pragma unroll
-      for (int i = 0; i < TN; ++i) acc[i][j] = mma16<F16>(wf[i], xf[j], acc[i][j]);
-    __builtin_amdgcn_s_setprio(0);
-  };
-  auto turn = [] {   // ends one; what was read from LDS is there
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  auto turn_landed = [] {   // and this wave's loads into LDS, too
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  if (steps > 0) {
-    load(0);
-    turn_landed();
-    if (group == 1) turn();
-    for (int c = 0; c < steps; ++c) {
-      read(c & 1, at0);
-      if (c + 1 < steps) load(c + 1);
-      turn();
-      products();
-      turn();
-      read(c & 1, at1);
-      if (group == 1) turn_landed();
-      else turn();
-      products();
-      if (group == 0) turn_landed();
-      else turn();
-    }
-    if (group == 0) turn();
-  }
-  turn();   // the operands' places are free
-  store_tile<TM, TN>(a, acc, (float*)lds + wave * kOutRows * kOutStride<TN>, m0 + group * (BM / 2),
-                     n0 + wn * (BN / 4));
-}
-
 constexpr int64_t kMaxTiles = 1 << 22;   // a launch holds fewer than 2^32 threads
 
 template <typename K>
@@ -427,26 +276,33 @@ hipError_t launch_tiles(LinearCall a, int64_t tiles, K kernel, int threads,
   return hipSuccess;
 }
 
-template <bool F16, int BM, int BN, int BK, int WM, int WN, int S, int KG>
-hipError_t launch_tile(const LinearCall& a, hipStream_t stream) {
-  const int64_t tiles = (((int64_t)a.M + BM - 1) / BM) * (((int64_t)a.N + BN - 1) / BN);
-  return launch_tiles(a, tiles, k_linear_tile<F16, BM, BN, BK, WM, WN, S, KG>, WM * WN * KG * kWave,
-                      stream);
+int64_t tiles_of(const LinearCall& a, int bm, int bn) {
+  return (((int64_t)a.M + bm - 1) / bm) * (((int64_t)a.N + bn - 1) / bn);
 }
 
+template <bool F16, int BM, int BN, int BK, int WM, int WN, int S, int KG>
+hipError_t launch_tile(const LinearCall& a, hipStream_t stream) {
+  return launch_tiles(a, tiles_of(a, BM, BN), k_linear_tile<F16, BM, BN, BK, WM, WN, S, KG>,
+                      WM * WN * KG * kWave, stream);
+}
+
+// The smallest tile of which every CU has one at most, with as many groups and steps under way as LDS
+// holds: such products are bound by the bytes' way to the CUs. Of larger products, tiles of 128 x 256,
+// two on a CU, once they fill three fifths of their places.
 template <bool F16>
 hipError_t launch_t(LinearCall a, hipStream_t stream) {
-  const int64_t n = ((int64_t)a.N + 15) / 16;
   const int bytes = a.out_type == kFP32 ? 4 : 2;
   a.vec4 = ((uintptr_t)a.out & (4 * bytes - 1)) == 0 && a.out_stride % 4 == 0 &&
            (!a.resid || (((uintptr_t)a.resid & (4 * bytes - 1)) == 0 && a.resid_stride % 4 == 0));
-  if (a.M <= 16) return launch_tiles(a, n, k_linear_rows<F16, 1, 8>, 512, stream);
-  if (a.M <= 32) return launch_tiles(a, n, k_linear_rows<F16, 2, 8>, 512, stream);
-  if (a.M <= 64) return launch_tiles(a, n, k_linear_rows<F16, 4, 8>, 512, stream);
-  auto tiles = [&](int64_t b) { return (a.M + b - 1) / b * ((a.N + b - 1) / b); };
-  if (tiles(256) >= 200) return launch_tiles(a, tiles(256), k_linear_turns<F16>, 512, stream);
-  if (tiles(128) >= 200) return launch_tile<F16, 128, 128, 64, 2, 2, 2, 1>(a, stream);
-  return launch_tile<F16, 64, 64, 64, 2, 2, 4, 1>(a, stream);
+  auto one_each = [&](int bm, int bn) { return tiles_of(a, bm, bn) <= 256; };
+  if (one_each(16, 16)) return launch_tile<F16, 16, 16, 64, 1, 1, 4, 8>(a, stream);
+  if (one_each(16, 32)) return launch_tile<F16, 16, 32, 64, 1, 2, 4, 4>(a, stream);
+  if (a.M <= 16) return launch_tile<F16, 16, 64, 64, 1, 2, 4, 4>(a, stream);
+  if (one_each(32, 32)) return launch_tile<F16, 32, 32, 64, 2, 2, 4, 4>(a, stream);
+  if (one_each(64, 32)) return launch_tile<F16, 64, 32, 64, 2, 2, 4, 2>(a, stream);
+  if (one_each(64, 64)) return launch_tile<F16, 64, 64, 64, 2, 2, 4, 2>(a, stream);
+  if (tiles_of(a, 128, 256) < 320) return launch_tile<F16, 64, 64, 64, 2, 2, 3, 1>(a, stream);
+  return launch_tile<F16, 128, 256, 32, 2, 4, 3, 1>(a, stream);
 }
 
 }  // namespace
