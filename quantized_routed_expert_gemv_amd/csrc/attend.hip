@@ -892,17 +892,29 @@ __global__ __launch_bounds__(kRowThreads) void k_attend_join(AttendCall a) {
   __shared__ float weight[kMaxSplits];
   __shared__ f32x4 sums[NW][kWave];
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const int64_t row = a.block0 + blockIdx.x;
-  const int64_t token = row / a.n_q_heads;
-  if (token < first_row(a.batch, 0) || token >= first_row(a.batch, a.batch.n_seq)) return;
-  int splits = a.few ? a.splits_few : a.splits;
-  if (a.both) {
-    const int seq = wave_find(a.batch.n_seq, token, [&](int i) { return first_row(a.batch, i); });
-    const int64_t n = first_row(a.batch, seq + 1) - first_row(a.batch, seq);
-    splits = n * a.group <= kFewRows ? a.splits_few : a.splits;
-    if (splits == 1) return;   // written already
+  int64_t id = a.block0 + blockIdx.x, token;
+  int splits = a.few ? a.splits_few : a.splits, head;
+  if (a.both && a.splits == 1) {   // of the sequences with few rows alone: row r of one and a KV head
+    const int r = (int)(id % kFewRows);
+    id /= kFewRows;
+    const int kv = (int)(id % a.cache.n_heads), seq = (int)(id / a.cache.n_heads);
+    const int lo = first_row(a.batch, seq), n = first_row(a.batch, seq + 1) - lo;
+    if (n <= 0 || (int64_t)n * a.group > kFewRows || r >= n * a.group) return;
+    token = lo + r / a.group;
+    head = kv * a.group + r % a.group;
+    splits = a.splits_few;
+  } else {
+    token = id / a.n_q_heads;
+    head = (int)(id - token * a.n_q_heads);
+    if (token < first_row(a.batch, 0) || token >= first_row(a.batch, a.batch.n_seq)) return;
+    if (a.both) {
+      const int seq = wave_find(a.batch.n_seq, token, [&](int i) { return first_row(a.batch, i); });
+      const int64_t n = first_row(a.batch, seq + 1) - first_row(a.batch, seq);
+      splits = n * a.group <= kFewRows ? a.splits_few : a.splits;
+      if (splits == 1) return;   // written already
+    }
   }
-  const int head = (int)(row - token * a.n_q_heads);
+  const int64_t row = token * a.n_q_heads + head;
   const int64_t all = (int64_t)a.batch.T * a.n_q_heads;
   typedef float f32x2 __attribute__((__vector_size__(8)));
   f32x2 st[kMaxSplits / kWave];
@@ -990,7 +1002,9 @@ hipError_t launch_depth(AttendCall a, hipStream_t stream) {
   }
   const bool join = (tiles && a.splits > 1) || (rows && a.splits_few > 1);
   if (!join || e != hipSuccess) return e;
-  return launch_blocks(a, (int64_t)a.batch.T * a.n_q_heads, k_attend_join<F16>, kRowThreads, stream);
+  const int64_t n = a.both && a.splits == 1 ? (int64_t)a.batch.n_seq * a.cache.n_heads * kFewRows
+                                           : (int64_t)a.batch.T * a.n_q_heads;
+  return launch_blocks(a, n, k_attend_join<F16>, kRowThreads, stream);
 }
 
 template <bool F16, bool FP8>

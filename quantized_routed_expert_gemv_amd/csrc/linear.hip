@@ -286,9 +286,13 @@ hipError_t launch_tile(const LinearCall& a, hipStream_t stream) {
                       WM * WN * KG * kWave, stream);
 }
 
-// The smallest tile of which every CU has one at most, with as many groups and steps under way as LDS
-// holds: such products are bound by the bytes' way to the CUs. Of larger products, tiles of 128 x 256,
-// two on a CU, once they fill three fifths of their places.
+// The tile, by how many there are of it. Up to 256: the smallest of which every CU has one at most, with
+// as many groups and steps under way as LDS holds, for such products are bound by the bytes' way to the
+// CUs (16 x 5120 x 2880, us: 16 x 32 tiles 7.3, 32 x 32 8.0, 64 x 32 10.9, 64 x 64 13.5; 64 rows: 32 x 32
+// 14.0, 64 x 32 11.6, 64 x 64 14.8). Then 64 x 64 in two groups, two workgroups a CU (333 x 2880 x 4096:
+// 26.7 against 29.4 for three of one group; 512 x 5120 x 2880: 40.7 against 31.8), in one group, 128 x 128
+// (2048 x 5120 x 2880: 83 against 100, and 87 for 128 x 256), and 128 x 256 once they fill one and a half
+// rounds of two a CU (16384 x 5120 x 2880: 485 against 521; 256 x 256, one a CU: 511).
 template <bool F16>
 hipError_t launch_t(LinearCall a, hipStream_t stream) {
   const int bytes = a.out_type == kFP32 ? 4 : 2;
@@ -301,7 +305,9 @@ hipError_t launch_t(LinearCall a, hipStream_t stream) {
   if (one_each(32, 32)) return launch_tile<F16, 32, 32, 64, 2, 2, 4, 4>(a, stream);
   if (one_each(64, 32)) return launch_tile<F16, 64, 32, 64, 2, 2, 4, 2>(a, stream);
   if (one_each(64, 64)) return launch_tile<F16, 64, 64, 64, 2, 2, 4, 2>(a, stream);
-  if (tiles_of(a, 128, 256) < 320) return launch_tile<F16, 64, 64, 64, 2, 2, 3, 1>(a, stream);
+  if (tiles_of(a, 64, 64) <= 400) return launch_tile<F16, 64, 64, 64, 2, 2, 2, 2>(a, stream);
+  if (tiles_of(a, 128, 128) < 300) return launch_tile<F16, 64, 64, 64, 2, 2, 3, 1>(a, stream);
+  if (tiles_of(a, 128, 256) < 768) return launch_tile<F16, 128, 128, 64, 2, 2, 2, 1>(a, stream);
   return launch_tile<F16, 128, 256, 32, 2, 4, 3, 1>(a, stream);
 }
 

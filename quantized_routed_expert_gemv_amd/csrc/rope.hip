@@ -13,7 +13,6 @@ namespace moe {
 
 namespace {
 
-constexpr int kTokens = 4;       // tokens a workgroup
 constexpr int kThreads = 256;
 
 template <int N> struct Vals { float v[N]; };
@@ -160,10 +159,12 @@ __device__ __forceinline__ void unit(const T* x, int u, int type, const RopeView
   }
 }
 
-// kTokens tokens a workgroup; T is the rows' element (uint16_t or float), V the values a thread
-// moves at once: 8, or 1 where sizes, strides or addresses are not of 16 bytes.
-template <typename T, int V>
+// TK tokens a workgroup; T is the rows' element (uint16_t or float), V the values a thread moves at
+// once: 8, or 1 where sizes, strides or addresses are not of 16 bytes. The units of a token's heads
+// are shared out among the workgroups of the grid's second dimension, each of which forms the angles.
+template <typename T, int V, int TK>
 __global__ __launch_bounds__(kThreads) void k_rope(RopeCall a) {
+  constexpr int kTokens = TK;
   extern __shared__ float cs[];   // [kTokens][2][dim / 2]
   const int64_t t0 = ((int64_t)a.block0 + blockIdx.x) * kTokens;
   const int nt = (int)min((int64_t)kTokens, a.T - t0);
@@ -176,10 +177,11 @@ __global__ __launch_bounds__(kThreads) void k_rope(RopeCall a) {
   }
   __syncthreads();
   const int per_head = units<V>(a.D, a.rope.dim), per_token = a.n_heads * per_head;
+  const int first = blockIdx.y * kThreads + threadIdx.x, stride = gridDim.y * kThreads;
   for (int t = 0; t < nt; ++t) {
     const T* x = (const T*)a.x.p + (t0 + t) * a.x.token;
     T* out = (T*)a.out.p + (t0 + t) * a.out.token;
-    for (int i = threadIdx.x; i < per_token; i += kThreads) {
+    for (int i = first; i < per_token; i += stride) {
       const int h = i / per_head;
       unit<V>(x + h * a.x.head, i - h * per_head, a.type, a.rope, cs + 2 * t * n,
               [&](int d, const Vals<V>& r) { store<V>(out + h * a.out.head + d, r, a.type); });
@@ -187,8 +189,9 @@ __global__ __launch_bounds__(kThreads) void k_rope(RopeCall a) {
   }
 }
 
-template <typename T, int V>
+template <typename T, int V, int TK>
 __global__ __launch_bounds__(kThreads) void k_append(AppendCall a) {
+  constexpr int kTokens = TK;
   extern __shared__ float cs[];   // [kTokens][2][dim / 2]
   __shared__ int64_t place[kTokens][2];   // of the token's row in the k and v planes; < 0: none
   __shared__ int turn_by[kTokens];
@@ -226,6 +229,7 @@ __global__ __launch_bounds__(kThreads) void k_append(AppendCall a) {
     angle(a.rope.freq[j], turn_by[t], a.rope.scale, &cs[2 * t * n + j], &cs[(2 * t + 1) * n + j]);
   }
   __syncthreads();
+  const int first = blockIdx.y * kThreads + threadIdx.x, stride = gridDim.y * kThreads;
   const int D = a.cache.D, Hkv = a.cache.n_heads;
   const int per_head = units<V>(D, a.rope.dim);
   const int n_q = a.q.p ? a.n_q_heads * per_head : 0, n_k = Hkv * per_head, n_v = Hkv * (D / V);
@@ -233,7 +237,7 @@ __global__ __launch_bounds__(kThreads) void k_append(AppendCall a) {
     const int64_t row = t0 + t;
     const int64_t kp = place[t][0], vp = place[t][1];
     const float* angles = cs + 2 * t * n;
-    for (int i = threadIdx.x; i < n_q + n_k + n_v; i += kThreads) {
+    for (int i = first; i < n_q + n_k + n_v; i += stride) {
       if (i < n_q) {
         const int h = i / per_head;
         T* out = (T*)a.q_out.p + row * a.q_out.token + h * a.q_out.head;
@@ -268,18 +272,37 @@ bool vector_rows(const HeadsView& h, int size) {
 // A launch holds fewer than 2^32 threads.
 constexpr int kMaxBlocks = 1 << 21;
 
+// `units`: of a token's heads. For up to 256 tokens latency is all: one a workgroup, and one unit a
+// thread as far as eight workgroups go (four tokens of 64 + 2 * 8 heads of 64: 10.0 us with four tokens
+// in one workgroup, one after the other). Else four a workgroup, whose angles fill its threads.
 template <typename Call, typename K>
-hipError_t launch_blocks(Call a, int64_t T, K kernel, hipStream_t stream) {
-  const int64_t blocks = (T + kTokens - 1) / kTokens;
-  const size_t lds = (size_t)kTokens * a.rope.dim * sizeof(float);
+hipError_t launch_blocks(Call a, int64_t T, int64_t units, K few, K many, hipStream_t stream) {
+  const bool small = T <= 256;
+  const int tokens = small ? 1 : 4;
+  const int64_t blocks = (T + tokens - 1) / tokens;
+  const unsigned across = small ? (unsigned)min((units + kThreads - 1) / kThreads, (int64_t)8) : 1u;
+  const size_t lds = (size_t)tokens * a.rope.dim * sizeof(float);
   for (int64_t b = 0; b < blocks; b += kMaxBlocks) {
     a.block0 = (int)b;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)min(blocks - b, (int64_t)kMaxBlocks)), dim3(kThreads),
-                       lds, stream, a);
+    hipLaunchKernelGGL(small ? few : many, dim3((unsigned)min(blocks - b, (int64_t)kMaxBlocks), across),
+                       dim3(kThreads), lds, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+template <typename T, int V>
+hipError_t launch_rope_t(const RopeCall& a, hipStream_t stream) {
+  const int64_t per_head = a.rope.dim / (2 * V) + (a.D - a.rope.dim) / V;
+  return launch_blocks(a, a.T, a.n_heads * per_head, k_rope<T, V, 1>, k_rope<T, V, 4>, stream);
+}
+template <typename T, int V>
+hipError_t launch_append_t(const AppendCall& a, hipStream_t stream) {
+  const int64_t per_head = a.rope.dim / (2 * V) + (a.cache.D - a.rope.dim) / V;
+  const int64_t heads = (a.q.p ? a.n_q_heads : 0) + a.cache.n_heads;
+  return launch_blocks(a, a.batch.T, heads * per_head + a.cache.n_heads * (a.cache.D / V),
+                       k_append<T, V, 1>, k_append<T, V, 4>, stream);
 }
 
 }  // namespace
@@ -289,8 +312,8 @@ hipError_t launch_rope(const RopeCall& a, hipStream_t stream) {
   const int size = f32 ? 4 : 2;
   const bool wide = a.rope.dim % 16 == 0 && a.D % 8 == 0 && vector_rows(a.x, size) &&
                     vector_rows(a.out, size);
-  if (f32) return launch_blocks(a, a.T, wide ? k_rope<float, 8> : k_rope<float, 1>, stream);
-  return launch_blocks(a, a.T, wide ? k_rope<uint16_t, 8> : k_rope<uint16_t, 1>, stream);
+  if (f32) return wide ? launch_rope_t<float, 8>(a, stream) : launch_rope_t<float, 1>(a, stream);
+  return wide ? launch_rope_t<uint16_t, 8>(a, stream) : launch_rope_t<uint16_t, 1>(a, stream);
 }
 
 hipError_t launch_append(const AppendCall& a, hipStream_t stream) {
@@ -298,9 +321,8 @@ hipError_t launch_append(const AppendCall& a, hipStream_t stream) {
   const int size = f32 ? 4 : 2;
   const bool wide = a.rope.dim % 16 == 0 && vector_rows(a.k, size) && vector_rows(a.v, size) &&
                     (!a.q.p || (vector_rows(a.q, size) && vector_rows(a.q_out, size)));
-  const int64_t T = a.batch.T;
-  if (f32) return launch_blocks(a, T, wide ? k_append<float, 8> : k_append<float, 1>, stream);
-  return launch_blocks(a, T, wide ? k_append<uint16_t, 8> : k_append<uint16_t, 1>, stream);
+  if (f32) return wide ? launch_append_t<float, 8>(a, stream) : launch_append_t<float, 1>(a, stream);
+  return wide ? launch_append_t<uint16_t, 8>(a, stream) : launch_append_t<uint16_t, 1>(a, stream);
 }
 
 }  // namespace moe
