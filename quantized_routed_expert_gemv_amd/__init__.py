@@ -790,6 +790,9 @@ _ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}           #
 
 def _strided(t, dtypes, shape, name, like):
     """A device tensor of one of `dtypes` whose last dimension is dense, on the device of `like`."""
+    if t.dtype in dtypes and t.shape == shape and t.get_device() == like.get_device() >= 0 and \
+            t.stride()[-1] == 1:
+        return
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
     if t.shape != shape:
@@ -806,7 +809,9 @@ def _stride(t, i):
 
 
 def _heads(t):
-    return HeadsStruct(t.data_ptr(), _stride(t, 0), _stride(t, 1))
+    T, n, _ = t.shape
+    token, head, _ = t.stride()
+    return HeadsStruct(t.data_ptr(), token if T > 1 else 0, head if n > 1 else 0)
 
 
 def _new_like(shape, dtype, like, stream):
@@ -814,6 +819,13 @@ def _new_like(shape, dtype, like, stream):
         return like.new_empty(shape, dtype=dtype)
     with _on(stream):
         return like.new_empty(shape, dtype=dtype)
+
+
+def _like(t, stream):
+    if stream is None:
+        return torch.empty_like(t)
+    with _on(stream):
+        return torch.empty_like(t)
 
 
 def _check_flags(err_flags, like):
@@ -832,7 +844,7 @@ class Rope:
         _tensor(freq, (torch.float64,), (freq.numel(),), "freq", freq)
         if freq.numel() > _SIZE // 2:
             _too_large(2 * freq.numel())
-        self.freq, self.layout, self.scale = freq, layout, scale
+        self.freq, self.layout, self.scale, self.index = freq, layout, scale, freq.get_device()
         self.struct = RopeStruct(freq.data_ptr(), 2 * freq.numel(), _LAYOUTS[layout], scale)
 
     @classmethod
@@ -886,6 +898,7 @@ class KvCache:
                 _tensor(t, (torch.float32,), (k.shape[2],), name, k)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.page_size, self.n_heads, self.D = k.shape
+        self.index = k.get_device()
         self.struct = KvCacheStruct(_CACHE_TYPES[k.dtype], *k.shape,
                                     k.data_ptr(), *(_stride(k, i) for i in range(3)),
                                     v.data_ptr(), *(_stride(v, i) for i in range(3)),
@@ -915,7 +928,7 @@ class KvBatch:
         if max(n, page_table.shape[1], max_q, max_len) > _SIZE:
             _too_large(n, page_table.shape[1], max_q, max_len)
         self.q_start, self.seq_len, self.page_table = q_start, seq_len, page_table
-        self.n_seq, self.max_q, self.max_len = n, max_q, max_len
+        self.n_seq, self.max_q, self.max_len, self.index = n, max_q, max_len, seq_len.get_device()
         self._structs, self._scratch = {}, {}
 
     def struct(self, T: int):
@@ -929,9 +942,9 @@ class KvBatch:
         return s
 
 
-def _same_device(name, t, like):
-    if t.device != like.device:
-        raise ValueError(f"{name}: on {t.device}, expected {like.device}")
+def _same_device(name, index, like):
+    if index != like.get_device():
+        raise ValueError(f"{name}: on device {index}, expected {like.device}")
 
 
 def rope(x, positions, plan: Rope, inverse: bool = False, out=None, stream=None):
@@ -945,9 +958,9 @@ def rope(x, positions, plan: Rope, inverse: bool = False, out=None, stream=None)
         _too_large(T, n, D)
     _strided(x, _DT, (T, n, D), "x", x)
     _tensor(positions, (torch.int32,), (T,), "positions", x)
-    _same_device("plan", plan.freq, x)
+    _same_device("plan", plan.index, x)
     if out is None:
-        out = _new_like((T, n, D), x.dtype, x, stream)
+        out = _like(x, stream)
     else:
         _strided(out, (x.dtype,), (T, n, D), "out", x)
     _run(_rope, x, stream, plan.struct, _heads(x), _DT[x.dtype], T, n, D, positions.data_ptr(),
@@ -968,10 +981,10 @@ def kv_append(cache: KvCache, batch: KvBatch, k, v, rope: Rope = None, positions
         _too_large(T)
     _strided(k, _DT, (T, cache.n_heads, cache.D), "k", k)
     _strided(v, (k.dtype,), k.shape, "v", k)
-    _same_device("cache", cache.k, k)
-    _same_device("batch", batch.seq_len, k)
+    _same_device("cache", cache.index, k)
+    _same_device("batch", batch.index, k)
     if rope is not None:
-        _same_device("rope", rope.freq, k)
+        _same_device("rope", rope.index, k)
     if positions is not None:
         _tensor(positions, (torch.int32,), (T,), "positions", k)
     _check_flags(err_flags, k)
@@ -982,7 +995,7 @@ def kv_append(cache: KvCache, batch: KvBatch, k, v, rope: Rope = None, positions
         n_q = q.shape[1]
         _strided(q, (k.dtype,), (T, n_q, cache.D), "q", k)
         if q_out is None:
-            q_out = _new_like(q.shape, q.dtype, q, stream)
+            q_out = _like(q, stream)
         else:
             _strided(q_out, (k.dtype,), q.shape, "q_out", k)
     elif q_out is not None:
@@ -1014,13 +1027,13 @@ def attend(q, cache: KvCache, batch: KvBatch, scale: float = None, causal: bool 
     if T > _SIZE or n > _SIZE:
         _too_large(T, n)
     _strided(q, _HALF_TYPES, (T, n, cache.D), "q", q)
-    _same_device("cache", cache.k, q)
-    _same_device("batch", batch.seq_len, q)
+    _same_device("cache", cache.index, q)
+    _same_device("batch", batch.index, q)
     if sinks is not None:
         _tensor(sinks, (torch.float32,), (n,), "sinks", q)
     _check_flags(err_flags, q)
     if out is None:
-        out = _new_like((T, n, D), q.dtype, q, stream)
+        out = _like(q, stream)
     else:
         _strided(out, (q.dtype,), (T, n, D), "out", q)
     key = (cache.n_heads, D, cache.page_size, T, n, window, keep_first)
@@ -1041,11 +1054,13 @@ def linear(x, w, bias=None, act: str = "none", resid=None, out_dtype=None, out=N
     """resid + act(x w^T + bias): x [M, K] and w [N, K] bf16 or fp16 (rows dense), bias [N] and resid
     [M, N] of any float type, act "none", "relu", "gelu", "gelu_tanh" or "silu" -> out [M, N] of
     out_dtype (resid's type, or x's without one). out may be resid."""
-    _one_of("act", act, _ACTS)
+    code = _ACTS.get(act)
+    if code is None:
+        _one_of("act", act, _ACTS)
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x, w: expected [M, K] and [N, K]")
     (M, K), N = x.shape, w.shape[0]
-    if max(M, N, K) > _SIZE:
+    if M > _SIZE or N > _SIZE or K > _SIZE:
         _too_large(M, N, K)
     _strided(x, _HALF_TYPES, (M, K), "x", x)
     _strided(w, (x.dtype,), (N, K), "w", x)
@@ -1055,15 +1070,17 @@ def linear(x, w, bias=None, act: str = "none", resid=None, out_dtype=None, out=N
         out_dtype = out.dtype
     if out_dtype is None:
         out_dtype = x.dtype if resid is None else resid.dtype
-    _one_of("out_dtype", out_dtype, _DT)
+    elif out_dtype not in _DT:
+        _one_of("out_dtype", out_dtype, _DT)
     if resid is not None:
         _strided(resid, (out_dtype,), (M, N), "resid", x)
     if out is None:
         out = _new_like((M, N), out_dtype, x, stream)
     else:
         _strided(out, (out_dtype,), (M, N), "out", x)
-    _run(_linear, x, stream, x.data_ptr(), _stride(x, 0), w.data_ptr(), _stride(w, 0), _DT[x.dtype],
-         M, N, K, _addr(bias), 0 if bias is None else _DT[bias.dtype], _ACTS[act], _addr(resid),
+    _run(_linear, x, stream, x.data_ptr(), x.stride()[0] if M > 1 else 0, w.data_ptr(),
+         w.stride()[0] if N > 1 else 0, _DT[x.dtype], M, N, K, _addr(bias),
+         0 if bias is None else _DT[bias.dtype], code, _addr(resid),
          0 if resid is None else _stride(resid, 0), out.data_ptr(), _DT[out_dtype],
-         out.stride(0) if M > 1 else N)
+         out.stride()[0] if M > 1 else N)
     return out

@@ -254,11 +254,13 @@ def test_buffers_belong_to_the_given_stream(monkeypatch):
         finally:
             current[0] = before
 
-    new_empty = torch.Tensor.new_empty
+    new_empty, empty_like = torch.Tensor.new_empty, torch.empty_like
     monkeypatch.setattr(torch.cuda, "stream", stream)
     monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
     monkeypatch.setattr(torch.Tensor, "new_empty",
                         lambda t, *a, **k: (seen.append(current[0]), new_empty(t, *a, **k))[1])
+    monkeypatch.setattr(torch, "empty_like",
+                        lambda t, *a, **k: (seen.append(current[0]), empty_like(t, *a, **k))[1])
     monkeypatch.setattr(qm, "_run", lambda *a: None)
     i32, side = torch.int32, object()
     p = qm.Rope(z(32, dt=torch.float64))
