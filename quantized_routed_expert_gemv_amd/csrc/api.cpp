@@ -1204,6 +1204,7 @@ moe_status moe_attend(const moe_kv_cache* cache, const moe_kv_batch* batch, cons
   a.cache = cache_view(cache), a.batch = batch_view(batch);
   a.q = heads_view(q), a.out = heads_view(out);
   a.type = type, a.n_q_heads = n_q_heads, a.group = n_q_heads / cache->n_heads;
+  a.group_inv = 0xFFFFFFFFu / (uint32_t)a.group;
   a.scale = scale, a.causal = causal != 0, a.window = window, a.keep_first = keep_first;
   a.sinks = sinks, a.err = err_flags;
   clear_stale_error();

@@ -110,6 +110,11 @@ struct Tile {
   int first_of_last;   // the last row: between them every row sees every key
 };
 
+// The new token of a row.
+__device__ __forceinline__ int token_of(const AttendCall& a, int row) {
+  return div_by(row, a.group, a.group_inv);
+}
+
 // The first key in the window of position pos.
 __device__ __forceinline__ int window_start(const AttendCall& a, int pos) {
   return a.window ? (int)max((int64_t)pos - a.window + 1, (int64_t)0) : 0;
@@ -140,7 +145,7 @@ __device__ __forceinline__ bool find_tile(const AttendCall& a, int64_t x, int he
   t->rows = (int)min(rows, (int64_t)R);
   t->token0 = lo;
   t->pos0 = len - n;
-  const int first_tok = t->row0 / a.group, last_tok = (t->row0 + t->rows - 1) / a.group;
+  const int first_tok = token_of(a, t->row0), last_tok = token_of(a, t->row0 + t->rows - 1);
   const int end = (int)min((int64_t)len, cap);
   t->end = a.causal ? max(min(end, t->pos0 + last_tok + 1), 0) : end;
   t->last_of_first = a.causal ? min(t->pos0 + first_tok, t->end - 1) : t->end - 1;
@@ -195,7 +200,7 @@ __device__ __forceinline__ KeyRow key_row(const AttendCall& a, const Tile& t, in
 template <bool F16, int N>
 __device__ __forceinline__ void store_row(const AttendCall& a, const Tile& t, int splits, int split,
                                           int r, int d, float m, float l, const float* o) {
-  const int tok = (t.row0 + r) / a.group, g = t.row0 + r - tok * a.group;
+  const int tok = token_of(a, t.row0 + r), g = t.row0 + r - tok * a.group;
   const int64_t token = t.token0 + tok;
   const int head = t.head * a.group + g;
   if (splits > 1) {
@@ -251,7 +256,7 @@ __device__ void add_odd_values(const AttendCall& a, const Tile& t, const Blocks<
       const float v = plane_value(a.cache.v, kv.v + d, a.cache.type) * vs;
       if (fabsf(v) < INFINITY) continue;
       for (int r = 0; r < t.rows; ++r) {
-        const int tok = (t.row0 + r) / a.group, pos = t.pos0 + tok;
+        const int tok = token_of(a, t.row0 + r), pos = t.pos0 + tok;
         if (a.causal && key > pos) continue;
         if (key < window_start(a, pos) && key >= a.keep_first) continue;
         const int64_t token = t.token0 + tok;
@@ -296,11 +301,11 @@ __global__ __launch_bounds__(kRowThreads, DV > 128 ? 1 : 2) void k_attend_rows(A
   __shared__ int s_odd;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int n = lane & 15, g = lane >> 4;
-  const int64_t id = a.block0 + blockIdx.x;
-  const int split = (int)(id % a.splits_few);
-  const int64_t th = id / a.splits_few;
+  // workgroups go KV head by KV head (an XCD's stay on few of them), then split by split
+  const int split = (int)(blockIdx.x / (unsigned)a.cache.n_heads);
+  const int head = (int)blockIdx.x - split * a.cache.n_heads;
   Tile t;
-  if (!find_tile<kRowTile, true>(a, th / a.cache.n_heads, (int)(th % a.cache.n_heads), &t)) return;
+  if (!find_tile<kRowTile, true>(a, a.block0 + blockIdx.y, head, &t)) return;
   const Blocks<32> blocks(t);
   const int b0 = (int)((int64_t)blocks.count * split / a.splits_few);
   const int b1 = (int)((int64_t)blocks.count * (split + 1) / a.splits_few);
@@ -309,7 +314,7 @@ __global__ __launch_bounds__(kRowThreads, DV > 128 ? 1 : 2) void k_attend_rows(A
   __syncthreads();
 
   // this lane's query: the keys that it sees, and its row of q as an operand
-  const int tok = (t.row0 + n) / a.group;
+  const int tok = token_of(a, t.row0 + n);
   const bool row_ok = n < t.rows;
   const int pos = t.pos0 + tok;
   const int see_last = !row_ok ? -1 : a.causal ? min(pos, t.end - 1) : t.end - 1;
@@ -559,13 +564,11 @@ __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int n = lane & 31, hf = lane >> 5;
-  const int64_t id = a.block0 + blockIdx.x;
-  const int head = (int)(id % a.cache.n_heads);
-  const int64_t th = id / a.cache.n_heads;
-  const int split = (int)(th % a.splits);
+  const int split = (int)(blockIdx.x / (unsigned)a.cache.n_heads);
+  const int head = (int)blockIdx.x - split * a.cache.n_heads;
   Tile t;
   // later tiles, which see more keys, first
-  if (!find_tile<kTileRows, false>(a, a.tiles - 1 - th / a.splits, head, &t)) return;
+  if (!find_tile<kTileRows, false>(a, a.tiles - 1 - a.block0 - blockIdx.y, head, &t)) return;
   const Blocks<kTileKeys> blocks(t);
   const int b0 = (int)((int64_t)blocks.count * split / a.splits);
   const int b1 = (int)((int64_t)blocks.count * (split + 1) / a.splits);
@@ -574,7 +577,7 @@ __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles
   __syncthreads();
 
   const int r = 32 * wave + n;
-  const int tok = (t.row0 + r) / a.group;
+  const int tok = token_of(a, t.row0 + r);
   const bool row_ok = r < t.rows;
   const int pos = t.pos0 + tok;
   const int see_last = !row_ok ? -1 : a.causal ? min(pos, t.end - 1) : t.end - 1;
@@ -582,8 +585,8 @@ __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles
   const int keep = a.window ? a.keep_first : 0;
   // what all of the wave's rows see last, and first
   const int w_rows = min(max(t.rows - 32 * wave, 0), 32);
-  const int w_first = t.pos0 + (t.row0 + 32 * wave) / a.group;
-  const int w_last = t.pos0 + (t.row0 + 32 * wave + max(w_rows, 1) - 1) / a.group;
+  const int w_first = t.pos0 + token_of(a, t.row0 + 32 * wave);
+  const int w_last = t.pos0 + token_of(a, t.row0 + 32 * wave + max(w_rows, 1) - 1);
   const int w_all = a.causal ? min(w_first, t.end - 1) : t.end - 1;
   const int w_from = window_start(a, w_last);
   float c = a.scale * kLog2e;
@@ -892,20 +895,17 @@ __global__ __launch_bounds__(kRowThreads) void k_attend_join(AttendCall a) {
   __shared__ float weight[kMaxSplits];
   __shared__ f32x4 sums[NW][kWave];
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  int64_t id = a.block0 + blockIdx.x, token;
   int splits = a.few ? a.splits_few : a.splits, head;
+  int64_t token = a.block0 + blockIdx.y;
   if (a.both && a.splits == 1) {   // of the sequences with few rows alone: row r of one and a KV head
-    const int r = (int)(id % kFewRows);
-    id /= kFewRows;
-    const int kv = (int)(id % a.cache.n_heads), seq = (int)(id / a.cache.n_heads);
+    const int r = blockIdx.x, kv = (int)(token % a.cache.n_heads), seq = (int)(token / a.cache.n_heads);
     const int lo = first_row(a.batch, seq), n = first_row(a.batch, seq + 1) - lo;
     if (n <= 0 || (int64_t)n * a.group > kFewRows || r >= n * a.group) return;
     token = lo + r / a.group;
     head = kv * a.group + r % a.group;
     splits = a.splits_few;
   } else {
-    token = id / a.n_q_heads;
-    head = (int)(id - token * a.n_q_heads);
+    head = blockIdx.x;
     if (token < first_row(a.batch, 0) || token >= first_row(a.batch, a.batch.n_seq)) return;
     if (a.both) {
       const int seq = wave_find(a.batch.n_seq, token, [&](int i) { return first_row(a.batch, i); });
@@ -966,14 +966,16 @@ __global__ __launch_bounds__(kRowThreads) void k_attend_join(AttendCall a) {
   *(u32x2*)p = u32x2{pack2<F16>(o[0], o[1]), pack2<F16>(o[2], o[3])};
 }
 
-constexpr int64_t kMaxBlocks = 1 << 22;   // a launch holds fewer than 2^32 threads
-
+// across workgroups for each of `count` tiles or rows, as many of these at a time as a launch takes.
 template <typename K>
-hipError_t launch_blocks(AttendCall a, int64_t blocks, K kernel, int threads, hipStream_t stream) {
-  for (int64_t b = 0; b < blocks; b += kMaxBlocks) {
+hipError_t launch_blocks(AttendCall a, int64_t across, int64_t count, K kernel, int threads,
+                         hipStream_t stream) {
+  // a launch holds fewer than 2^32 threads, a grid's second dimension fewer than 2^16 workgroups
+  const int64_t most = min(max((int64_t(1) << 22) / across, (int64_t)1), (int64_t)kMaxGridY);
+  for (int64_t b = 0; b < count; b += most) {
     a.block0 = b;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)min(blocks - b, kMaxBlocks)), dim3(threads), 0,
-                       stream, a);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)across, (unsigned)min(count - b, most)), dim3(threads),
+                       0, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -986,25 +988,26 @@ hipError_t launch_depth(AttendCall a, hipStream_t stream) {
   const bool tiles = a.both || !a.few, rows = a.both || a.few;
   if (tiles) {
     a.tiles = (int64_t)a.batch.T * a.group / kTileRows + a.batch.n_seq;
-    const int64_t blocks = a.tiles * a.cache.n_heads * a.splits;
+    const int64_t across = (int64_t)a.cache.n_heads * a.splits;
     // a page's 16 rows have to be within 32-bit offsets of the first
     const bool near = max(a.cache.k_token, a.cache.v_token) < (int64_t(1) << 26);
     e = a.cache.page_size % 16 == 0 && near
-            ? launch_blocks(a, blocks, k_attend_tiles<F16, FP8, DV, true>, kTileThreads, stream)
-            : launch_blocks(a, blocks, k_attend_tiles<F16, FP8, DV, false>, kTileThreads, stream);
+            ? launch_blocks(a, across, a.tiles, k_attend_tiles<F16, FP8, DV, true>, kTileThreads, stream)
+            : launch_blocks(a, across, a.tiles, k_attend_tiles<F16, FP8, DV, false>, kTileThreads, stream);
   }
   if (rows && e == hipSuccess) {
     a.tiles = (int64_t)a.batch.T * a.group / kRowTile + a.batch.n_seq;
-    const int64_t blocks = a.tiles * a.cache.n_heads * a.splits_few;
+    const int64_t across = (int64_t)a.cache.n_heads * a.splits_few;
     e = a.cache.page_size % 8 == 0
-            ? launch_blocks(a, blocks, k_attend_rows<F16, FP8, DV, true>, kRowThreads, stream)
-            : launch_blocks(a, blocks, k_attend_rows<F16, FP8, DV, false>, kRowThreads, stream);
+            ? launch_blocks(a, across, a.tiles, k_attend_rows<F16, FP8, DV, true>, kRowThreads, stream)
+            : launch_blocks(a, across, a.tiles, k_attend_rows<F16, FP8, DV, false>, kRowThreads, stream);
   }
   const bool join = (tiles && a.splits > 1) || (rows && a.splits_few > 1);
   if (!join || e != hipSuccess) return e;
-  const int64_t n = a.both && a.splits == 1 ? (int64_t)a.batch.n_seq * a.cache.n_heads * kFewRows
-                                           : (int64_t)a.batch.T * a.n_q_heads;
-  return launch_blocks(a, n, k_attend_join<F16>, kRowThreads, stream);
+  if (a.both && a.splits == 1)
+    return launch_blocks(a, kFewRows, (int64_t)a.batch.n_seq * a.cache.n_heads, k_attend_join<F16>,
+                         kRowThreads, stream);
+  return launch_blocks(a, a.n_q_heads, a.batch.T, k_attend_join<F16>, kRowThreads, stream);
 }
 
 template <bool F16, bool FP8>

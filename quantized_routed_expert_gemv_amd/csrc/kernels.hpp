@@ -216,6 +216,7 @@ struct AttendCall {
   KvBatchView batch;
   HeadsView q, out;
   int type, n_q_heads, group;   // group: query heads a KV head
+  uint32_t group_inv;           // floor((2^32 - 1) / group)
   float scale;
   bool causal;
   int window, keep_first;
@@ -225,7 +226,7 @@ struct AttendCall {
   bool few, both;           // sequences with few rows only; with few and with many
   float* part;              // splits > 1: [splits][T * n_q_heads][D] sums of weighted values,
   float* stats;             // [splits][T * n_q_heads][2] maximum (of log2 e s) and sum of weights
-  int64_t tiles, block0;    // set by the launcher: tiles, and first workgroup, of a launch
+  int64_t tiles, block0;    // set by the launcher: tiles, and first tile or row, of a launch
 };
 struct AttendPlan {
   int splits, splits_few;

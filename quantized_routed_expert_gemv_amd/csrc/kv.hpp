@@ -36,6 +36,12 @@ __device__ __forceinline__ int page_of(uint32_t pos, int page_size, uint32_t inv
   return (int)q;
 }
 
+// x / d for 0 <= x < 2^31, with inv = floor((2^32 - 1) / d).
+__device__ __forceinline__ int div_by(int x, int d, uint32_t inv) {
+  int rest;
+  return page_of((uint32_t)x, d, inv, &rest);
+}
+
 // First row of sequence b's new tokens (b = n_seq: the end of the last), within [0, T].
 __device__ __forceinline__ int first_row(const KvBatchView& b, int i) {
   return min(max(b.q_start[i], 0), b.T);

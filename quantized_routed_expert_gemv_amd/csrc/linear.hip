@@ -149,13 +149,15 @@ __device__ __forceinline__ void meet() {
 // tiles of rows of x side by side, column by column.
 template <int BM, int BN>
 __device__ __forceinline__ void find_tile(const LinearCall& a, int64_t* m0, int64_t* n0) {
-  const int64_t tm = ((int64_t)a.M + BM - 1) / BM, tn = ((int64_t)a.N + BN - 1) / BN;
-  int64_t id = a.tile0 + blockIdx.x;
-  const int64_t all = tm * tn, per = (all + 7) / 8, x = id % 8, full = all - 8 * (per - 1);
+  // M * N is below 2^40, and tiles of fewer than 64 x 64 are few: their number fits 32 bits
+  const uint32_t tm = (uint32_t)(a.M + BM - 1) / BM, tn = (uint32_t)(a.N + BN - 1) / BN;
+  uint32_t id = (uint32_t)a.tile0 + blockIdx.x;
+  const uint32_t all = tm * tn, per = (all + 7) / 8, x = id % 8, full = all - 8 * (per - 1);
   id = id / 8 + (x < full ? x * per : full * per + (x - full) * (per - 1));
-  const int64_t band = id / (8 * tn), left = id % (8 * tn), high = min(tm - 8 * band, (int64_t)8);
-  *m0 = (8 * band + left % high) * BM;
-  *n0 = left / high * BN;
+  const uint32_t band = id / (8 * tn), left = id - band * (8 * tn), high = min(tm - 8 * band, 8u);
+  const uint32_t col = high == 8 ? left / 8 : left / high;
+  *m0 = (int64_t)(8 * band + left - col * high) * BM;
+  *n0 = (int64_t)col * BN;
 }
 
 // Many rows. A workgroup of KG groups of WM x WN waves makes a tile of BM rows of x and BN of w; each
