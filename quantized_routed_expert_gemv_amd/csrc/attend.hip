@@ -528,29 +528,33 @@ constexpr int kTileThreads = 256;
 constexpr int kTileRows = 128;   // 32 a wave
 constexpr int kTileKeys = 64;
 
-// Row strides, in 16-bit values, of a tile's keys and values in LDS: keys are read 16 bytes a lane
-// over 32 rows (rows 4 banks apart: no conflict), values through the transposing read, 4 rows of 32
-// bytes for 16 lanes (rows 16 banks apart: none either).
-template <int DV> constexpr int kKeyStride = DV + 8;
-template <int DV> constexpr int kValueStride = DV + 32;
+// A row of keys or values in LDS is DV values in 16-byte pieces, in the order piece ^ key_order(row) or
+// piece ^ value_order(row). Keys are read a piece a lane over 16 rows, values through the transposing
+// read, four pieces of four rows at once: either way on all banks.
+template <int DV> __device__ __forceinline__ int key_order(int row) {
+  return row & (DV >= 128 ? 15 : 7);
+}
+template <int DV> __device__ __forceinline__ int value_order(int row) {
+  return DV >= 128 ? 4 * (row & 3) : 4 * (row >> 1 & 1);
+}
 
-template <int DV> struct alignas(16) TileBuffer {
-  uint16_t k[kTileKeys][kKeyStride<DV>];
-  uint16_t v[kTileKeys][kValueStride<DV>];
-};
+__device__ __align__(16) const uint32_t g_zero[4] = {0, 0, 0, 0};   // read in place of what is behind D
 
 // The transposing LDS read: of 16 lanes, lane i reads 8 bytes (its address) of row i / 4, columns
-// 4 (i % 4) on, and is left with column i of the four rows.
-__device__ __forceinline__ u32x2 read_columns(const uint16_t* p) {
+// 4 (i % 4) on, and is left with column i of the four rows. (The compiler waits in front of it for
+// every load into LDS that is under way. Reads in inline assembly, which carry their own wait, gained
+// 2.3-3.9 per cent over staging through registers, these 3.4-4.7.)
+__device__ __forceinline__ u32x2 read_columns(const uint8_t* p) {
   typedef __attribute__((address_space(3))) i16x4* lds_p;
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)p));
 }
 
 // Many rows a sequence: the matrix instructions bound it. Four waves of 32 rows (columns of
-// 32x32x16 instructions) share tiles of 64 keys and values, which go through registers into two LDS
-// buffers, the next tile's loads in flight behind the products of this one. Values reach the second
-// product through the transposing LDS read, in the order of keys in which the first left the
-// weights: 16 s + {4 h .. + 3, 8 + 4 h .. + 3} for k-step s and lane half h.
+// 32x32x16 instructions) share tiles of 64 keys and values in two LDS buffers, the next tile's loads in
+// flight behind the products of this one: of a 16-bit cache straight into LDS, of an 8-bit one through
+// registers, where they are widened. Values reach the second product through the transposing LDS read,
+// in the order of keys in which the first left the weights: 16 s + {4 h .. + 3, 8 + 4 h .. + 3} for
+// k-step s and lane half h.
 // U16: pages hold a multiple of 16 tokens, so the 16 rows of a tile that a wave loads are on one.
 template <bool F16, bool FP8, int DV, bool U16>
 __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles(AttendCall a) {
@@ -558,7 +562,8 @@ __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles
   constexpr int CH = DV * (FP8 ? 1 : 2) / 16;          // 16-byte chunks of a row
   constexpr int RP = kWave / CH, NP = 16 / RP;         // rows a wave loads at once; passes
   constexpr int CV = FP8 ? 16 : 8;                     // values of a chunk
-  __shared__ TileBuffer<DV> buf[2];
+  constexpr int kRow = 2 * DV;                         // bytes of a row in LDS
+  __shared__ __align__(16) uint8_t s_k[2][kTileKeys * kRow], s_v[2][kTileKeys * kRow];
   __shared__ uint64_t s_ok[2];                         // rows of the tile that are on a page
   __shared__ int s_odd;
   const int lane = threadIdx.x & (kWave - 1);
@@ -611,13 +616,30 @@ __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles
     for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
   float m = -INFINITY, l = 0.f;
 
-  // Loads: this lane's chunk of a row, and the rows of each pass, j RP + rsub.
-  const int chunk = lane % CH, rsub = lane / CH;
-  const bool chunk_ok = chunk * CV < D;
+  // Loads: the rows of each pass, j RP + rsub, and this lane's chunk of them. Straight into LDS lane l's
+  // piece lands at place l, so the chunk is the one whose place that is.
+  typedef __attribute__((address_space(3))) void* lds_ptr;
+  typedef __attribute__((address_space(1))) const void* global_ptr;
   constexpr int kSize = FP8 ? 1 : 2;
-  const uint32_t k_off = (uint32_t)(rsub * a.cache.k_token + (chunk_ok ? chunk * CV : 0)) * kSize;
-  const uint32_t v_off = (uint32_t)(rsub * a.cache.v_token + (chunk_ok ? chunk * CV : 0)) * kSize;
-  u32x4 kr[NP], vr[NP];
+  const int rsub = lane / CH;
+  int k_chunk[NP], v_chunk[NP];
+  uint32_t k_off[NP], v_off[NP];
+#pragma unroll
+  for (int j = 0; j < NP; ++j) {
+    k_chunk[j] = FP8 ? lane % CH : (lane % CH) ^ key_order<DV>(j * RP + rsub);
+    v_chunk[j] = FP8 ? lane % CH : (lane % CH) ^ value_order<DV>(j * RP + rsub);
+    k_off[j] = (uint32_t)(rsub * a.cache.k_token + (k_chunk[j] * CV < D ? k_chunk[j] * CV : 0)) * kSize;
+    v_off[j] = (uint32_t)(rsub * a.cache.v_token + (v_chunk[j] * CV < D ? v_chunk[j] * CV : 0)) * kSize;
+  }
+  u32x4 kr[NP], vr[NP];   // of an 8-bit cache
+  auto fetch = [&](const uint8_t* p, bool in, uint8_t* to, u32x4& reg) {
+    if constexpr (FP8)
+      reg = *(const u32x4*)p;
+    else if (D == DV)
+      __builtin_amdgcn_global_load_lds((global_ptr)p, (lds_ptr)to, 16, 0, 0);
+    else
+      __builtin_amdgcn_global_load_lds(in ? (global_ptr)p : (global_ptr)g_zero, (lds_ptr)to, 16, 0, 0);
+  };
   // Of this wave's 16 rows of a block: U16, their page (asked for a block ahead of its use) and the
   // row of it, and which are on a page and in sight.
   struct Rows {
@@ -650,19 +672,22 @@ __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles
     }
     return r;
   };
-  auto load_k = [&](int b, Rows& r) {
+  auto load_k = [&](int b, int to, Rows& r) {
+    uint8_t* lds = s_k[to] + 16 * wave * kRow;
     if constexpr (U16) {
       const uint8_t* base = a.cache.k + (r.page * a.cache.k_page + r.row * a.cache.k_token +
                                          t.head * a.cache.k_head) * kSize;
 #pragma unroll
       for (int j = 0; j < NP; ++j)
-        kr[j] = *(const u32x4*)(base + j * RP * a.cache.k_token * kSize + k_off);
+        fetch(base + j * RP * a.cache.k_token * kSize + k_off[j], k_chunk[j] * CV < D, lds + 1024 * j,
+              kr[j]);
     } else {
       r.ok = 0;
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
         const KeyRow kv = key_row<1>(a, t, blocks.key(b) + 16 * wave + j * RP + rsub);
-        kr[j] = *(const u32x4*)(a.cache.k + (kv.k + (chunk_ok ? chunk * CV : 0)) * kSize);
+        const bool in = k_chunk[j] * CV < D;
+        fetch(a.cache.k + (kv.k + (in ? k_chunk[j] * CV : 0)) * kSize, in, lds + 1024 * j, kr[j]);
         const uint64_t rows = __ballot(kv.ok);
 #pragma unroll
         for (int i = 0; i < RP; ++i) r.ok |= (uint32_t)(rows >> (i * CH) & 1) << (j * RP + i);
@@ -670,62 +695,85 @@ __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles
       r.ok = __builtin_amdgcn_readfirstlane(r.ok);
     }
   };
-  auto load_v = [&](int b, const Rows& r) {
+  auto load_v = [&](int b, int to, const Rows& r) {
+    uint8_t* lds = s_v[to] + 16 * wave * kRow;
     if constexpr (U16) {
       const uint8_t* base = a.cache.v + (r.page * a.cache.v_page + r.row * a.cache.v_token +
                                          t.head * a.cache.v_head) * kSize;
 #pragma unroll
       for (int j = 0; j < NP; ++j)
-        vr[j] = *(const u32x4*)(base + j * RP * a.cache.v_token * kSize + v_off);
+        fetch(base + j * RP * a.cache.v_token * kSize + v_off[j], v_chunk[j] * CV < D, lds + 1024 * j,
+              vr[j]);
     } else {
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
         const KeyRow kv = key_row<1>(a, t, blocks.key(b) + 16 * wave + j * RP + rsub);
-        vr[j] = *(const u32x4*)(a.cache.v + (kv.v + (chunk_ok ? chunk * CV : 0)) * kSize);
+        const bool in = v_chunk[j] * CV < D;
+        fetch(a.cache.v + (kv.v + (in ? v_chunk[j] * CV : 0)) * kSize, in, lds + 1024 * j, vr[j]);
       }
     }
   };
-  constexpr int NW = CV / 2;   // dwords of a chunk's 16-bit values
-  auto widened = [&](const u32x4& raw, uint32_t* w) {
-    widen<CV, F16, FP8>((const uint32_t*)&raw, w);
-    if (D != DV) {
-#pragma unroll
-      for (int i = 0; i < NW; ++i) w[i] = chunk_ok ? w[i] : 0;
-    }
-  };
+  // What lies in registers goes to LDS, widened; values as `finish` says.
   auto store_k = [&](int to) {
+    if constexpr (FP8) {
 #pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      uint32_t w[8];
-      widened(kr[j], w);
-      uint16_t* p = &buf[to].k[16 * wave + j * RP + rsub][chunk * CV];
+      for (int j = 0; j < NP; ++j) {
+        const int row = 16 * wave + j * RP + rsub;
+        uint32_t w[8];
+        widen<16, F16, true>((const uint32_t*)&kr[j], w);
 #pragma unroll
-      for (int i = 0; i < NW; i += 4) *(u32x4*)(p + 2 * i) = u32x4{w[i], w[i + 1], w[i + 2], w[i + 3]};
+        for (int i = 0; i < 2; ++i) {
+          u32x4 v = {w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+          if (D != DV && k_chunk[j] * CV >= D) v = u32x4{0, 0, 0, 0};
+          *(u32x4*)(s_k[to] + row * kRow + ((2 * k_chunk[j] + i) ^ key_order<DV>(row)) * 16) = v;
+        }
+      }
     }
   };
-  auto store_v = [&](int b, int to, const Rows& r) {
+  // The block's values are in LDS, those out of sight as zeros. In sight of some rows only: an infinity
+  // or NaN is 0 here, and given to the rows that see it at the end (add_odd_values).
+  auto finish_v = [&](int b, int to, const Rows& r) {
     const bool seen = whole_block<kTileKeys>(a, t, blocks.key(b));
     const bool plain = seen && r.ok == 0xFFFFu;
     bool odd = false;
+    if (FP8 || !plain) {
+      if (!FP8) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's loads are in LDS
 #pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      const int row = j * RP + rsub;
-      uint32_t w[8];
-      widened(vr[j], w);
-      if (!plain) {
-        const bool some = r.ok >> row & 1;   // out of sight: zeros
+      for (int j = 0; j < NP; ++j) {
+        const int row = j * RP + rsub;
+        const bool some = r.ok >> row & 1;
+        uint32_t w[8];
+        uint8_t* at[2];
+        if constexpr (FP8) {
+          widen<16, F16, true>((const uint32_t*)&vr[j], w);
 #pragma unroll
-        for (int i = 0; i < NW; ++i) {
-          w[i] = some ? w[i] : 0;
-          odd |= take_odd<F16>(w[i], !seen);
+          for (int i = 0; i < 2; ++i)
+            at[i] = s_v[to] + (16 * wave + row) * kRow + ((2 * v_chunk[j] + i) ^ value_order<DV>(row)) * 16;
+        } else {
+          at[0] = s_v[to] + 16 * wave * kRow + 1024 * j + 16 * lane;
+          const u32x4 v = *(const u32x4*)at[0];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = v[i];
         }
-      }
-      uint16_t* p = &buf[to].v[16 * wave + row][chunk * CV];
+        if (!plain) {
 #pragma unroll
-      for (int i = 0; i < NW; i += 4) *(u32x4*)(p + 2 * i) = u32x4{w[i], w[i + 1], w[i + 2], w[i + 3]};
+          for (int i = 0; i < CV / 2; ++i) {
+            w[i] = some ? w[i] : 0;
+            odd |= take_odd<F16>(w[i], !seen);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < CV / 8; ++i)
+          *(u32x4*)at[i] = u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+      }
     }
     if (odd) s_odd = 1;
     if (lane == 0) ((uint16_t*)&s_ok[to])[wave] = (uint16_t)r.ok;
+  };
+  auto meet = [] {   // loads into LDS and stores to it are done, of all waves
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
   };
 
   // Whether all rows of this wave see all of a block. (A wave none of whose rows sees any of it goes
@@ -734,12 +782,13 @@ __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles
     return key0 + kTileKeys - 1 <= w_all && (key0 >= w_from || key0 + kTileKeys - 1 < keep);
   };
   auto key_frag = [&](int at, int u, int k) {   // operand of k-step k of the scores of half u
-    return *(const u32x4*)&buf[at].k[32 * u + n][16 * k + 8 * hf];
+    return *(const u32x4*)(s_k[at] + (32 * u + n) * kRow + ((2 * k + hf) ^ key_order<DV>(n)) * 16);
   };
+  const int v_row = (lane & 15) / 4, v_piece = 2 * (n / 16) + (lane & 3) / 2;
   auto value_frag = [&](int at, int k, int d) {   // of keys 16 k on, values 32 d on
-    const uint16_t* v = &buf[at].v[16 * k + 4 * hf + (lane & 15) / 4]
-                                  [32 * d + 16 * (n / 16) + 4 * (lane & 3)];
-    const u32x2 lo = read_columns(v), hi = read_columns(v + 8 * kValueStride<DV>);
+    const uint8_t* v = s_v[at] + (16 * k + 4 * hf + v_row) * kRow +
+                       ((4 * d + v_piece) ^ value_order<DV>(v_row)) * 16 + 8 * (lane & 1);
+    const u32x2 lo = read_columns(v), hi = read_columns(v + 8 * kRow);
     return u32x4{lo[0], lo[1], hi[0], hi[1]};
   };
   auto raise = [&](float top) {
@@ -766,25 +815,26 @@ __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles
   Rows now = {0, 0, 0}, next = {0, 0, 0}, far = {0, 0, 0};
   if (b0 < b1) {
     now = checked(lookup(b0));
-    load_k(b0, now);
-    load_v(b0, now);
+    load_k(b0, 0, now);
+    load_v(b0, 0, now);
     next = lookup(b0 + 1);
     store_k(0);
-    store_v(b0, 0, now);
+    finish_v(b0, 0, now);
     next = checked(next);
     if (low && b0 + 1 < b1) {
-      load_k(b0 + 1, next);
+      load_k(b0 + 1, 1, next);
       store_k(1);
     }
     far = lookup(b0 + 2);
   }
-  __syncthreads();
+  meet();
   // Scores of the blocks' first and second halves: [i] of key 8 (i / 4) + 4 hf + i % 4 of the half.
   f32x16 s0, s1;
 #pragma unroll
   for (int i = 0; i < 16; ++i) s0[i] = 0.f;
 #pragma unroll
   for (int k = 0; k < NK; ++k) s0 = mma32<F16>(key_frag(0, 0, k), q[k], s0);
+  meet();   // the first step loads over these keys
   auto step = [&](auto half, int key0, uint32_t ok, bool all, int at, const f32x16& in, f32x16& out) {
     constexpr int U = decltype(half)::value;
     float x[16];   // scores, then weights
@@ -856,19 +906,19 @@ __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles
     far = lookup(b + 3);
     const int kb = low ? b + 2 : b + 1;   // whose keys this wave loads
     if (kb < b1) {
-      if (low) load_k(kb, last);
-      else load_k(kb, next);
+      if (low) load_k(kb, at, last);
+      else load_k(kb, at ^ 1, next);
     }
-    if (b + 1 < b1) load_v(b + 1, next);
+    if (b + 1 < b1) load_v(b + 1, at ^ 1, next);
     const int key0 = blocks.key(b);
     const uint64_t ok = s_ok[at];
     const bool all = whole(key0);
     step(std::integral_constant<int, 0>{}, key0, (uint32_t)ok, all, at, s0, s1);
     step(std::integral_constant<int, 1>{}, key0, (uint32_t)(ok >> 32), all, at, s1, s0);
     if (kb < b1) store_k(low ? at : at ^ 1);
-    if (b + 1 < b1) store_v(b + 1, at ^ 1, next);
+    if (b + 1 < b1) finish_v(b + 1, at ^ 1, next);
     next = last;
-    __syncthreads();
+    meet();
   }
 
   l += wave_xor(l, 32);
