@@ -484,7 +484,7 @@ moe_status moe_combine_norm(const float* y, const int32_t* inv_perm, const float
  * moe_add_norm's delta: dense products, rotary positions, a paged cache of keys and values, and
  * attention of new tokens over it ([T] "How it works": sink tokens with a sliding window, a
  * static cache, 8-bit keys and values). All arithmetic is fp32 unless said otherwise, and each
- * output is rounded once, to nearest even.
+ * output is rounded once, to nearest even. Outputs must not overlap inputs, except as said.
  *
  * Rows of heads: x [T][n_heads][D] are addressed by strides, value (t, h, d) at t * token +
  * h * head + d elements, so q, k and v can be parts of the rows that one product wrote.
@@ -533,7 +533,7 @@ moe_status moe_rope(const moe_rope_plan* plan, const moe_heads* x, int32_t type,
  *              page of positions p * page_size .. of sequence b
  *   max_q, max_len   the largest number of new tokens and of keys of a sequence, or 0 where they
  *              are not known. They choose the launch; results do not depend on their truth.
- * T * n_heads <= 2^30, n_seq < 2^24. Values outside these rules in device memory (rows past T, pages
+ * n_heads * D < 2^28, T * n_heads <= 2^30, n_seq < 2^24, of the cache's and the queries' heads. Values outside these rules in device memory (rows past T, pages
  * outside the cache, positions below zero or past the table) are never followed: what would be
  * there is left out, and bit 0 of *err_flags is set (nullable uint32, atomic OR). Entries of pages
  * that no key in sight lies on are not read.

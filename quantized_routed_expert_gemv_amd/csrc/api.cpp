@@ -1043,8 +1043,9 @@ moe_status check_batch(const moe_kv_batch* b, const moe_kv_cache* c, int64_t n_q
     return fail(MOE_ERR_INVALID_ARG, "n_seq = %d outside [0, 2^24)", b->n_seq);
   if (b->T < 0) return fail(MOE_ERR_INVALID_ARG, "T = %d < 0", b->T);
   const int64_t heads = n_q_heads > c->n_heads ? n_q_heads : c->n_heads;
-  if (heads * c->D > (1 << 28) || heads * (b->T > 0 ? b->T : 1) > (1 << 30))
-    return fail(MOE_ERR_INVALID_ARG, "%lld heads, D = %d, T = %d: heads * D <= 2^28, T * heads <= 2^30",
+  // fewer than 2^24 heads, a workgroup of 256 threads each: a grid's dimension has below 2^32 threads
+  if (heads * c->D >= (1 << 28) || heads * (b->T > 0 ? b->T : 1) > (1 << 30))
+    return fail(MOE_ERR_INVALID_ARG, "%lld heads, D = %d, T = %d: heads * D < 2^28, T * heads <= 2^30",
                 (long long)heads, c->D, b->T);
   if (b->max_pages < 1 || (int64_t)b->max_pages * c->page_size > 0x7FFFF000)
     return fail(MOE_ERR_INVALID_ARG, "page table of %d pages of %d tokens: 1 to 2^31 - 4096 tokens",
@@ -1188,6 +1189,7 @@ moe_status moe_attend(const moe_kv_cache* cache, const moe_kv_batch* batch, cons
   if ((s = check_batch_ptrs(batch, err_flags)) != MOE_OK) return s;
   if ((s = check_heads("q", q, 16, 8)) != MOE_OK) return s;
   if ((s = check_heads("out", out, 16, 8)) != MOE_OK) return s;
+  if (out->p == q->p) return fail(MOE_ERR_INVALID_ARG, "out is q");
   if ((uintptr_t)sinks & 3) return fail(MOE_ERR_INVALID_ARG, "sinks misaligned");
   moe::AttendCall a{};
   const moe::AttendPlan plan = plan_of(cache, batch, n_q_heads, window, keep_first);
@@ -1248,6 +1250,7 @@ moe_status moe_linear(const void* x, int64_t x_stride, const void* w, int64_t w_
                 (long long)resid_stride);
   if (resid == out && M > 1 && resid_stride != out_stride)
     return fail(MOE_ERR_INVALID_ARG, "out is resid with another stride");
+  if (K > 0 && (out == x || out == w)) return fail(MOE_ERR_INVALID_ARG, "out is x or w");
   moe::LinearCall a{};
   a.x = (const uint16_t*)x, a.w = (const uint16_t*)w;
   a.x_stride = x_stride, a.w_stride = w_stride, a.resid_stride = resid_stride;

@@ -8,6 +8,7 @@ import quantized_routed_expert_gemv_amd as qm  # noqa: E402
 lib = qm._lib
 OK, INVALID, UNSUPPORTED = 0, 1, 2
 FAKE, ODD = 0x10000, 0x10004        # never dereferenced
+OUT = 0x30000
 BF, FP, F32, E4 = 1, 2, 3, 4
 
 
@@ -78,7 +79,7 @@ def append(c=None, b=None, k=None, v=None, type=BF, r=None, pos=None, q=None, n_
 def attend(c=None, b=None, q=None, type=BF, n_q=4, scale=1.0, causal=1, window=0, keep=0, sinks=None,
            out=None, scratch=None, size=0, err=None):
     return lib.moe_attend(c or cache(), b or batch(), q or heads(), type, n_q, scale, causal, window,
-                          keep, sinks, out or heads(), scratch, size, err, None)
+                          keep, sinks, out or heads(OUT), scratch, size, err, None)
 
 
 def test_caches_and_batches():
@@ -114,6 +115,10 @@ def test_attend():
                dict(q=heads(0x10008)), dict(q=heads(head=60)), dict(out=heads(token=-8)),
                dict(sinks=0x10002)):
         assert attend(**kw) == INVALID, kw
+    assert attend(out=heads()) == INVALID and "out is q" in said()
+    # a grid's dimension holds fewer than 2^24 workgroups of 256 threads
+    for call in (append, attend):
+        assert call(c=cache(n_heads=1 << 24, D=16), b=batch(T=1)) == INVALID and "heads" in said()
     long = batch(n_seq=1, T=1, max_pages=4096, max_len=60000)
     need = lib.moe_attend_scratch_bytes(cache(), long, 4, 0, 0)
     assert need > 0 and need % (4 * 66 * 4) == 0           # whole splits of 4 rows
@@ -125,7 +130,7 @@ def test_attend():
 
 
 def linear(x=FAKE, xs=64, w=FAKE, ws=64, type=BF, M=4, N=32, K=64, bias=None, bt=0, act=0, resid=None,
-           rs=32, out=FAKE, ot=BF, os=32):
+           rs=32, out=OUT, ot=BF, os=32):
     return lib.moe_linear(x, xs, w, ws, type, M, N, K, bias, bt, act, resid, rs, out, ot, os, None)
 
 
@@ -138,7 +143,8 @@ def test_linear():
                dict(w=ODD), dict(xs=-8), dict(ws=60), dict(xs=1 << 39), dict(out=None),
                dict(out=0x10001), dict(ot=F32, out=0x10002), dict(resid=0x10001),
                dict(bias=0x10002, bt=F32), dict(os=31), dict(os=1 << 39), dict(resid=FAKE, rs=-1),
-               dict(resid=FAKE, rs=1 << 39), dict(resid=FAKE, rs=64, os=32)):
+               dict(resid=FAKE, rs=1 << 39), dict(resid=OUT, rs=64, os=32), dict(out=FAKE, w=0x20000),
+               dict(out=FAKE, x=0x20000)):
         assert linear(**kw) == INVALID, kw
         assert said()
     assert linear(M=0) == OK and linear(N=0) == OK
