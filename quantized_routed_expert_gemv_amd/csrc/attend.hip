@@ -123,17 +123,46 @@ __device__ __forceinline__ int window_start(const AttendCall& a, int pos) {
 // Sequences of up to this many rows (new tokens * group) go to the kernel for few rows.
 constexpr int kFewRows = 32;
 
-// The x-th tile of R rows: sequence b's begin at floor(q_start[b] * group / R) + b, which leaves
-// each sequence as many places as it can need. FEW: of the sequences with few rows; else of the
-// others, or of all where no second launch takes them.
+// The tile that stands at place x of the launch, of R rows; false: none.
+// FEW: of the sequences with few rows; else of the others, or of all where no second launch takes them.
+// Sequence b's begin at floor(q_start[b] * group / R) + b, which leaves each sequence as many places
+// as it can need. Beside the launch for many rows, each has as many as few rows need.
 template <int R, bool FEW>
 __device__ __forceinline__ bool find_tile(const AttendCall& a, int64_t x, int head, Tile* t) {
+  constexpr int kFewTiles = kFewRows / R;
   const KvBatchView& b = a.batch;
-  const int seq = wave_find(b.n_seq, x, [&](int i) {
-    return (int64_t)first_row(b, i) * a.group / R + i;
-  });
+  int seq;
+  int64_t row0;
+  if (FEW && a.both) {
+    seq = (int)(x / max(kFewTiles, 1));
+    row0 = (x - (int64_t)seq * kFewTiles) * R;
+  } else if (!FEW && b.n_seq <= kWave) {
+    // The longest context's tiles first, and of a sequence those of its last rows, which see most: a
+    // batch ends with short tiles. A lane counts the tiles in front of its sequence's.
+    const int lane = threadIdx.x & (kWave - 1);
+    int tiles = 0, len = 0, before = 0;
+    if (lane < b.n_seq) {
+      const int64_t rows = (int64_t)(first_row(b, lane + 1) - first_row(b, lane)) * a.group;
+      if (rows > (a.both ? kFewRows : 0)) tiles = (int)((rows + R - 1) / R);
+      len = b.seq_len[lane];
+    }
+    for (int i = 0; i < b.n_seq; ++i) {
+      const int other = __builtin_amdgcn_readlane(len, i), n = __builtin_amdgcn_readlane(tiles, i);
+      before += other > len || (other == len && i < lane) ? n : 0;
+    }
+    const uint64_t here = __ballot(before <= x && x < (int64_t)before + tiles);
+    if (here == 0) return false;
+    seq = __builtin_ctzll(here);
+    row0 = ((int64_t)__builtin_amdgcn_readlane(before, seq) + __builtin_amdgcn_readlane(tiles, seq) - 1 -
+            x) * R;
+  } else {
+    if (!FEW) x = a.tiles - 1 - x;   // later tiles first
+    seq = wave_find(b.n_seq, x, [&](int i) {
+      return (int64_t)first_row(b, i) * a.group / R + i;
+    });
+    row0 = (x - (int64_t)first_row(b, seq) * a.group / R - seq) * R;
+  }
   const int lo = first_row(b, seq), n = first_row(b, seq + 1) - lo;
-  const int64_t row0 = (x - (int64_t)lo * a.group / R - seq) * R;
   const int64_t rows = (int64_t)n * a.group - row0;
   if (n <= 0 || row0 < 0 || rows <= 0) return false;
   if (a.both && ((int64_t)n * a.group <= kFewRows) != FEW) return false;
@@ -572,8 +601,7 @@ __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles
   const int split = (int)(blockIdx.x / (unsigned)a.cache.n_heads);
   const int head = (int)blockIdx.x - split * a.cache.n_heads;
   Tile t;
-  // later tiles, which see more keys, first
-  if (!find_tile<kTileRows, false>(a, a.tiles - 1 - a.block0 - blockIdx.y, head, &t)) return;
+  if (!find_tile<kTileRows, false>(a, a.block0 + blockIdx.y, head, &t)) return;
   const Blocks<kTileKeys> blocks(t);
   const int b0 = (int)((int64_t)blocks.count * split / a.splits);
   const int b1 = (int)((int64_t)blocks.count * (split + 1) / a.splits);
@@ -1046,7 +1074,8 @@ hipError_t launch_depth(AttendCall a, hipStream_t stream) {
             : launch_blocks(a, across, a.tiles, k_attend_tiles<F16, FP8, DV, false>, kTileThreads, stream);
   }
   if (rows && e == hipSuccess) {
-    a.tiles = (int64_t)a.batch.T * a.group / kRowTile + a.batch.n_seq;
+    a.tiles = a.both ? (int64_t)a.batch.n_seq * (kFewRows / kRowTile)
+                     : (int64_t)a.batch.T * a.group / kRowTile + a.batch.n_seq;
     const int64_t across = (int64_t)a.cache.n_heads * a.splits_few;
     e = a.cache.page_size % 8 == 0
             ? launch_blocks(a, across, a.tiles, k_attend_rows<F16, FP8, DV, true>, kRowThreads, stream)
