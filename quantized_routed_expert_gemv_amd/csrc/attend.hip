@@ -120,7 +120,10 @@ __device__ __forceinline__ int window_start(const AttendCall& a, int pos) {
   return a.window ? (int)max((int64_t)pos - a.window + 1, (int64_t)0) : 0;
 }
 
-// Sequences of up to this many rows (new tokens * group) go to the kernel for few rows.
+// Sequences of up to this many rows (new tokens * group) go to the kernel for few rows. Alone behind 16384
+// keys (32 over 4 heads of 128, us): 32 rows 24 against 29 with the one for many, 48 rows 26 against 29, 64
+// rows 32 against 29; 16 sequences of up to 40 rows, where the keys are read again for each 16 of them:
+// 269 for all, 237 for those of up to 32.
 constexpr int kFewRows = 32;
 
 // The tile that stands at place x of the launch, of R rows; false: none.
@@ -319,6 +322,8 @@ constexpr int kRowThreads = 256;
 // dword). The four waves take every fourth block of 32 keys and join in LDS.
 // Key of matrix row m of the block's product u: 8 (m / 4) + 4 u + m % 4, so that a lane's eight
 // scores are those of eight neighbouring keys, 8 (lane / 16) on.
+// Blocks are loaded one ahead, into registers. 64 sequences of up to 16384 keys, 32 heads over 8 of 128:
+// 556 us, 4.9 TB/s; 131072 keys of an 8-bit cache, 32 over 4 heads, in 128 splits: 37 us, 3.6 TB/s.
 // P8: pages hold a multiple of 8 tokens, so such a run of keys is on one page.
 template <bool F16, bool FP8, int DV, bool P8>
 __global__ __launch_bounds__(kRowThreads, DV > 128 ? 1 : 2) void k_attend_rows(AttendCall a) {
@@ -584,6 +589,11 @@ __device__ __forceinline__ u32x2 read_columns(const uint8_t* p) {
 // registers, where they are widened. Values reach the second product through the transposing LDS read,
 // in the order of keys in which the first left the weights: 16 s + {4 h .. + 3, 8 + 4 h .. + 3} for
 // k-step s and lane half h.
+// 8192 tokens behind 8192 others, 32 heads over 8 of 128: 1.81-1.96 ms, 0.84-0.91 PFLOP/s, 2.04 where 16-bit
+// keys and values were staged through registers. The matrix pipes are busy in 40 cycles of 100 and the
+// vector ones in 55: the scores' exponentials, sums and roundings are as long as the products, and run
+// beside them by halves of a block, but not all of the way; without any loads it would take 1.50. LDS
+// reads have no conflicts. 128 rows: at 2 waves a SIMD the sums and operands just fit the registers.
 // U16: pages hold a multiple of 16 tokens, so the 16 rows of a tile that a wave loads are on one.
 template <bool F16, bool FP8, int DV, bool U16>
 __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles(AttendCall a) {
@@ -966,6 +976,8 @@ __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles
 
 // The splits of a row meet: one workgroup a row. Each wave adds every fourth split's sums, several of
 // them in flight at once, and the four meet in LDS; the order depends on the sizes alone.
+// 32 heads of 128, 128 splits: 5.5 us (with a wave a row, one split after the other, the call took 239 us
+// in place of 82).
 constexpr int kMaxSplits = 256;
 template <bool F16>
 __global__ __launch_bounds__(kRowThreads) void k_attend_join(AttendCall a) {
@@ -1111,8 +1123,15 @@ AttendPlan attend_plan(const KvCacheView& c, const KvBatchView& b, int n_q_heads
   if (window) keys = min(keys, (int64_t)window + keep_first + chunk);
   const int64_t few_tiles = (p.both ? b.n_seq : (b.T * group / kRowTile + b.n_seq)) * c.n_heads;
   const int64_t tiles = (b.T * group / kTileRows + 1) * c.n_heads;
-  // enough workgroups for the CUs, with enough keys each: two blocks a wave, or eight tiles
-  p.splits_few = (int)max(min(min(512 / max(few_tiles, (int64_t)1), keys / 256),
+  // Workgroups for the CUs, with enough keys each: two blocks a wave, or eight tiles.
+  // Few rows: two a CU (131072 keys of one sequence, 32 over 4 heads, us: 43 for 256, 36 for 512, 40 for
+  // 1024; 2 sequences 27 for 512, 32 for 1024), and four where sequences of different lengths would leave
+  // some CUs the long ones (8 over 8 heads 112 for 512, 100 for 1024; 32 of them 483, 330, 310 for 2048; 64
+  // of them 635, 591, 592).
+  // Many rows: the sums' way through memory costs more than a last round of tiles that is not full (2048
+  // tokens behind 8192, 516 tiles: 386; in two splits 446).
+  const int64_t few_groups = b.n_seq >= 8 ? 1024 : 512;
+  p.splits_few = (int)max(min(min(few_groups / max(few_tiles, (int64_t)1), keys / 256),
                               (int64_t)kMaxSplits), (int64_t)1);
   p.splits = (int)max(min(min(1024 / max(tiles, (int64_t)1), keys / 512), (int64_t)kMaxSplits),
                       (int64_t)1);

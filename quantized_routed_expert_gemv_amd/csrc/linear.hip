@@ -1,6 +1,6 @@
 // Dense products: out = resid + act(x w^T + bias), x [M][K], w [N][K], 16-bit operands, fp32 sums.
 // Few rows are bound by w's bytes, many by the matrix instructions. One kernel, whose tile, steps under
-// way and groups follow the sizes.
+// way and groups follow the sizes (launch_t).
 #include <type_traits>
 
 #include "common.hpp"
@@ -160,10 +160,16 @@ __device__ __forceinline__ void find_tile(const LinearCall& a, int64_t* m0, int6
   *n0 = (int64_t)col * BN;
 }
 
-// Many rows. A workgroup of KG groups of WM x WN waves makes a tile of BM rows of x and BN of w; each
-// group takes a part of K, BK values a step, and the groups' sums meet in LDS. Steps land in LDS straight
+// A workgroup of KG groups of WM x WN waves makes a tile of BM rows of x and BN of w; each group takes a
+// part of K, BK values a step, and the groups' sums meet in LDS, in their order. Steps land in LDS straight
 // from memory, S - 1 of them under way. A row's 16-byte pieces lie there in the order piece ^ row (BK
-// 64) or piece ^ row / 4 (BK 32), so that eight neighbouring rows of a read fall on different banks.
+// 64) or piece ^ row / 2 (BK 32), so that eight neighbouring rows of a read fall on different banks
+// (piece ^ row / 4 had 23 conflict cycles in 100).
+// w is the matrix instruction's row operand, so that a lane's four sums are neighbours of one row of out.
+// Measured: 4 x 5120 x 2880 8.4 us, 3.5 TB/s of w (a copy here: 4.85); 333 x 2880 x 4096 28 us, bound by
+// the tiles' way from the L2s (290 MB); 16384 x 5120 x 2880 with bias and SiLU 490-530 us, 0.91-0.98
+// PFLOP/s, the matrix pipes busy in 44 cycles of 100, at the clock that power leaves (a library's product
+// alone: 330-380 us).
 template <bool F16, int BM, int BN, int BK, int WM, int WN, int S, int KG>
 __global__ __launch_bounds__(WM * WN * KG * kWave) void k_linear_tile(LinearCall a) {
   constexpr int NW = WM * WN, PR = BK / 8;                 // waves of a group; pieces of a row
@@ -185,7 +191,7 @@ __global__ __launch_bounds__(WM * WN * KG * kWave) void k_linear_tile(LinearCall
   find_tile<BM, BN>(a, &m0, &n0);
 
   // this wave's rows to load, RL at a time: the lane's row and piece
-  auto swizzle = [](int row) { return BK == 64 ? row & 7 : row >> 2 & 3; };
+  auto swizzle = [](int row) { return BK == 64 ? row & 7 : row >> 1 & 3; };
   const int lrow = lane / PR, piece = (lane % PR) ^ swizzle(lrow);
   const int steps = ((a.K + BK - 1) / BK + KG - 1) / KG, k0 = group * steps * BK + 8 * piece;
   const uint16_t* src[LM + LN];

@@ -79,7 +79,7 @@ def test_many_split_sequences(qm, hints):
         at += n
 
 
-@pytest.mark.parametrize("T", [255, 256, 257, 263])
+@pytest.mark.parametrize("T", [255, 257, 2047, 2048, 2049, 2055])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_rows_where_the_launch_changes(qm, T, dtype):
     """Rotation and append of as many tokens as the small launch takes, and of one more; many heads,
