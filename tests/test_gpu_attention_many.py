@@ -79,6 +79,32 @@ def test_many_split_sequences(qm, hints):
         at += n
 
 
+@pytest.mark.parametrize("B", [2, 63, 64, 65, 129])
+@pytest.mark.parametrize("causal", [True, False])
+def test_chunks_of_many_sequences(qm, B, causal):
+    """Chunks of one to three tiles and single tokens, sequences without new tokens among them, many of
+    the same length, on either side of the number of sequences that a wave orders by length."""
+    b = torch.arange(B)
+    new = torch.tensor([40, 1, 0, 70, 33, 1, 9])[b % 7]
+    total = torch.tensor([80, 71, 200, 200, 33])[b % 5].maximum(new)
+    Hkv, G, D = 2, 4, 32
+    cache, batch, (k, v) = _shared(qm, new, total, Hkv, D, 16, 208, False, seed=B)
+    T = int(new.sum())
+    q = torch.randn(T + 3, Hkv * G, D, generator=torch.Generator().manual_seed(1)).to(BF)
+    out = torch.full_like(q, 3.0).to(DEV)
+    qm.attend(q.to(DEV), cache, batch, causal=causal, out=out)
+    assert (out[T:] == 3).all()
+    out, at = out.cpu(), 0
+    for n, t in zip(new.tolist(), total.tolist()):
+        pick = sorted({0, 16, 31, 32, n - 1} & set(range(n)))
+        if pick:
+            rows = torch.tensor([at + i for i in pick])
+            want, tol = ref.attend(q[rows], k[:t], v[:t], torch.tensor([t - n + i for i in pick]),
+                                   D ** -0.5, causal=causal)
+            ref.near(out[rows], want, tol, f"{n} of {t}")
+        at += n
+
+
 @pytest.mark.parametrize("T", [255, 257, 2047, 2048, 2049, 2055])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_rows_where_the_launch_changes(qm, T, dtype):
