@@ -822,10 +822,13 @@ def _new_like(shape, dtype, like, stream):
 
 
 def _like(t, stream):
+    """Rows of heads in the order of t's, the last dimension dense. empty_like alone would put another
+    dimension of stride 1 innermost, where t's rows overlap."""
     if stream is None:
-        return torch.empty_like(t)
+        out = torch.empty_like(t)
+        return out if out.stride()[-1] == 1 else t.new_empty(t.shape)
     with _on(stream):
-        return torch.empty_like(t)
+        return _like(t, None)
 
 
 def _check_flags(err_flags, like):
