@@ -1088,14 +1088,16 @@ moe::AttendPlan plan_of(const moe_kv_cache* c, const moe_kv_batch* b, int32_t n_
   return moe::attend_plan(cache_view(c), batch_view(b), n_q_heads, window, keep_first, b->max_q,
                           b->max_len);
 }
-// Splits whose sums meet in scratch memory.
-int parts_of(const moe::AttendPlan& p) {
-  const int few = p.few || p.both ? p.splits_few : 1, many = p.few ? 1 : p.splits;
-  return few > many ? few : many;
+// Rows of splits whose sums meet in scratch memory, of the sequences with many rows and with few. A row
+// has D sums and two statistics.
+int64_t part_rows(const moe::AttendPlan& p) {
+  return p.few || p.splits <= 1 ? 0 : p.splits * p.rows;
 }
-size_t attend_scratch(const moe_kv_cache* c, const moe_kv_batch* b, int32_t n_q_heads, int parts) {
-  if (parts <= 1) return 0;
-  return (size_t)parts * b->T * n_q_heads * (c->D + 2) * sizeof(float);
+int64_t part_rows_few(const moe::AttendPlan& p) {
+  return !(p.few || p.both) || p.splits_few <= 1 ? 0 : p.splits_few * p.rows_few;
+}
+size_t attend_scratch(const moe_kv_cache* c, const moe::AttendPlan& p) {
+  return (size_t)(part_rows(p) + part_rows_few(p)) * (c->D + 2) * sizeof(float);
 }
 
 moe_status check_16bit(const char* name, int32_t type) {
@@ -1170,8 +1172,7 @@ size_t moe_attend_scratch_bytes(const moe_kv_cache* cache, const moe_kv_batch* b
                                 int32_t n_q_heads, int32_t window, int32_t keep_first) {
   if (check_attend(cache, batch, n_q_heads, window, keep_first) != MOE_OK) return 0;
   if (batch->T == 0 || batch->n_seq == 0) return 0;
-  return attend_scratch(cache, batch, n_q_heads,
-                        parts_of(plan_of(cache, batch, n_q_heads, window, keep_first)));
+  return attend_scratch(cache, plan_of(cache, batch, n_q_heads, window, keep_first));
 }
 
 moe_status moe_attend(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_heads* q,
@@ -1193,15 +1194,16 @@ moe_status moe_attend(const moe_kv_cache* cache, const moe_kv_batch* batch, cons
   if ((uintptr_t)sinks & 3) return fail(MOE_ERR_INVALID_ARG, "sinks misaligned");
   moe::AttendCall a{};
   const moe::AttendPlan plan = plan_of(cache, batch, n_q_heads, window, keep_first);
-  const int parts = parts_of(plan);
   a.splits = plan.splits, a.splits_few = plan.splits_few, a.few = plan.few, a.both = plan.both;
-  if (parts > 1) {
-    const size_t need = attend_scratch(cache, batch, n_q_heads, parts);
+  if (const size_t need = attend_scratch(cache, plan)) {
     CHECK_PTR(scratch);
     if (scratch_bytes < need)
       return fail(MOE_ERR_INVALID_ARG, "scratch holds %zu bytes, %zu needed", scratch_bytes, need);
-    a.part = (float*)scratch;
-    a.stats = a.part + (size_t)parts * batch->T * n_q_heads * cache->D;
+    const int64_t many = part_rows(plan), few = part_rows_few(plan);
+    float* sums = (float*)scratch;
+    float* stats = sums + (many + few) * cache->D;
+    a.parts = {sums, stats, plan.rows};
+    a.parts_few = {sums + many * cache->D, stats + 2 * many, plan.rows_few};
   }
   a.cache = cache_view(cache), a.batch = batch_view(batch);
   a.q = heads_view(q), a.out = heads_view(out);

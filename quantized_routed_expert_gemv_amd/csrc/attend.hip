@@ -228,21 +228,33 @@ __device__ __forceinline__ KeyRow key_row(const AttendCall& a, const Tile& t, in
   return r;
 }
 
+// The row of a split's parts that holds row r of a tile. Beside a launch for many rows, each sequence's few
+// rows have kFewRows places for every KV head, so that the room that they need does not grow with the
+// others' rows.
+template <bool FEW>
+__device__ __forceinline__ int64_t part_row(const AttendCall& a, const Tile& t, int split, int r,
+                                            int64_t token, int head) {
+  if (FEW && a.both)
+    return split * a.parts_few.rows + ((int64_t)t.seq * a.cache.n_heads + t.head) * kFewRows + t.row0 + r;
+  return split * (FEW ? a.parts_few.rows : a.parts.rows) + token * a.n_q_heads + head;
+}
+
 // Where a tile's sums go: out, or a split's part.
-template <bool F16, int N>
-__device__ __forceinline__ void store_row(const AttendCall& a, const Tile& t, int splits, int split,
-                                          int r, int d, float m, float l, const float* o) {
+template <bool F16, bool FEW, int N>
+__device__ __forceinline__ void store_row(const AttendCall& a, const Tile& t, int split, int r, int d,
+                                          float m, float l, const float* o) {
   const int tok = token_of(a, t.row0 + r), g = t.row0 + r - tok * a.group;
   const int64_t token = t.token0 + tok;
   const int head = t.head * a.group + g;
-  if (splits > 1) {
-    const int64_t at = ((int64_t)split * a.batch.T + token) * a.n_q_heads + head;
+  if ((FEW ? a.splits_few : a.splits) > 1) {
+    const AttendParts& parts = FEW ? a.parts_few : a.parts;
+    const int64_t at = part_row<FEW>(a, t, split, r, token, head);
     if (d == 0) {
-      a.stats[2 * at] = m;
-      a.stats[2 * at + 1] = l;
+      parts.stats[2 * at] = m;
+      parts.stats[2 * at + 1] = l;
     }
 #pragma unroll
-    for (int i = 0; i < N; i += 4) *(f32x4*)(a.part + at * a.cache.D + d + i) = f32x4{
+    for (int i = 0; i < N; i += 4) *(f32x4*)(parts.sums + at * a.cache.D + d + i) = f32x4{
         o[i], o[i + 1], o[i + 2], o[i + 3]};
     return;
   }
@@ -271,9 +283,9 @@ __device__ __forceinline__ bool whole_block(const AttendCall& a, const Tile& t, 
 // values. Where not every row sees a block, values that are infinite or NaN go into the product as 0,
 // and a workgroup that met one comes here when its rows are stored: each row takes the odd values of
 // the keys that it sees, times a weight that is not 0, which is adding them.
-template <bool F16, int B>
+template <bool F16, bool FEW, int B>
 __device__ void add_odd_values(const AttendCall& a, const Tile& t, const Blocks<B>& blocks, int b0,
-                               int b1, int splits, int split) {
+                               int b1, int split) {
   __threadfence_block();
   __syncthreads();   // the rows are stored
   const int d = threadIdx.x;
@@ -293,8 +305,8 @@ __device__ void add_odd_values(const AttendCall& a, const Tile& t, const Blocks<
         if (key < window_start(a, pos) && key >= a.keep_first) continue;
         const int64_t token = t.token0 + tok;
         const int head = t.head * a.group + t.row0 + r - tok * a.group;
-        if (splits > 1) {
-          a.part[(((int64_t)split * a.batch.T + token) * a.n_q_heads + head) * a.cache.D + d] += v;
+        if ((FEW ? a.splits_few : a.splits) > 1) {
+          (FEW ? a.parts_few : a.parts).sums[part_row<FEW>(a, t, split, r, token, head) * a.cache.D + d] += v;
         } else {
           uint16_t* p = (uint16_t*)a.out.p + token * a.out.token + head * a.out.head + d;
           *p = (uint16_t)pack2<F16>(value<F16>(*p) + v, 0.f);
@@ -553,9 +565,9 @@ __global__ __launch_bounds__(kRowThreads, DV > 128 ? 1 : 2) void k_attend_rows(A
       for (int w = 0; w < NW; ++w) v[i] = fmaf(f[w], so[w][r][d + i], v[i]);
       v[i] *= vs;
     }
-    store_row<F16, E>(a, t, a.splits_few, split, r, d, sum != sum ? fmaxf(top, 0.f) : top, sum, v);
+    store_row<F16, true, E>(a, t, split, r, d, sum != sum ? fmaxf(top, 0.f) : top, sum, v);
   }
-  if (s_odd) add_odd_values<F16>(a, t, blocks, b0, b1, a.splits_few, split);
+  if (s_odd) add_odd_values<F16, true>(a, t, blocks, b0, b1, split);
 }
 
 constexpr int kTileThreads = 256;
@@ -969,9 +981,9 @@ __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles
       const int at_d = 32 * d + 8 * (i / 4) + 4 * hf;
       if (at_d >= D || !row_ok) continue;
       const float v[4] = {o[d][i] * vs, o[d][i + 1] * vs, o[d][i + 2] * vs, o[d][i + 3] * vs};
-      store_row<F16, 4>(a, t, a.splits, split, r, at_d, top, l, v);
+      store_row<F16, false, 4>(a, t, split, r, at_d, top, l, v);
     }
-  if (s_odd) add_odd_values<F16>(a, t, blocks, b0, b1, a.splits, split);
+  if (s_odd) add_odd_values<F16, false>(a, t, blocks, b0, b1, split);
 }
 
 // The splits of a row meet: one workgroup a row. Each wave adds every fourth split's sums, several of
@@ -985,34 +997,42 @@ __global__ __launch_bounds__(kRowThreads) void k_attend_join(AttendCall a) {
   __shared__ float weight[kMaxSplits];
   __shared__ f32x4 sums[NW][kWave];
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  int splits = a.few ? a.splits_few : a.splits, head;
-  int64_t token = a.block0 + blockIdx.y;
+  bool few = a.few;
+  int head;
+  int64_t token = a.block0 + blockIdx.y, row;
   if (a.both && a.splits == 1) {   // of the sequences with few rows alone: row r of one and a KV head
     const int r = blockIdx.x, kv = (int)(token % a.cache.n_heads), seq = (int)(token / a.cache.n_heads);
+    few = true;
+    row = token * kFewRows + r;
     const int lo = first_row(a.batch, seq), n = first_row(a.batch, seq + 1) - lo;
     if (n <= 0 || (int64_t)n * a.group > kFewRows || r >= n * a.group) return;
     token = lo + r / a.group;
     head = kv * a.group + r % a.group;
-    splits = a.splits_few;
   } else {
     head = blockIdx.x;
     if (token < first_row(a.batch, 0) || token >= first_row(a.batch, a.batch.n_seq)) return;
+    row = token * a.n_q_heads + head;
     if (a.both) {
       const int seq = wave_find(a.batch.n_seq, token, [&](int i) { return first_row(a.batch, i); });
-      const int64_t n = first_row(a.batch, seq + 1) - first_row(a.batch, seq);
-      splits = n * a.group <= kFewRows ? a.splits_few : a.splits;
-      if (splits == 1) return;   // written already
+      const int lo = first_row(a.batch, seq), hi = first_row(a.batch, seq + 1), kv = head / a.group;
+      if (token < lo || token >= hi) return;
+      few = (int64_t)(hi - lo) * a.group <= kFewRows;
+      if (few) {
+        if (a.splits_few == 1) return;   // written already
+        row = ((int64_t)seq * a.cache.n_heads + kv) * kFewRows + (token - lo) * a.group + head - kv * a.group;
+      }
     }
   }
-  const int64_t row = token * a.n_q_heads + head;
-  const int64_t all = (int64_t)a.batch.T * a.n_q_heads;
+  const int splits = few ? a.splits_few : a.splits;
+  const AttendParts parts = few ? a.parts_few : a.parts;
+  const int64_t all = parts.rows;
   typedef float f32x2 __attribute__((__vector_size__(8)));
   f32x2 st[kMaxSplits / kWave];
   float top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kMaxSplits / kWave; ++i) {
     const int s = i * kWave + lane;
-    st[i] = s < splits ? *(const f32x2*)(a.stats + 2 * (s * all + row)) : f32x2{-INFINITY, 0.f};
+    st[i] = s < splits ? *(const f32x2*)(parts.stats + 2 * (s * all + row)) : f32x2{-INFINITY, 0.f};
     top = fmaxf(top, st[i][0]);
   }
 #pragma unroll
@@ -1035,7 +1055,7 @@ __global__ __launch_bounds__(kRowThreads) void k_attend_join(AttendCall a) {
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
   const int d = 4 * lane;
   if (d < a.cache.D) {
-    const float* part = a.part + row * a.cache.D + d;
+    const float* part = parts.sums + row * a.cache.D + d;
 #pragma unroll 8
     for (int s = wave; s < splits; s += NW) {
       const f32x4 v = *(const f32x4*)(part + s * all * a.cache.D);
@@ -1135,6 +1155,8 @@ AttendPlan attend_plan(const KvCacheView& c, const KvBatchView& b, int n_q_heads
                               (int64_t)kMaxSplits), (int64_t)1);
   p.splits = (int)max(min(min(1024 / max(tiles, (int64_t)1), keys / 512), (int64_t)kMaxSplits),
                       (int64_t)1);
+  p.rows = (int64_t)b.T * n_q_heads;
+  p.rows_few = p.both ? (int64_t)b.n_seq * c.n_heads * kFewRows : p.rows;
   return p;
 }
 

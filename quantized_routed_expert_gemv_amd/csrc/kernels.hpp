@@ -210,7 +210,12 @@ struct AppendCall {
 hipError_t launch_append(const AppendCall& a, hipStream_t stream);
 
 // Attention over a paged cache (csrc/attend.hip). The keys of a sequence are shared out among
-// `splits` workgroups, whose sums meet in a second launch through `part`.
+// `splits` workgroups, whose sums meet in a second launch through `parts`.
+struct AttendParts {
+  float* sums;     // [splits][rows][D] sums of weighted values
+  float* stats;    // [splits][rows][2] maximum (of log2 e s) and sum of weights
+  int64_t rows;
+};
 struct AttendCall {
   KvCacheView cache;
   KvBatchView batch;
@@ -224,13 +229,13 @@ struct AttendCall {
   uint32_t* err;
   int splits, splits_few;   // of sequences with many rows (new tokens * group) and with few
   bool few, both;           // sequences with few rows only; with few and with many
-  float* part;              // splits > 1: [splits][T * n_q_heads][D] sums of weighted values,
-  float* stats;             // [splits][T * n_q_heads][2] maximum (of log2 e s) and sum of weights
+  AttendParts parts, parts_few;   // where splits, splits_few > 1
   int64_t tiles, block0;    // set by the launcher: tiles, and first tile or row, of a launch
 };
 struct AttendPlan {
   int splits, splits_few;
   bool few, both;
+  int64_t rows, rows_few;   // of the parts
 };
 AttendPlan attend_plan(const KvCacheView& c, const KvBatchView& b, int n_q_heads, int window,
                        int keep_first, int max_q, int max_len);
