@@ -1137,7 +1137,7 @@ AttendPlan attend_plan(const KvCacheView& c, const KvBatchView& b, int n_q_heads
   // new tokens of the longest chunk; where that is not known, as if all rows were one's
   const int64_t chunk = max_q > 0 ? min(max_q, b.T) : b.T;
   p.few = chunk * group <= kFewRows;
-  p.both = !p.few && b.n_seq > 1;
+  p.both = !p.few && b.n_seq > 1 && group <= kFewRows;   // one token's rows may be more than few
   int64_t keys = (int64_t)b.max_pages * c.page_size;
   if (max_len > 0) keys = min(keys, (int64_t)max_len);
   if (window) keys = min(keys, (int64_t)window + keep_first + chunk);

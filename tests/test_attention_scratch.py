@@ -49,3 +49,11 @@ def test_whole_range():
             (1, 3, 8, 16, 32, 33, 128), (64, 128, 256), (True, False)):
         got = need(new, max(keys, *new), Hkv, G, D, hints=hints)
         assert got <= few_limit(D) + many_limit(D), (new[:4], keys, Hkv, G, D, hints)
+
+
+@pytest.mark.parametrize("G", [33, 64, 128])
+def test_groups_of_more_than_few_rows(G):
+    """Then no sequence has few rows, and beside a chunk whose tiles fill the launch nothing is split."""
+    for new in ([16384, 1], [16384, 3, 700]):
+        assert need(new, 131072, 1, 32, 128) > 0
+        assert need(new, 131072, 1, G, 128) == 0

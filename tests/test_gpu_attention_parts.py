@@ -112,3 +112,12 @@ def test_malformed_batches_stay_inside(qm):
         big = torch.full((T + 8, 16, 64), 3.0, dtype=BF, device=DEV)
         qm.attend(s.q[:T].to(DEV), s.kv, s.batch, out=big[4:4 + T], scratch=memory[:need])
         assert (big[:4] == 3).all() and (big[4 + T:] == 3).all() and (memory[need:] == 0xFF).all()
+
+
+@pytest.mark.parametrize("new,total,Hkv,G,D", [([1, 1, 1], [3000, 1, 700], 1, 33, 64),
+                                               ([40, 1, 0, 2], [900, 20000, 5, 77], 2, 64, 128),
+                                               ([1] * 70 + [9], [31 * i + 1 for i in range(71)], 1, 48, 32)])
+def test_groups_of_more_than_few_rows(qm, new, total, Hkv, G, D):
+    """Tokens and chunks of more query heads a KV head than the kernel for few rows takes."""
+    s = Shared(qm, new, total, Hkv, G, D)
+    s.check(run(qm, s)[0])
