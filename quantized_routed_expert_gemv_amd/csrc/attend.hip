@@ -494,10 +494,10 @@ __global__ __launch_bounds__(kRowThreads, DV > 128 ? 1 : 2) void k_attend_rows(A
 #pragma unroll
     for (int j = 1; j < 8; ++j) top = fmaxf(top, x[j]);
     top *= c;
-    if (__any(top > m + kRaise)) {
+    if (__any(top - m > kRaise)) {   // (not m + kRaise: past 2^27 that is rounded by 8)
       top = fmaxf(top, wave_xor(top, 16));
       top = fmaxf(top, wave_xor(top, 32));
-      const float to = top > m + kRaise ? ceilf(top) : m;   // by a row's own scores alone
+      const float to = top - m > kRaise ? ceilf(top) : m;   // by a row's own scores alone
       const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - to);
       m = to;
       l *= f;
@@ -843,9 +843,9 @@ __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles
   };
   auto raise = [&](float top) {
     top *= c;
-    if (__any(top > m + kRaise)) {
+    if (__any(top - m > kRaise)) {   // (not m + kRaise: past 2^27 that is rounded by 8)
       top = fmaxf(top, wave_xor(top, 32));
-      const float to = top > m + kRaise ? ceilf(top) : m;   // by a row's own scores alone
+      const float to = top - m > kRaise ? ceilf(top) : m;   // by a row's own scores alone
       const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - to);
       m = to;
       l *= f;
