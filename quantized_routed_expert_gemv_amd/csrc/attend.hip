@@ -1,10 +1,15 @@
 // Attention of new tokens over a paged cache: with s_j = scale <q, k_j> over the keys in sight,
 //   out = sum_j e^{s_j} v_j / (sum_j e^{s_j} + e^{sink})
 // in one pass over the keys with a running reference m and sum l: weights are 2^{s'_j - m} with
-// s' = s log2 e. m is a whole number, so that rescaling is exact, and is raised only where a score
-// passes it by 8: weights stay below 2^8 and the sums seldom have to be rescaled.
+// s' = s log2 e. m is a whole number, so that rescaling is exact, and is raised only where a score is
+// more than 8 above the one that m was set by: the sums seldom have to be rescaled.
 // m, l and the weighted sum are fp32; a weight is rounded to the queries' 16-bit type where it
-// meets the values in a matrix instruction, which adds half a step of that type to each term.
+// meets the values in a matrix instruction, which adds half a step of that type to each term. In fp16
+// that holds down to 2^-14; below, it is 2^-25. So m is set 7 below the highest score there, which
+// leaves a row's largest weight between 2^6 and 2^15 (fp16 ends at 65504): weights down to 2^-20 of the
+// largest have all of their bits, and smaller ones lose at most 2^-31 of it each. With m at the highest
+// score, 131068 keys 23 binary orders below four others, 0.5 per cent of a row, came to a fifth less.
+// (Scores past 2^28 in s' are too far apart in fp32 for fp16 weights.)
 //
 // The query heads of a KV head are rows of one tile, so its keys and values are read once. Both
 // products have keys as the matrix rows: S^T = K Q^T leaves a lane the scores of one query, in
@@ -26,7 +31,9 @@ typedef float f32x16 __attribute__((__vector_size__(16 * sizeof(float))));
 typedef short i16x4 __attribute__((__vector_size__(4 * sizeof(short))));
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kRaise = 8.f;   // by how much a score passes the running maximum before it moves
+// How far below the highest score m is set, and how far above m a score has to be to raise it.
+template <bool F16> constexpr float kBelow = F16 ? 7.f : 0.f;
+template <bool F16> constexpr float kRaise = kBelow<F16> + 8.f;
 
 template <bool F16>
 __device__ __forceinline__ f32x4 mma16(u32x4 a, u32x4 b, f32x4 c) {
@@ -494,10 +501,10 @@ __global__ __launch_bounds__(kRowThreads, DV > 128 ? 1 : 2) void k_attend_rows(A
 #pragma unroll
     for (int j = 1; j < 8; ++j) top = fmaxf(top, x[j]);
     top *= c;
-    if (__any(top - m > kRaise)) {   // (not m + kRaise: past 2^27 that is rounded by 8)
+    if (__any(top - m > kRaise<F16>)) {   // (m + kRaise would be rounded, past 2^27 by 8)
       top = fmaxf(top, wave_xor(top, 16));
       top = fmaxf(top, wave_xor(top, 32));
-      const float to = top - m > kRaise ? ceilf(top) : m;   // by a row's own scores alone
+      const float to = top - m > kRaise<F16> ? ceilf(top) - kBelow<F16> : m;   // by a row's own scores alone
       const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - to);
       m = to;
       l *= f;
@@ -843,9 +850,9 @@ __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles
   };
   auto raise = [&](float top) {
     top *= c;
-    if (__any(top - m > kRaise)) {   // (not m + kRaise: past 2^27 that is rounded by 8)
+    if (__any(top - m > kRaise<F16>)) {   // (m + kRaise would be rounded, past 2^27 by 8)
       top = fmaxf(top, wave_xor(top, 32));
-      const float to = top - m > kRaise ? ceilf(top) : m;   // by a row's own scores alone
+      const float to = top - m > kRaise<F16> ? ceilf(top) - kBelow<F16> : m;   // by a row's own scores alone
       const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - to);
       m = to;
       l *= f;

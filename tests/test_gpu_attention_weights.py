@@ -1,4 +1,6 @@
-"""Scores that are far apart."""
+"""Softmax weights far below the row's largest, and scores that are far apart."""
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -6,7 +8,7 @@ import attention_ref as ref  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
-BF, FP = torch.bfloat16, torch.float16
+BF, FP, E4 = torch.bfloat16, torch.float16, torch.float8_e4m3fn
 
 
 @pytest.fixture(scope="module")
@@ -19,6 +21,38 @@ def _batch(qm, T, L, page, max_len):
     i32 = dict(dtype=torch.int32, device=DEV)
     return qm.KvBatch(torch.tensor([0, T], **i32), torch.tensor([L], **i32),
                       torch.arange(-(-L // page), **i32)[None], T, max_len)
+
+
+@pytest.mark.parametrize("T", [1, 40])                # the kernels for few and for many rows
+@pytest.mark.parametrize("top", [13.0, 16.0, 18.0, 20.0])
+@pytest.mark.parametrize("dtype,cache", [(FP, FP), (FP, E4), (BF, BF)])
+@pytest.mark.parametrize("split", [False, True])
+def test_small_weights_of_many_keys(qm, T, top, dtype, cache, split):
+    """Four keys that stand 18 to 28 binary orders above 131068 others, whose weights are together far
+    from nothing: values of 1 (others) beside 0 (the four), and of 1 everywhere."""
+    L, D, page, G, low = 131072, 64, 64, 4, 0.25
+    k = torch.zeros(L // page, page, 1, D, device=DEV)
+    v = torch.ones(L // page, page, 1, D, device=DEV)
+    k[..., 0] = low
+    high = [0, 32, 64, 96]           # each wave that shares out the keys has one of them first
+    for j in high:
+        k[j // page, j % page, 0, 0] = top
+        v[j // page, j % page, 0, :32] = 0.0
+    q = torch.zeros(T, G, D, dtype=dtype, device=DEV)
+    q[..., 0] = 1.0
+    out = qm.attend(q, qm.KvCache(k.to(cache), v.to(cache)), _batch(qm, T, L, page, L if split else 1),
+                    scale=1.0).double().cpu()
+    n = torch.arange(L - T, L, dtype=torch.float64) + 1 - len(high)
+    share = n * math.exp(low) / (n * math.exp(low) + len(high) * math.exp(top))
+    want = torch.ones(T, G, D, dtype=torch.float64)
+    want[..., :32] = share[:, None, None]
+    # a weight is rounded to the type: half a step, and of fp16 half of the smallest step, 2^-25, of
+    # weights whose largest is above 2^6. Scores: two roundings of a number below 2^5, and exp2's; the
+    # sums, L additions of the weights' sum in fp32 each.
+    tol = (ref.half_step(dtype) + 2 * 2.0 ** -17 + 2 * (L + 64) * ref.F32) * want
+    if dtype == FP:
+        tol = tol + L * 2.0 ** -25 / 2 ** 6
+    ref.near(out, want, tol + ref.rounded(want, dtype), "weights")
 
 
 @pytest.mark.parametrize("T", [1, 40])
