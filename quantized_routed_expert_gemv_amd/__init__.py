@@ -837,10 +837,28 @@ def _check_flags(err_flags, like):
         raise ValueError("err_flags: needs 32-bit words on the operands' device")
 
 
-class Rope:
+class _Described:
+    """What a C structure was made from stays as it is: the structure holds the tensors' addresses, and
+    with another tensor in a tensor's place it would be left on memory that was given back. Tensors may
+    be written to, and must not be resized or given other storage."""
+    _fixed = ()
+
+    def __setattr__(self, name, value):
+        if name in self._fixed and name in self.__dict__:
+            raise AttributeError(f"{name} is fixed: make another {type(self).__name__}")
+        self.__dict__[name] = value
+
+    def __delattr__(self, name):
+        if name in self._fixed:
+            raise AttributeError(f"{name} is fixed: make another {type(self).__name__}")
+        super().__delattr__(name)
+
+
+class Rope(_Described):
     """Rotary positions: freq float64 [dim/2] radians a position on the device, the layout of the
     pairs ("half": values i and i + dim/2, "interleaved": 2i and 2i + 1), and a factor on the
-    turned values."""
+    turned values. Its attributes are fixed; freq may be written to."""
+    _fixed = ("freq", "layout", "scale", "index", "struct")
 
     def __init__(self, freq, layout: str = "half", scale: float = 1.0):
         _one_of("layout", layout, _LAYOUTS)
@@ -883,11 +901,12 @@ class Rope:
         return cls(freq.to(device), layout, scale)
 
 
-class KvCache:
+class KvCache(_Described):
     """Paged keys and values: k, v [n_pages, page_size, n_heads, D] bf16, fp16 or float8_e4m3fn, the
     last dimension dense, the others with any strides of whole 16 bytes (a page's tokens or its
     heads first, k and v in one tensor). k_scale, v_scale: float32 [n_heads] or None, of an 8-bit
-    cache: a key is code * k_scale[head]."""
+    cache: a key is code * k_scale[head]. Its attributes are fixed; the tensors may be written to."""
+    _fixed = ("k", "v", "k_scale", "v_scale", "n_pages", "page_size", "n_heads", "D", "index", "struct")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         if k.dim() != 4:
@@ -916,10 +935,14 @@ class KvCache:
         return cls(k, v, k_scale, v_scale)
 
 
-class KvBatch:
+class KvBatch(_Described):
     """The sequences of a step: q_start int32 [n_seq + 1], seq_len int32 [n_seq] (keys of each, its
     new tokens included), page_table int32 [n_seq, max_pages]. max_q and max_len, the largest number
-    of new tokens and of keys of a sequence, choose the launch; results do not depend on them."""
+    of new tokens and of keys of a sequence, choose the launch and how much scratch memory it needs;
+    what a row sees does not depend on them. Its attributes are fixed; a step's lengths and pages are
+    written to the tensors, or come in another KvBatch."""
+    _fixed = ("q_start", "seq_len", "page_table", "n_seq", "max_q", "max_len", "index", "_structs",
+              "_scratch")
 
     def __init__(self, q_start, seq_len, page_table, max_q: int = 0, max_len: int = 0):
         i32, n = (torch.int32,), seq_len.shape[0]

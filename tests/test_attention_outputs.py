@@ -43,3 +43,27 @@ def test_new_outputs_of_ordinary_rows_keep_their_order(passed):
     x = torch.zeros(4, 8, 64, dtype=torch.bfloat16).transpose(0, 1)     # heads first
     out = qm.rope(x, torch.zeros(8, dtype=torch.int32), qm.Rope(torch.zeros(32, dtype=torch.float64)))
     assert out.stride() == x.stride()
+
+
+def test_descriptions_keep_their_tensors(passed):
+    """Calls read the addresses that were taken from the tensors: another tensor in a tensor's place would
+    leave them on memory that was given back."""
+    i32 = dict(dtype=torch.int32)
+    plan = qm.Rope(torch.zeros(32, dtype=torch.float64))
+    kv = qm.KvCache(*(torch.zeros(4, 16, 1, 64, dtype=torch.float8_e4m3fn) for _ in range(2)),
+                    torch.ones(1), torch.ones(1))
+    b = qm.KvBatch(torch.zeros(2, **i32), torch.zeros(1, **i32), torch.zeros(1, 4, **i32), 1, 9)
+    for of, names in ((plan, ("freq", "layout", "scale", "index", "struct")),
+                      (kv, ("k", "v", "k_scale", "v_scale", "n_pages", "page_size", "n_heads", "D",
+                            "index", "struct")),
+                      (b, ("q_start", "seq_len", "page_table", "n_seq", "max_q", "max_len", "index"))):
+        for name in names:
+            before = getattr(of, name)
+            with pytest.raises(AttributeError, match=name):
+                setattr(of, name, before)
+            with pytest.raises(AttributeError, match=name):
+                delattr(of, name)
+            assert getattr(of, name) is before
+        of.note = "a caller's own"
+        of.note = "again"
+        assert of.note == "again"
