@@ -487,7 +487,8 @@ moe_status moe_combine_norm(const float* y, const int32_t* inv_perm, const float
  * output is rounded once, to nearest even. Outputs must not overlap inputs, except as said.
  *
  * Rows of heads: x [T][n_heads][D] are addressed by strides, value (t, h, d) at t * token +
- * h * head + d elements, so q, k and v can be parts of the rows that one product wrote.
+ * h * head + d elements, so q, k and v can be parts of the rows that one product wrote. Rows that are
+ * read may overlap (strides of 0 among them), rows that are written may not.
  */
 typedef struct {
   void* p;
@@ -564,7 +565,8 @@ typedef struct {
  *   positions int32 [T] to turn by, or NULL: each token's place in its sequence
  *   q, q_out rows [T][n_q_heads][D] of type, q_out may be q itself; both NULL: no queries
  * Values are rounded to the cache's type; MOE_T_E4M3 codes are value / scale, saturated at 448 (NaN
- * stays NaN). Two new tokens on one place of the cache are a caller error: either is kept.
+ * stays NaN). Two new tokens on one place of the cache are a caller error: either is kept. The
+ * cache's heads must not overlap.
  * Padding rows of q_out are left as they are.
  */
 moe_status moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_heads* k,

@@ -990,6 +990,23 @@ bool same_heads(const moe_heads* a, const moe_heads* b) {
   return a->p != b->p || (a->token == b->token && a->head == b->head);
 }
 
+// Rows that are written must not meet: those of (t, h) and (t', h') start at least D elements apart.
+moe_status check_apart(const char* name, const moe_heads* h, int64_t T, int64_t n, int64_t D) {
+  bool apart = (T <= 1 || h->token >= D) && (n <= 1 || h->head >= D);
+  if (apart && T > 1 && n > 1 && h->token < (n - 1) * h->head + D && h->head < (T - 1) * h->token + D) {
+    // heads between tokens and tokens between heads: the differences of one kind, next to those of the other
+    const int64_t few = T < n ? T : n, many = T < n ? n : T;
+    const int64_t step = T < n ? h->token : h->head, other = T < n ? h->head : h->token;
+    for (int64_t i = 1; apart && i < few; ++i) {
+      const int64_t at = i * step, j = at / other;
+      apart = (j >= many || at - j * other >= D) && (j + 1 >= many || (j + 1) * other - at >= D);
+    }
+  }
+  if (apart) return MOE_OK;
+  return fail(MOE_ERR_INVALID_ARG, "%s strides (%lld, %lld): rows of %lld values overlap", name,
+              (long long)h->token, (long long)h->head, (long long)D);
+}
+
 int type_bytes(int32_t type) { return type == MOE_T_FP32 ? 4 : type == MOE_T_E4M3 ? 1 : 2; }
 
 moe_status check_rope(const moe_rope_plan* plan, int32_t D) {
@@ -1122,6 +1139,7 @@ moe_status moe_rope(const moe_rope_plan* plan, const moe_heads* x, int32_t type,
   if ((s = check_heads("x", x, type_bytes(type), 1)) != MOE_OK) return s;
   if ((s = check_heads("out", out, type_bytes(type), 1)) != MOE_OK) return s;
   if (!same_heads(x, out)) return fail(MOE_ERR_INVALID_ARG, "out is x with other strides");
+  if ((s = check_apart("out", out, T, n_heads, D)) != MOE_OK) return s;
   if (positions == nullptr || ((uintptr_t)positions & 3))
     return fail(MOE_ERR_INVALID_ARG, "positions is %s", positions ? "misaligned" : "NULL");
   moe::RopeCall a{};
@@ -1155,7 +1173,11 @@ moe_status moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, c
     if ((s = check_heads("q", q, bytes, 1)) != MOE_OK) return s;
     if ((s = check_heads("q_out", q_out, bytes, 1)) != MOE_OK) return s;
     if (!same_heads(q, q_out)) return fail(MOE_ERR_INVALID_ARG, "q_out is q with other strides");
+    if ((s = check_apart("q_out", q_out, batch->T, n_q_heads, cache->D)) != MOE_OK) return s;
   }
+  if (cache->n_heads > 1 && (cache->k_head < cache->D || cache->v_head < cache->D))
+    return fail(MOE_ERR_INVALID_ARG, "cache head strides (%lld, %lld): heads of %d values overlap",
+                (long long)cache->k_head, (long long)cache->v_head, cache->D);
   if ((uintptr_t)positions & 3) return fail(MOE_ERR_INVALID_ARG, "positions misaligned");
   moe::AppendCall a{};
   a.cache = cache_view(cache), a.batch = batch_view(batch);
@@ -1191,6 +1213,7 @@ moe_status moe_attend(const moe_kv_cache* cache, const moe_kv_batch* batch, cons
   if ((s = check_heads("q", q, 16, 8)) != MOE_OK) return s;
   if ((s = check_heads("out", out, 16, 8)) != MOE_OK) return s;
   if (out->p == q->p) return fail(MOE_ERR_INVALID_ARG, "out is q");
+  if ((s = check_apart("out", out, batch->T, n_q_heads, cache->D)) != MOE_OK) return s;
   if ((uintptr_t)sinks & 3) return fail(MOE_ERR_INVALID_ARG, "sinks misaligned");
   moe::AttendCall a{};
   const moe::AttendPlan plan = plan_of(cache, batch, n_q_heads, window, keep_first);
