@@ -871,13 +871,14 @@ class Rope(_Described):
     @classmethod
     def make(cls, dim: int, base: float = 10000.0, layout: str = "half", scaling: str = "none",
              factor: float = 1.0, original: int = 4096, beta_fast: float = 32.0,
-             beta_slow: float = 1.0, device="cuda"):
+             beta_slow: float = 1.0, device="cuda", whole_pairs: bool = True):
         """Frequencies base^(-2i/dim), scaled for contexts `factor` times as long:
         "linear"  all of them over factor;
         "ntk"     base * factor^(dim/(dim-2)): the slowest pair over factor, the fastest kept;
         "yarn"    pairs that turn more than beta_fast times over `original` positions kept, those
                   below beta_slow over factor, a ramp between; turned values times
-                  0.1 ln(factor) + 1."""
+                  0.1 ln(factor) + 1. whole_pairs: the ramp's ends are rounded outwards to
+                  whole pairs; False where a model's configuration has them unrounded."""
         _one_of("scaling", scaling, ("none", "linear", "ntk", "yarn"))
         if dim < 2 or dim % 2:
             raise ValueError(f"dim: {dim}, expected a positive even number")
@@ -894,7 +895,10 @@ class Rope(_Described):
         elif scaling == "yarn":
             def pair(turns):   # the (fractional) pair that turns so often over `original` positions
                 return dim * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
-            lo, hi = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), dim - 1)
+            lo, hi = pair(beta_fast), pair(beta_slow)
+            if whole_pairs:
+                lo, hi = math.floor(lo), math.ceil(hi)
+            lo, hi = max(lo, 0), min(hi, dim - 1)
             slow = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
             freq = freq * (1 - slow) + freq / factor * slow
             scale = 0.1 * math.log(factor) + 1 if factor > 1 else 1.0
