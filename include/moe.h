@@ -533,11 +533,13 @@ moe_status moe_rope(const moe_rope_plan* plan, const moe_heads* x, int32_t type,
  *   page_table int32 [n_seq] rows of max_pages entries, table_stride apart: entry p of row b is the
  *              page of positions p * page_size .. of sequence b
  *   max_q, max_len   the largest number of new tokens and of keys of a sequence, or 0 where they
- *              are not known. They choose the launch; results do not depend on their truth.
- * n_heads * D < 2^28, T * n_heads <= 2^30, n_seq < 2^24, of the cache's and the queries' heads. Values outside these rules in device memory (rows past T, pages
- * outside the cache, positions below zero or past the table) are never followed: what would be
- * there is left out, and bit 0 of *err_flags is set (nullable uint32, atomic OR). Entries of pages
- * that no key in sight lies on are not read.
+ *              are not known. They choose the launch and how much scratch memory it takes; what a
+ *              row sees does not depend on their truth.
+ * n_heads * D < 2^28, T * n_heads <= 2^30, n_seq < 2^24, of the cache's and the queries' heads.
+ * Values outside these rules in device memory (rows past T, pages outside the cache, positions below
+ * zero or past the table) are never followed: what would be there is left out, and bit 0 of
+ * *err_flags is set (nullable uint32, atomic OR). Entries of pages that no key in sight lies on are
+ * not read.
  */
 #define MOE_T_E4M3 4   /* a moe_dtype, of caches only */
 typedef struct {
@@ -588,7 +590,9 @@ moe_status moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, c
  *   Products are of 16-bit operands, summed in fp32; softmax statistics are fp32 and its weights
  *   are rounded to type before they meet the values.
  *   scratch: at least moe_attend_scratch_bytes(...) bytes, 16-byte aligned (NULL where that is 0);
- *   calls that share it must not overlap in time. Padding rows of out are left as they are.
+ *   calls that share it must not overlap in time. It holds the sums of split contexts: at most 170 MB
+ *   (D = 256), and 34 MB beside a chunk that is not split itself. Padding rows of out are left as
+ *   they are.
  */
 size_t moe_attend_scratch_bytes(const moe_kv_cache* cache, const moe_kv_batch* batch,
                                 int32_t n_q_heads, int32_t window, int32_t keep_first);

@@ -167,9 +167,11 @@ __device__ __forceinline__ void find_tile(const LinearCall& a, int64_t* m0, int6
 // (piece ^ row / 4 had 23 conflict cycles in 100).
 // w is the matrix instruction's row operand, so that a lane's four sums are neighbours of one row of out.
 // Measured: 4 x 5120 x 2880 8.4 us, 3.5 TB/s of w (a copy here: 4.85); 333 x 2880 x 4096 28 us, bound by
-// the tiles' way from the L2s (290 MB); 16384 x 5120 x 2880 with bias and SiLU 490-530 us, 0.91-0.98
-// PFLOP/s, the matrix pipes busy in 44 cycles of 100, at the clock that power leaves (a library's product
-// alone: 330-380 us).
+// the tiles' way from the L2s (290 MB); 16384 x 5120 x 2880 with bias and SiLU 507-534 us a call in a row of
+// calls, 0.90-0.95 PFLOP/s, and 574-597 after idle time, the matrix pipes busy in 44 cycles of 100, at the
+// clock that power leaves (without bias and SiLU 495-506; a library's product 329-415). Products with few
+// tiles and a deep K leave most CUs idle, since K is shared inside a workgroup alone: 16 x 512 x 14336 in 32
+// of them 19.7 us, where its bytes are 3.1; 1 x 64 x 14336 11.0 (a library's products 19 and 18).
 template <bool F16, int BM, int BN, int BK, int WM, int WN, int S, int KG>
 __global__ __launch_bounds__(WM * WN * KG * kWave) void k_linear_tile(LinearCall a) {
   constexpr int NW = WM * WN, PR = BK / 8;                 // waves of a group; pieces of a row
@@ -300,7 +302,7 @@ hipError_t launch_tile(const LinearCall& a, hipStream_t stream) {
 // 14.0, 64 x 32 11.6, 64 x 64 14.8). Then 64 x 64 in two groups, two workgroups a CU (333 x 2880 x 4096:
 // 26.7 against 29.4 for three of one group; 512 x 5120 x 2880: 40.7 against 31.8), in one group, 128 x 128
 // (2048 x 5120 x 2880: 83 against 100, and 87 for 128 x 256), and 128 x 256 once they fill one and a half
-// rounds of two a CU (16384 x 5120 x 2880: 485 against 521; 256 x 256, one a CU: 511).
+// rounds of two a CU (16384 x 5120 x 2880: 526 against 581; 256 x 256, one a CU: 554).
 template <bool F16>
 hipError_t launch_t(LinearCall a, hipStream_t stream) {
   const int bytes = a.out_type == kFP32 ? 4 : 2;
