@@ -586,7 +586,8 @@ moe_status moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, c
  *   NULL: no such term). A token that sees no key gets zeros. Keys and values out of sight do not
  *   reach a row, whatever they hold, infinities and NaN among it.
  *   q, out of type (bf16, fp16) [T][n_q_heads][D], 16-byte aligned, strides multiples of 8; a 16-bit
- *   cache is of the same type; n_q_heads a multiple of cache->n_heads; scale is finite
+ *   cache is of the same type; n_q_heads a multiple of cache->n_heads; scale is finite, and scores
+ *   stay below 2^27 in magnitude (past it fp32 scores are too far apart for 16-bit weights)
  *   Products are of 16-bit operands, summed in fp32; softmax statistics are fp32 and its weights
  *   are rounded to type before they meet the values.
  *   scratch: at least moe_attend_scratch_bytes(...) bytes, 16-byte aligned (NULL where that is 0);
