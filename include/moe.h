@@ -588,8 +588,9 @@ moe_status moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, c
  *   q, out of type (bf16, fp16) [T][n_q_heads][D], 16-byte aligned, strides multiples of 8; a 16-bit
  *   cache is of the same type; n_q_heads a multiple of cache->n_heads; scale is finite, and scores
  *   stay below 2^27 in magnitude (past it fp32 scores are too far apart for 16-bit weights)
- *   Products are of 16-bit operands, summed in fp32; softmax statistics are fp32 and its weights
- *   are rounded to type before they meet the values.
+ *   Products are of 16-bit operands, summed in fp32; softmax statistics are fp32. Its weights meet the
+ *   values rounded to type in chunks of more than 32 rows (new tokens * query heads a KV head), and with
+ *   at least 13 bits in others.
  *   scratch: at least moe_attend_scratch_bytes(...) bytes, 16-byte aligned (NULL where that is 0);
  *   calls that share it must not overlap in time. It holds the sums of split contexts: at most 170 MB
  *   (D = 256), and 34 MB beside a chunk that is not split itself. Padding rows of out are left as

@@ -4,7 +4,8 @@
 // s' = s log2 e. m is a whole number, so that rescaling is exact, and is raised only where a score is
 // more than 8 above the one that m was set by: the sums seldom have to be rescaled.
 // m, l and the weighted sum are fp32; a weight is rounded to the queries' 16-bit type where it
-// meets the values in a matrix instruction, which adds half a step of that type to each term. In fp16
+// meets the values in a matrix instruction, which adds half a step of that type to each term (many rows),
+// or to two numbers of it, which leaves the outputs' own rounding (few rows, see kMost). In fp16
 // that holds down to 2^-14; below, it is 2^-25. So m is set 7 below the highest score there, which
 // leaves a row's largest weight between 2^6 and 2^15 (fp16 ends at 65504): weights down to 2^-20 of the
 // largest have all of their bits, and smaller ones lose at most 2^-31 of it each. With m at the highest
@@ -63,6 +64,10 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {   // RNE, NaN kept
 template <bool F16>
 __device__ __forceinline__ float value(uint32_t bits) {
   return F16 ? fp16_to_f32(uint16_t(bits)) : bf16_lo(bits);
+}
+template <bool F16>
+__device__ __forceinline__ float value_hi(uint32_t bits) {
+  return F16 ? fp16_to_f32(uint16_t(bits >> 16)) : bf16_hi(bits);
 }
 // Two E4M3 codes (the low or the high half of v) as two values of the 16-bit type, exactly.
 template <bool F16, bool HI>
@@ -335,12 +340,20 @@ __device__ __forceinline__ bool take_odd(uint32_t& v, bool take = true) {
 constexpr int kRowTile = 16;
 constexpr int kRowThreads = 256;
 
+// The part of a weight that is rounded to its first operand; its second one is what is left. Together
+// they have 14 bits (bf16) or 13 (fp16), where one has 8 or 11. Both are positive, so that an infinite value
+// stays one: a rest of 0 or less, as beside the rounded weight itself, would make it NaN. (Of fp16 a quarter
+// is left, a number down to weights of 2^-22.)
+template <bool F16> constexpr float kMost = F16 ? 0.75f : 0.984375f;
+
 // Few rows a sequence: the cache's bytes bound it. A tile is 16 rows, the columns of 16x16x32
 // instructions, so nothing goes through LDS but the end: a lane's 16-byte loads of K rows are
 // operands as they are, and its loads of eight V rows become V^T operands by 16-bit picks (one a
 // dword). The four waves take every fourth block of 32 keys and join in LDS.
 // Key of matrix row m of the block's product u: 8 (m / 4) + 4 u + m % 4, so that a lane's eight
 // scores are those of eight neighbouring keys, 8 (lane / 16) on.
+// The matrix pipes have time, so a weight is two operands: rounded to one, it added as much error to the
+// outputs as their own rounding (0.0024 in place of 0.0017 of bf16). It costs 2 us of the 557 below, 1 of 43.
 // Blocks are loaded one ahead, into registers. 64 sequences of up to 16384 keys, 32 heads over 8 of 128:
 // 556 us, 4.9 TB/s; 131072 keys of an 8-bit cache, 32 over 4 heads, in 128 splits: 37 us, 3.6 TB/s.
 // P8: pages hold a multiple of 8 tokens, so such a run of keys is on one page.
@@ -519,8 +532,12 @@ __global__ __launch_bounds__(kRowThreads, DV > 128 ? 1 : 2) void k_attend_rows(A
       x[j] = __builtin_amdgcn_exp2f(fmaf(x[j], c, -base));
       l += x[j];
     }
-    const u32x4 pf = {pack2<F16>(x[0], x[1]), pack2<F16>(x[2], x[3]), pack2<F16>(x[4], x[5]),
-                      pack2<F16>(x[6], x[7])};
+    u32x4 most, rest;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      most[j] = pack2<F16>(kMost<F16> * x[2 * j], kMost<F16> * x[2 * j + 1]);
+      rest[j] = pack2<F16>(x[2 * j] - value<F16>(most[j]), x[2 * j + 1] - value_hi<F16>(most[j]));
+    }
 #pragma unroll
     for (int h = 0; h < NH; ++h)
 #pragma unroll
@@ -530,7 +547,8 @@ __global__ __launch_bounds__(kRowThreads, DV > 128 ? 1 : 2) void k_attend_rows(A
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           vt[j] = __builtin_amdgcn_perm(vf[2 * j + 1][h][i / 2], vf[2 * j][h][i / 2], sel);
-        o[h][i] = mma16<F16>(vt, pf, o[h][i]);
+        o[h][i] = mma16<F16>(vt, most, o[h][i]);
+        o[h][i] = mma16<F16>(vt, rest, o[h][i]);
       }
     raw = next;
   }
