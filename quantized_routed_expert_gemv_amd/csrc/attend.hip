@@ -4,8 +4,9 @@
 // s' = s log2 e. m is a whole number, so that rescaling is exact, and is raised only where a score is
 // more than 8 above the one that m was set by: the sums seldom have to be rescaled.
 // m, l and the weighted sum are fp32; a weight is rounded to the queries' 16-bit type where it
-// meets the values in a matrix instruction, which adds half a step of that type to each term (many rows),
-// or to two numbers of it, which leaves the outputs' own rounding (few rows, see kMost). In fp16
+// meets the values in a matrix instruction, or to two numbers of it (few rows, see kMost). With one number
+// (many rows) l adds up the rounded weights, so that half a step of each counts by how far its value is
+// from the row's output: with few keys, or one that has most of the weight, by little. In fp16
 // that holds down to 2^-14; below, it is 2^-25. So m is set 7 below the highest score there, which
 // leaves a row's largest weight between 2^6 and 2^15 (fp16 ends at 65504): weights down to 2^-20 of the
 // largest have all of their bits, and smaller ones lose at most 2^-31 of it each. With m at the highest
@@ -68,6 +69,14 @@ __device__ __forceinline__ float value(uint32_t bits) {
 template <bool F16>
 __device__ __forceinline__ float value_hi(uint32_t bits) {
   return F16 ? fp16_to_f32(uint16_t(bits >> 16)) : bf16_hi(bits);
+}
+// sum and both 16-bit values. The instruction's own sum of three is not always to nearest in fp16.
+template <bool F16>
+__device__ __forceinline__ float add2(uint32_t w, float sum) {
+  if constexpr (F16)
+    return sum + __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, w), f16x2{1, 1}, 0.f, false);
+  else
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), bf16x2{1, 1}, sum, false);
 }
 // Two E4M3 codes (the low or the high half of v) as two values of the 16-bit type, exactly.
 template <bool F16, bool HI>
@@ -353,9 +362,9 @@ template <bool F16> constexpr float kMost = F16 ? 0.75f : 0.984375f;
 // Key of matrix row m of the block's product u: 8 (m / 4) + 4 u + m % 4, so that a lane's eight
 // scores are those of eight neighbouring keys, 8 (lane / 16) on.
 // The matrix pipes have time, so a weight is two operands: rounded to one, it added as much error to the
-// outputs as their own rounding (0.0024 in place of 0.0017 of bf16). It costs 2 us of the 557 below, 1 of 43.
+// outputs as their own rounding (0.0024 in place of 0.0017 of bf16). It added 2 us to the 555 below, and 1 to 42.
 // Blocks are loaded one ahead, into registers. 64 sequences of up to 16384 keys, 32 heads over 8 of 128:
-// 556 us, 4.9 TB/s; 131072 keys of an 8-bit cache, 32 over 4 heads, in 128 splits: 37 us, 3.6 TB/s.
+// 557 us, 4.9 TB/s; 131072 keys of an 8-bit cache, 32 over 4 heads, in 128 splits: 37 us, 3.6 TB/s.
 // P8: pages hold a multiple of 8 tokens, so such a run of keys is on one page.
 template <bool F16, bool FP8, int DV, bool P8>
 __global__ __launch_bounds__(kRowThreads, DV > 128 ? 1 : 2) void k_attend_rows(AttendCall a) {
@@ -942,9 +951,10 @@ __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles
     auto weights = [&](int i) {   // of two keys
       x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], c, base));
       x[i + 1] = __builtin_amdgcn_exp2f(fmaf(x[i + 1], c, base));
-      l += x[i] + x[i + 1];
+      const uint32_t w = pack2<F16>(x[i], x[i + 1]);
+      l = add2<F16>(w, l);
       asm("" : "+v"(l));   // here, not behind the loop's end: the weights would stay in registers
-      p[i / 8][i % 8 / 2] = pack2<F16>(x[i], x[i + 1]);
+      p[i / 8][i % 8 / 2] = w;
     };
     // Each matrix instruction has weights to run beside it. (Behind the last block the scores are of
     // what lies in LDS, and are dropped.)

@@ -56,3 +56,30 @@ def test_infinite_values_stay_infinite(qm, bad, dtype, new, total, G):
     assert torch.equal(out[:T][..., others], clean[:T][..., others])
     hit = out[:T][pos >= 5][..., 9].float()
     assert (hit.isnan() if bad != bad else hit == bad).all()
+
+
+@pytest.mark.parametrize("new,total", [([40], [40]), ([90, 50], [90, 52]), ([300, 33], [300, 400]), ([64], [3000])])
+@pytest.mark.parametrize("Hkv,G,D", [(2, 1, 64), (1, 4, 128), (1, 2, 256)])
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (FP, FP), (BF, E4)])
+def test_many_rows_weights_sum_to_one(qm, new, total, Hkv, G, D, dtype, cache):
+    """Rounded weights over the sum of the same rounded weights: what a weight's rounding moves is its
+    value's distance from the row's output, which is little where few keys have most of the weight."""
+    s = Shared(qm, new, total, Hkv, G, D, dtype, cache)
+    out, _ = run(qm, s)
+    h = ref.half_step(dtype)
+    for b, (n, t) in enumerate(zip(new, total)):
+        if n * G <= 32:
+            continue
+        pick = sorted({*range(12), 31, 32, n // 2, n - 1})
+        rows = torch.tensor([s.start[b] + i for i in pick])
+        pos = torch.tensor([t - n + i for i in pick])
+        k, v = s.rows[0][:t], s.rows[1][:t]
+        want, tol = ref.attend(s.q[rows], k, v, pos, D ** -0.5, dtype=F32)    # all but the weights' rounding
+        for j in range(Hkv * G):
+            x = s.q[rows, j].double() @ k[:, j // G].T * D ** -0.5
+            w = x.masked_fill(torch.arange(t) > pos[:, None], -torch.inf).softmax(-1)
+            away = (v[None, :, j // G] - want[:, None, j]).abs()
+            tol[:, j] += h * (1 + 2 * h) * (w[..., None] * away).sum(1)
+            if dtype == FP:      # and 2^-25 where the row's largest weight is above 2^6
+                tol[:, j] += t * 2.0 ** -31 * away.amax(1)
+        ref.near(out[rows], want, tol + ref.rounded(want.abs() + tol, dtype), f"sequence {b}: {n} of {t}")
