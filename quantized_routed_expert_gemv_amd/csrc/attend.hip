@@ -6,9 +6,9 @@
 // m, l and the weighted sum are fp32; a weight is rounded to the queries' 16-bit type where it
 // meets the values in a matrix instruction, or to two numbers of it (few rows, see kMost). With one number
 // (many rows) l adds up the rounded weights, so that half a step of each counts by how far its value is
-// from the row's output: with few keys, or one that has most of the weight, by little. In fp16
-// that holds down to 2^-14; below, it is 2^-25. So m is set 7 below the highest score there, which
-// leaves a row's largest weight between 2^6 and 2^15 (fp16 ends at 65504): weights down to 2^-20 of the
+// from the row's output: with few keys, or one that has most of the weight, by little. In fp16 half a
+// step is 2^-25 for weights below 2^-14. So m is set 7 below the highest score there, which leaves
+// a row's largest weight between 2^6 and 2^15 (fp16 ends at 65504): weights down to 2^-20 of the
 // largest have all of their bits, and smaller ones lose at most 2^-31 of it each. With m at the highest
 // score, 131068 keys 23 binary orders below four others, 0.5 per cent of a row, came to a fifth less.
 // (Scores past 2^28 in s' are too far apart in fp32 for fp16 weights.)
@@ -364,7 +364,7 @@ template <bool F16> constexpr float kMost = F16 ? 0.75f : 0.984375f;
 // The matrix pipes have time, so a weight is two operands: rounded to one, it added as much error to the
 // outputs as their own rounding (0.0024 in place of 0.0017 of bf16). It added 2 us to the 555 below, and 1 to 42.
 // Blocks are loaded one ahead, into registers. 64 sequences of up to 16384 keys, 32 heads over 8 of 128:
-// 557 us, 4.9 TB/s; 131072 keys of an 8-bit cache, 32 over 4 heads, in 128 splits: 37 us, 3.6 TB/s.
+// 557-562 us, 4.9 TB/s; 131072 keys of an 8-bit cache, 32 over 4 heads, in 128 splits: 38 us, 3.5 TB/s.
 // P8: pages hold a multiple of 8 tokens, so such a run of keys is on one page.
 template <bool F16, bool FP8, int DV, bool P8>
 __global__ __launch_bounds__(kRowThreads, DV > 128 ? 1 : 2) void k_attend_rows(AttendCall a) {
@@ -635,13 +635,13 @@ __device__ __forceinline__ u32x2 read_columns(const uint8_t* p) {
 // registers, where they are widened. Values reach the second product through the transposing LDS read,
 // in the order of keys in which the first left the weights: 16 s + {4 h .. + 3, 8 + 4 h .. + 3} for
 // k-step s and lane half h.
-// 8192 tokens behind 8192 others, 32 heads over 8 of 128: 1.81-1.96 ms, 0.84-0.91 PFLOP/s, 2.04 where 16-bit
+// 8192 tokens behind 8192 others, 32 heads over 8 of 128: 1.78-1.85 ms, 0.89-0.92 PFLOP/s, 2.04 where 16-bit
 // keys and values were staged through registers. The matrix pipes are busy in 40 cycles of 100 and the
-// vector ones in 55: the scores' exponentials, sums and roundings are as long as the products, and run
+// vector ones in 52: the scores' exponentials, sums and roundings are as long as the products, and run
 // beside them by halves of a block, but not all of the way; without any loads it would take 1.50. LDS
 // reads have no conflicts. 128 rows: at 2 waves a SIMD the sums and operands just fit the registers.
-// The same over an 8-bit cache 1.82-1.85; as many operations in 64 heads over 8 of 64 2.16-2.21 on either
-// cache, in 16 over 8 of 256 2.51 (8-bit 2.43), one workgroup a CU; in a window of 4096 keys 0.67-0.70.
+// The same over an 8-bit cache 1.79-1.80; as many operations in 64 heads over 8 of 64 2.09-2.15 on either
+// cache, in 16 over 8 of 256 2.50 (8-bit 2.44), one workgroup a CU; in a window of 4096 keys 0.65-0.69.
 // U16: pages hold a multiple of 16 tokens, so the 16 rows of a tile that a wave loads are on one.
 template <bool F16, bool FP8, int DV, bool U16>
 __global__ __launch_bounds__(kTileThreads, DV > 128 ? 1 : 2) void k_attend_tiles(AttendCall a) {

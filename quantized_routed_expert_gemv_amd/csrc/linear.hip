@@ -167,9 +167,9 @@ __device__ __forceinline__ void find_tile(const LinearCall& a, int64_t* m0, int6
 // (piece ^ row / 4 had 23 conflict cycles in 100).
 // w is the matrix instruction's row operand, so that a lane's four sums are neighbours of one row of out.
 // Measured: 4 x 5120 x 2880 8.4 us, 3.5 TB/s of w (a copy here: 4.85); 333 x 2880 x 4096 28 us, bound by
-// the tiles' way from the L2s (290 MB); 16384 x 5120 x 2880 with bias and SiLU 507-534 us a call in a row of
-// calls, 0.90-0.95 PFLOP/s, and 574-597 after idle time, the matrix pipes busy in 44 cycles of 100, at the
-// clock that power leaves (without bias and SiLU 495-506; a library's product 329-415). Products with few
+// the tiles' way from the L2s (290 MB); 16384 x 5120 x 2880 with bias and SiLU 508-534 us a call in a row of
+// calls, 0.90-0.95 PFLOP/s, and 574-638 after idle time, the matrix pipes busy in 44 cycles of 100, at the
+// clock that power leaves (without bias and SiLU 483-506; a library's product 325-415). Products with few
 // tiles and a deep K leave most CUs idle, since K is shared inside a workgroup alone: 16 x 512 x 14336 in 32
 // of them 19.7 us, where its bytes are 3.1; 1 x 64 x 14336 11.0 (a library's products 19 and 18).
 template <bool F16, int BM, int BN, int BK, int WM, int WN, int S, int KG>
